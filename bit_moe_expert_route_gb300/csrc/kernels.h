@@ -239,4 +239,34 @@ cudaError_t decode_launch(const DecodeParams& p, cudaStream_t s);
 int decode_args_status(const uint16_t* x, const moe_weights_t* w, const moe_shape_t* shape,
                        const uint16_t* out);
 
+// ---------------------------------------------------------------- residual norm, 8-bit output
+struct NormParams {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;  // or null
+  const uint16_t* weight;
+  int T, d;
+  float eps;
+  int e4m3;
+  uint16_t* residual_out;    // or null
+  uint8_t* q;
+  float* scale;
+  uint16_t* values;          // or null
+};
+cudaError_t norm_launch(const NormParams& p, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- token log probabilities
+constexpr int kLogprobMaxK = 32;
+struct LogprobParams {
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;        // or null
+  int N, V, k, f32;
+  float* logprob;            // or null
+  float* entropy;            // or null
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
+
 }  // namespace moe

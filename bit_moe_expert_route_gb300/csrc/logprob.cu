@@ -1,0 +1,428 @@
+// Log probabilities of given tokens, entropy and top alternatives from logits,
+// each logit read once.
+//
+//   lse = ref + log S, S = sum exp(z - ref);  logprob = z_id - lse
+//   H = log S - U / S, U = sum exp(z - ref) (z - ref)
+//
+// Every thread keeps its own reference `ref`, sum S and weighted sum U over the
+// 16-byte vectors it reads. ref starts at the largest logit of the thread's
+// first vectors and moves only when a logit passes it by more than kLazy: sums
+// of fp32 need no nearer reference, and the rescale is almost never taken. The
+// row's sums are moved to the largest logit at the end, where neither
+// difference cancels. z - ref is taken in natural units before the
+// multiplication by log2 e, so that large logits lose nothing to the
+// constant's rounding. Two elements go through the packed fp32 add, multiply
+// and fused multiply-add at a time; what is left is one ex2 an element, the
+// nearest limit after HBM for bf16 logits.
+//
+// Top k (k <= 32): a warp holds its best 32 in order, one a lane, and inserts
+// what reaches the block's threshold (a lower bound of the row's k-th best: the
+// best k-th place of any warp). The threshold starts from the thread maxima of
+// the block's first pass, so that only a few elements a pass ever reach the
+// insertion. Ties go to the lower index: entries are 64-bit keys (value in
+// order, then the index reversed), and an element equal to the threshold is
+// still inserted.
+//
+// Many rows: one block a row. Few rows: a cluster of 2, 4 or 8 blocks shares a
+// row and the first block merges their states from distributed shared memory,
+// so one launch suffices at every size.
+#include <cmath>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kLpWarps = 8;
+constexpr int kLpThreads = 32 * kLpWarps;
+constexpr float kLazy = 20.f;  // e^20: fp32 sums hold it easily
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;
+
+MOE_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+MOE_DEVINL float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The order of a logit among the top alternatives: larger value, larger rank;
+// NaN below every number (rank 1), 0 = no element.
+MOE_DEVINL uint32_t rank_of(float z) { return z != z ? 1u : order_key(z); }
+MOE_DEVINL uint64_t key_of(float z, int index) {
+  return ((uint64_t)rank_of(z) << 32) | (uint32_t)(~index);
+}
+
+// A thread's sums over its elements.
+struct Sums {
+  float ref, S, U;  // S = sum exp(z - ref), U = sum exp(z - ref) (z - ref)
+  float top;        // the largest logit (NaN if one is)
+};
+
+// Moves (S, U) to another reference (both finite).
+MOE_DEVINL void rebase(Sums& s, float ref) {
+  const float d = s.ref - ref, f = exp2f(d * kLog2e);
+  // e (z - ref') = f e_old ((z - ref) + d); f = 0 far below leaves nothing
+  s.U = f > 0.f ? f * fmaf(s.S, d, s.U) : 0.f * s.U;
+  s.S *= f;
+  s.ref = ref;
+}
+MOE_DEVINL void merge(Sums& a, Sums b) {
+  const float ref = fmaxf(a.ref, b.ref);
+  rebase(a, ref);
+  rebase(b, ref);
+  a.S += b.S;
+  a.U += b.U;
+  a.top = max_nan(a.top, b.top);
+}
+
+// The best 32 of two descending lists of 32 (one entry a lane), descending.
+MOE_DEVINL uint64_t merge32(uint64_t a, uint64_t b, int lane) {
+  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  a = a > r ? a : r;  // the upper half of a bitonic sequence
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, a, off);
+    const bool upper = (lane & off) == 0;
+    a = (a > o) == upper ? a : o;
+  }
+  return a;
+}
+// 32 values (one a lane) into descending order.
+MOE_DEVINL uint32_t sort32(uint32_t a, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int off = size / 2; off > 0; off >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, a, off);
+      const bool keep_max = ((lane & off) == 0) == ((lane & size) == 0);
+      a = keep_max ? max(a, o) : min(a, o);
+    }
+  return a;
+}
+
+// Elements of a 16-byte vector.
+template <bool F32>
+constexpr int kVecElems = F32 ? 4 : 8;
+template <bool F32>
+MOE_DEVINL uint4 none_vec() {  // -infinity throughout
+  constexpr uint32_t w = F32 ? 0xFF800000u : 0xFF80FF80u;
+  return make_uint4(w, w, w, w);
+}
+
+// The vector of the row's elements first .. first + E - 1 (16-byte aligned);
+// those outside [0, V) as -infinity. A vector inside is one 16-byte load.
+template <bool F32>
+MOE_DEVINL uint4 load_vec(const void* row, int64_t first, int V) {
+  constexpr int E = kVecElems<F32>;
+  const float* f = static_cast<const float*>(row);
+  const uint16_t* h = static_cast<const uint16_t*>(row);
+  if (first >= 0 && first + E <= V) {
+    if constexpr (F32) return __ldg(reinterpret_cast<const uint4*>(f + first));
+    return __ldg(reinterpret_cast<const uint4*>(h + first));
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      w[i] = first + i >= 0 && first + i < V ? __float_as_uint(f[first + i]) : 0xFF800000u;
+    } else {
+      const int64_t a = first + 2 * i, b = a + 1;
+      const uint32_t x = a >= 0 && a < V ? h[a] : 0xFF80u;
+      const uint32_t y = b >= 0 && b < V ? h[b] : 0xFF80u;
+      w[i] = x | (y << 16);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool F32>
+MOE_DEVINL void widen(const uint4& v, float (&z)[kVecElems<F32>]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      z[i] = __uint_as_float(u[i]);
+    } else {
+      z[2 * i] = __uint_as_float(u[i] << 16);
+      z[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// The vector's largest element (NaN if one is).
+template <bool F32>
+MOE_DEVINL float largest(const uint4& v) {
+  if constexpr (F32) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3]));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+    return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+}
+
+template <bool F32>
+MOE_DEVINL void add_vec(Sums& s, const uint4& v, float vmax) {
+  constexpr int E = kVecElems<F32>;
+  s.top = max_nan(s.top, vmax);
+  if (vmax > s.ref + kLazy) rebase(s, vmax);  // (+infinity ends as NaN, as it should)
+  float z[E];
+  widen<F32>(v, z);
+  const float2 nref = make_float2(-s.ref, -s.ref), c = make_float2(kLog2e, kLog2e);
+  float2 S = make_float2(0.f, 0.f), U = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    const float2 d = __fadd2_rn(make_float2(z[i], z[i + 1]), nref);
+    const float2 x = __fmul2_rn(d, c);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    S = __fadd2_rn(S, e);
+    // -infinity: its weight is 0, and so is 0 * (a finite distance)
+    U = __ffma2_rn(e, make_float2(max_nan(d.x, kLowest), max_nan(d.y, kLowest)), U);
+  }
+  s.S += S.x + S.y;
+  s.U += U.x + U.y;
+}
+
+struct LpShared {
+  uint64_t list[kLpWarps][32];
+  Sums sums[kLpWarps];
+  uint64_t row_list[32];  // the block's results, read by the cluster's first block
+  Sums row_sums;
+  uint32_t threshold;     // rank that an element has to reach
+};
+
+// The best 32 of n lists in shared memory (n a power of two <= 8) into
+// list[0]: halving, one warp a pair. The whole block calls it.
+MOE_DEVINL void merge_lists(uint64_t (*list)[32], int n, int warp, int lane) {
+  for (; n > 1; n >>= 1) {
+    __syncthreads();
+    if (warp < n / 2) list[warp][lane] = merge32(list[warp][lane], list[warp + n / 2][lane], lane);
+  }
+  __syncthreads();
+}
+
+MOE_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `q` in the shared memory of the cluster's block r.
+MOE_DEVINL uint32_t remote_addr(const void* q, uint32_t r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
+  return a;
+}
+MOE_DEVINL float remote_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <bool F32, bool TOP>
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams p) {
+  constexpr int E = kVecElems<F32>;
+  constexpr int kUnroll = 4;  // vectors a thread loads before it uses them
+  __shared__ LpShared sh;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int64_t row = blockIdx.x / ranks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const char* base = static_cast<const char*>(p.logits) + row * p.ld * (F32 ? 4 : 2);
+  const int lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) / (F32 ? 4 : 2));
+  // the row's vectors, the first one starting `lead` elements before it, in
+  // contiguous parts for the cluster's blocks
+  const int nvec = (lead + p.V + E - 1) / E, part = (nvec + (int)ranks - 1) / (int)ranks;
+  const int v0 = (int)rank * part, v1 = min(nvec, v0 + part);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  Sums s;
+  s.ref = kLowest;
+  s.S = 0.f;
+  s.U = 0.f;
+  s.top = -INFINITY;
+  uint64_t mine = 0;  // this lane's entry of the warp's list, 0 = none
+  uint32_t bar = 0;   // the rank that an element has to reach
+  for (int v = v0; v < v1; v += kUnroll * kLpThreads) {
+    uint4 w[kUnroll];
+    float vm[kUnroll], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int vi = v + i * kLpThreads + tid;
+      w[i] = vi < v1 ? load_vec<F32>(base, (int64_t)vi * E - lead, p.V) : none_vec<F32>();
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      vm[i] = largest<F32>(w[i]);
+      m = max_nan(m, vm[i]);
+    }
+    if (v == v0) s.ref = fminf(fmaxf(m, kLowest), -kLowest);  // (NaN: the lowest)
+    if (TOP && v == v0) {
+      // the k-th largest of the threads' maxima bounds the k-th largest element
+      // from below. A thread without elements counts as nothing (rank 0).
+      const uint32_t sorted = sort32(v + tid < v1 ? rank_of(m) : 0u, lane);
+      sh.list[warp][lane] = ((uint64_t)sorted << 32);
+      merge_lists(sh.list, kLpWarps, warp, lane);
+      bar = (uint32_t)(sh.list[0][p.k - 1] >> 32);
+      if (tid == 0) sh.threshold = bar;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) add_vec<F32>(s, w[i], vm[i]);
+    if (TOP) {
+      bar = max(bar, *reinterpret_cast<volatile uint32_t*>(&sh.threshold));
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int vi = v + i * kLpThreads + tid;
+        const int64_t first = (int64_t)vi * E - lead;
+        // (a NaN hides the vector's other elements: look at each)
+        const bool any = vi < v1 && (vm[i] != vm[i] || rank_of(vm[i]) >= bar);
+        if (__any_sync(0xffffffffu, any)) {
+          float z[E];
+          widen<F32>(w[i], z);
+          bool moved = false;
+#pragma unroll 1
+          for (int e = 0; e < E; ++e) {
+            float ze = z[0];
+#pragma unroll
+            for (int q = 1; q < E; ++q) ze = q == e ? z[q] : ze;
+            const int64_t index = first + e;
+            const uint64_t key = any && index >= 0 && index < p.V ? key_of(ze, (int)index) : 0ull;
+            unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
+            while (todo) {
+              const int src = __ffs(todo) - 1;
+              todo &= todo - 1;
+              const uint64_t c = __shfl_sync(0xffffffffu, key, src);
+              const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
+              const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+              if (lane == at) mine = c;
+              else if (lane > at) mine = up;
+              moved = true;
+            }
+          }
+          if (moved) {  // the warp's k-th best may raise the block's threshold
+            const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
+            if (kth > bar) {
+              bar = kth;
+              if (lane == 0) atomicMax(&sh.threshold, kth);
+            }
+          }
+        }
+      }
+    }
+  }
+  // the block's sums and list
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    Sums o;
+    o.ref = __shfl_xor_sync(0xffffffffu, s.ref, off);
+    o.S = __shfl_xor_sync(0xffffffffu, s.S, off);
+    o.U = __shfl_xor_sync(0xffffffffu, s.U, off);
+    o.top = __shfl_xor_sync(0xffffffffu, s.top, off);
+    merge(s, o);
+  }
+  if (lane == 0) sh.sums[warp] = s;
+  if (TOP) {
+    sh.list[warp][lane] = mine;  // (its last readers passed a barrier in the first pass)
+    merge_lists(sh.list, kLpWarps, warp, lane);
+  } else {
+    __syncthreads();
+  }
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int w = 1; w < kLpWarps; ++w) merge(s, sh.sums[w]);
+      sh.row_sums = s;
+    }
+    if (TOP) sh.row_list[lane] = sh.list[0][lane];
+  }
+  if (ranks > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      if (TOP) {
+        if (warp < (int)ranks) {
+          uint64_t e;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(e) : "r"(remote_addr(&sh.row_list[lane], warp)) : "memory");
+          sh.list[warp][lane] = e;
+        }
+        merge_lists(sh.list, (int)ranks, warp, lane);
+      }
+      if (tid == 0) {
+        for (uint32_t r = 1; r < ranks; ++r) {
+          const uint32_t a = remote_addr(&sh.row_sums, r);
+          Sums o;
+          o.ref = remote_f32(a);
+          o.S = remote_f32(a + 4);
+          o.U = remote_f32(a + 8);
+          o.top = remote_f32(a + 12);
+          merge(s, o);
+        }
+        sh.row_sums = s;
+      }
+    }
+    cluster_sync();  // the other blocks' shared memory stays until the first has read it
+    if (rank != 0) return;
+  }
+  __syncthreads();
+  s = sh.row_sums;
+  const bool none = s.top == -INFINITY;   // nothing but -infinity
+  const bool bad = !(s.top <= -kLowest);  // +infinity or NaN
+  const float nan = __int_as_float(0x7fc00000);
+  if (!bad && !none) rebase(s, s.top);
+  const float logS = logf(s.S);
+  auto log_p = [&](float z) {
+    if (bad) return nan;
+    return none || z == -INFINITY ? -INFINITY : (z - s.ref) - logS;
+  };
+  if (tid == 32 && p.logprob) {
+    const int id = p.ids[row];
+    float lp = nan;
+    if (id >= 0 && id < p.V)
+      lp = log_p(F32 ? reinterpret_cast<const float*>(base)[id]
+                     : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(base)[id]));
+    p.logprob[row] = lp;
+  }
+  if (tid == 64 && p.entropy) p.entropy[row] = bad ? nan : none ? 0.f : fmaxf(logS - s.U / s.S, 0.f);
+  if (TOP && tid < p.k) {
+    const uint64_t e = sh.list[0][tid];
+    p.top_ids[row * p.k + tid] = (int)~(uint32_t)e;
+    p.top_logprobs[row * p.k + tid] = log_p(key_value((uint32_t)(e >> 32)));
+  }
+}
+
+template <bool F32, bool TOP>
+cudaError_t logprob_launch_t(const LogprobParams& p, int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.N * cluster));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<F32, TOP>, p);
+}
+
+}  // namespace
+
+cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s) {
+  // More blocks a row while the grid leaves multiprocessors short of 4 blocks
+  // and each block keeps two passes over its threads' vectors.
+  const int64_t pass = (int64_t)kLpThreads * (p.f32 ? 4 : 8);
+  int cluster = 1;
+  while (cluster < 8 && (int64_t)p.N * cluster * 2 <= (int64_t)sms * 4 && p.V >= cluster * 2 * 2 * pass) cluster *= 2;
+  if (p.f32) return p.k ? logprob_launch_t<true, true>(p, cluster, s) : logprob_launch_t<true, false>(p, cluster, s);
+  return p.k ? logprob_launch_t<false, true>(p, cluster, s) : logprob_launch_t<false, false>(p, cluster, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,256 @@
+// Residual addition, root-mean-square norm and an 8-bit output with a scale
+// per token, in one pass over the row.
+//
+//   r = bf16(x + residual), u = r w, a = max |u|, rms = sqrt(mean r^2 + eps)
+//   q = round(u top / a), scale = a / (top rms)      (top = 127 or 448)
+//
+// The root mean square cancels out of q: only the scale needs it, so one
+// reduction carries both the largest |u| and the sum of squares, and the
+// codes follow from values that stayed in registers. u is a product of two
+// bf16 values, exact in fp32; u * (top / a) in fp32 is within 3 * 2^-24 of the
+// exact quotient (relative), so only a quotient that near a rounding border
+// is decided in 64 bits: every code is the correctly rounded one.
+//
+// Bound by HBM: 7 bytes an element (x, residual in; residual, q out), 9 with
+// the bf16 values. A row belongs to G threads of NV 16-byte vectors each. Rows
+// in plenty: NV = 8, so a row of 2048 is one warp's, its 16 loads in flight at
+// once and its reduction five shuffles with no barrier. Few rows: NV = 1, the
+// row spread over as many warps as it has vectors, for latency.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kNormThreads = 256;  // a block's threads where a row needs no more
+
+MOE_DEVINL void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+MOE_DEVINL uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The larger of two values, NaN where one is.
+MOE_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Adding this and taking it away rounds |t| < 2^22 to a whole number (its low
+// byte, in two's complement, ends in the sum's), or |t| < 2^13 to a multiple
+// of 2^-9 (the spacing of e4m3 below 2^-6).
+constexpr float kRoundInt = 12582912.f;  // 1.5 * 2^23
+constexpr float kRoundSub = 24576.f;     // 1.5 * 2^14
+
+// Whether the fp32 quotient t may round to another code than the exact one
+// (its error is below 3 * 2^-24 |t|). True for a NaN.
+MOE_DEVINL bool near_border_int8(float t) {
+  const float n = (t + kRoundInt) - kRoundInt;
+  return !(fabsf(t - n) < 0.5f - 4e-5f);  // |t| <= 127: error below 2.4e-5
+}
+MOE_DEVINL bool near_border_e4m3(float t) {
+  // normal values keep 3 of the 23 fraction bits: near when the other 20 are
+  // within 8 of half
+  const bool cut = ((__float_as_uint(t) & 0xFFFFFu) - 0x7FFF8u) <= 16u;
+  const float n = (t + kRoundSub) - kRoundSub;
+  const bool sub = !(fabsf(t - n) < 0x1p-10f - 1e-8f);
+  return fabsf(t) >= 0x1p-6f ? cut : sub;
+}
+
+template <int NV, bool E4M3>
+__global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_kernel(const NormParams p, int G) {
+  // G threads a row (whole warps), blockDim / G rows a block
+  const int sub = threadIdx.x / G, lt = threadIdx.x % G;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / G) + sub;
+  const int nvec = p.d / 8;
+  const bool live = row < p.T;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  uint4 r[NV];
+  const int64_t base = row * p.d;
+  float ss = 0.f, a = 0.f;
+  if (live) {
+    const uint16_t* xr = p.x + row * p.ldx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lt + i * G;
+      r[i] = v < nvec ? *reinterpret_cast<const uint4*>(xr + 8 * v) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.residual) {
+      uint4 s[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = lt + i * G;
+        s[i] = v < nvec ? *reinterpret_cast<const uint4*>(p.residual + base + 8 * v) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[8], g[8];
+        unpack8(r[i], f);
+        unpack8(s[i], g);
+        r[i] = make_uint4(pack2(f[0] + g[0], f[1] + g[1]), pack2(f[2] + g[2], f[3] + g[3]),
+                          pack2(f[4] + g[4], f[5] + g[5]), pack2(f[6] + g[6], f[7] + g[7]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lt + i * G;
+      if (v < nvec) {
+        if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + base + 8 * v) = r[i];
+        float f[8], w[8], s8 = 0.f;
+        unpack8(r[i], f);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + v), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s8 = fmaf(f[e], f[e], s8);
+          a = max_nan(a, fabsf(f[e] * w[e]));
+        }
+        ss += s8;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
+  }
+  if (G > 32) {  // the same for the whole block: every thread takes the barrier
+    __shared__ float sh[2][32];
+    const int warp = threadIdx.x / 32, first = sub * (G / 32);
+    if ((threadIdx.x & 31) == 0) {
+      sh[0][warp] = ss;
+      sh[1][warp] = a;
+    }
+    __syncthreads();
+    ss = 0.f;
+    a = 0.f;
+    for (int w = first; w < first + G / 32; ++w) {
+      ss += sh[0][w];
+      a = max_nan(a, sh[1][w]);
+    }
+  }
+  if (!live) return;
+  constexpr float kTop = E4M3 ? 448.f : 127.f, kMax = 3.402823466e38f;
+  const float nan = __int_as_float(0x7fc00000);
+  // a NaN or an infinity in the row shows in the sum of squares, one in the
+  // products (a weight's, or an overflow) in a
+  const bool fine = ss <= kMax && a <= kMax;
+  const float scale = fine ? a / kTop / sqrtf(ss / (float)p.d + p.eps) : nan;
+  if (lt == 0) p.scale[row] = scale;
+  // Rows without a usable fp32 quotient (zeros, values that are not finite,
+  // and rows so small that top / a overflows) take the 64-bit path, as NaNs.
+  const bool some = fine && a > 0.f;
+  const float inv = some && a > 1e-36f ? kTop / a : nan;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lt + i * G;
+    if (v < nvec) {
+      float f[8], w[8], t[8];
+      unpack8(r[i], f);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + v), w);
+      bool near = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        t[e] = (f[e] * w[e]) * inv;
+        near |= E4M3 ? near_border_e4m3(t[e]) : near_border_int8(t[e]);
+      }
+      if (near) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!(E4M3 ? near_border_e4m3(t[e]) : near_border_int8(t[e]))) continue;
+          const double z = some ? (double)kTop * (double)(f[e] * w[e]) / (double)a : 0.0;
+          if constexpr (E4M3) {
+            // cut to fp32 with the last bit set when anything was cut off
+            // (round to odd), which the second rounding cannot mistake
+            const float c = __double2float_rz(z);
+            t[e] = (double)c == z ? c : __uint_as_float(__float_as_uint(c) | 1u);
+          } else {
+            t[e] = (float)rint(z);
+          }
+        }
+      }
+      uint32_t word[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (E4M3) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h], t[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h + 2], t[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+          word[h] = lo | (hi << 16);
+        } else {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = t[4 * h + e] + kRoundInt;
+            b[e] = __float_as_uint(s);
+            t[4 * h + e] = s - kRoundInt;
+          }
+          word[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        }
+      }
+      *reinterpret_cast<uint2*>(p.q + base + 8 * v) = make_uint2(word[0], word[1]);
+      if (p.values) {
+        if constexpr (E4M3) {  // what the codes stand for
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word[h >> 1] >> (16 * (h & 1))), __NV_E4M3);
+            const float2 v2 = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+            t[2 * h] = v2.x;
+            t[2 * h + 1] = v2.y;
+          }
+        }
+        *reinterpret_cast<uint4*>(p.values + base + 8 * v) =
+            make_uint4(pack2(t[0] * scale, t[1] * scale), pack2(t[2] * scale, t[3] * scale),
+                       pack2(t[4] * scale, t[5] * scale), pack2(t[6] * scale, t[7] * scale));
+      }
+    }
+  }
+}
+
+template <int NV, bool E4M3>
+cudaError_t norm_launch_nv(const NormParams& p, int G, cudaStream_t s) {
+  const int rows = G < kNormThreads ? kNormThreads / G : 1, threads = rows * G;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.T + (int64_t)rows - 1) / rows));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_kernel<NV, E4M3>, p, G);
+}
+
+}  // namespace
+
+cudaError_t norm_launch(const NormParams& p, int sms, cudaStream_t s) {
+  const int nvec = p.d / 8;
+  // The most vectors a thread that still leaves 16 warps a multiprocessor;
+  // rows of more than 1024 threads' worth always take more.
+  int nv = 8;
+  while (nv > 1 && (int64_t)p.T * ((nvec + nv - 1) / nv) < (int64_t)sms * 512 && nvec <= 1024 * (nv / 2)) nv /= 2;
+  const int G = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+  if (p.e4m3) {
+    if (nv == 8) return norm_launch_nv<8, true>(p, G, s);
+    if (nv == 4) return norm_launch_nv<4, true>(p, G, s);
+    if (nv == 2) return norm_launch_nv<2, true>(p, G, s);
+    return norm_launch_nv<1, true>(p, G, s);
+  }
+  if (nv == 8) return norm_launch_nv<8, false>(p, G, s);
+  if (nv == 4) return norm_launch_nv<4, false>(p, G, s);
+  if (nv == 2) return norm_launch_nv<2, false>(p, G, s);
+  return norm_launch_nv<1, false>(p, G, s);
+}
+
+}  // namespace moe

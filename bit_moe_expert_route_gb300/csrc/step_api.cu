@@ -1,0 +1,105 @@
+// C ABI of the operators around the layer (include/step.h): argument checks
+// and launches.
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "step.h"
+
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  (void)cudaGetLastError();  // clear a non-sticky launch error
+  return MOE_ERR_CUDA;
+}
+
+// The current device's SM count, or a status < 0. The attributes are looked
+// up once a device (they are most of a small call's time on the host).
+int device_sms() {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];  // 0 = not looked up
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDev) {
+    const int v = known[dev].load(std::memory_order_relaxed);
+    if (v) return v;
+  }
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const int r = major == 10 && minor == 3 ? sms : MOE_ERR_ARCH;
+  if (dev >= 0 && dev < kMaxDev) known[dev].store(r, std::memory_order_relaxed);
+  return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
+                       const uint16_t* weight, int T, int d, float eps, int format,
+                       uint16_t* residual_out, void* q, float* scale, uint16_t* values,
+                       void* stream) {
+  if (T < 0 || d < 8 || d > 16384 || d % 8 != 0 || ldx < d || ldx % 8 != 0) return MOE_ERR_SHAPE;
+  if (format != MOE_Q8_INT8 && format != MOE_Q8_E4M3) return MOE_ERR_SHAPE;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || !q || !scale) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(residual_out, 16) || !aligned(q, 8) || !aligned(scale, 4) || !aligned(values, 16))
+    return MOE_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
+  moe::NormParams p;
+  p.x = x;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.weight = weight;
+  p.T = T;
+  p.d = d;
+  p.eps = eps;
+  p.e4m3 = format == MOE_Q8_E4M3;
+  p.residual_out = residual_out;
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.values = values;
+  return cuda_status(moe::norm_launch(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_token_logprobs(const void* logits, int type, int64_t ld, const int32_t* ids, int N, int V,
+                       int k, float* logprob, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, void* stream) {
+  if (type != MOE_BF16 && type != MOE_F32) return MOE_ERR_SHAPE;
+  if (N < 0 || V < 1 || V >= 1 << 30 || ld < V || k < 0 || k > moe::kLogprobMaxK || k > V)
+    return MOE_ERR_SHAPE;
+  if (N == 0) return MOE_OK;
+  if (!logits || (ids == nullptr) != (logprob == nullptr)) return MOE_ERR_NULL;
+  if (k > 0 && (!top_ids || !top_logprobs)) return MOE_ERR_NULL;
+  if (!aligned(logits, type == MOE_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(logprob, 4) ||
+      !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+    return MOE_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
+  moe::LogprobParams p;
+  p.logits = logits;
+  p.ld = ld;
+  p.ids = ids;
+  p.N = N;
+  p.V = V;
+  p.k = k;
+  p.f32 = type == MOE_F32;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.top_ids = top_ids;
+  p.top_logprobs = top_logprobs;
+  return cuda_status(moe::logprob_launch(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

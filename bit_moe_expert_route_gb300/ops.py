@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe_gb300 (include/moe.h).
+"""ctypes binding of libmoe_gb300 (include/*.h).
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels. PyTorch provides device memory and the current stream. The library
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -112,6 +113,9 @@ def lib():
         L.moe_decode_batch_workspace_bytes.argtypes = [vp]
         L.moe_decode_batch_views.argtypes = [vp, sz, vp, vp]
         L.moe_decode_batch_w4.argtypes = [vp, vp, vp, vp, vp, sz, vp]
+        L.moe_add_rmsnorm_q8.argtypes = [vp, i64, vp, vp, i32, i32, ctypes.c_float, i32, vp, vp, vp,
+                                         vp, vp]
+        L.moe_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int32)]
         L.moe_debug_decode_fault.argtypes = [ctypes.c_uint64, i32]
         _lib = L
@@ -303,6 +307,96 @@ def decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: f
                                     _p(ws), ws.numel(), _stream(stream))
     _check("moe_decode_attention", rc)
     return out
+
+
+Q8_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
+_FLOAT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+class NormQ8(NamedTuple):
+    """add_rmsnorm_q8's outputs: codes [T, d], scale fp32 [T], the new residual bf16 [T, d]
+    and (where asked for) q * scale as bf16 [T, d]."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    residual: torch.Tensor
+    values: torch.Tensor | None
+
+
+def _want(fn, name, t, dtype, shape, rows=False):
+    """Refuses a tensor of another type, shape, device or layout than the call reads
+    (rows: only each row has to be contiguous)."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)}, {dtype} {tuple(shape)} is wanted")
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is not on the GPU")
+    if not t.is_contiguous() and not (rows and t.stride(-1) == 1):
+        raise ValueError(f"{fn}: {name} is not contiguous")
+
+
+def _ld(t):
+    """Elements from one row of a 2-D tensor to the next (its width where there is one row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                   eps: float = 1e-6, fmt: str = "int8", values: bool = False,
+                   residual_out: torch.Tensor | None = None, stream=None) -> NormQ8:
+    """moe_add_rmsnorm_q8 (include/step.h): x bf16 [T, d] (rows may be strided), weight bf16
+    [d], residual bf16 [T, d] or None. fmt "int8" or "e4m3". residual_out may be `residual`
+    (updated in place); without a residual and a residual_out, `.residual` is x itself."""
+    T, d = x.shape
+    fn, bf, dev = "add_rmsnorm_q8", torch.bfloat16, x.device
+    if fmt not in Q8_FORMATS:
+        raise ValueError(f"{fn}: fmt is {fmt!r}, 'int8' or 'e4m3' is wanted")
+    code, dtype = Q8_FORMATS[fmt]
+    _want(fn, "x", x, bf, (T, d), rows=True)
+    _want(fn, "weight", weight, bf, (d,))
+    if residual is not None:
+        _want(fn, "residual", residual, bf, (T, d))
+        if residual_out is None:
+            residual_out = torch.empty(T, d, dtype=bf, device=dev)
+    if residual_out is not None:
+        _want(fn, "residual_out", residual_out, bf, (T, d))
+    q = torch.empty(T, d, dtype=dtype, device=dev)
+    scale = torch.empty(T, dtype=torch.float32, device=dev)
+    vals = torch.empty(T, d, dtype=bf, device=dev) if values else None
+    _check("moe_add_rmsnorm_q8", lib().moe_add_rmsnorm_q8(
+        _p(x), _ld(x), _p(residual), _p(weight), T, d, eps, code, _p(residual_out), _p(q),
+        _p(scale), _p(vals), _stream(stream)))
+    return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
+
+
+class TokenLogprobs(NamedTuple):
+    """token_logprobs' outputs: fp32 [N], fp32 [N], int32 [N, k], fp32 [N, k]."""
+    logprob: torch.Tensor | None
+    entropy: torch.Tensor
+    top_ids: torch.Tensor
+    top_logprobs: torch.Tensor
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k: int = 0,
+                   stream=None) -> TokenLogprobs:
+    """moe_token_logprobs (include/step.h): logits bf16 or fp32 [N, V] (rows may be strided),
+    ids int32 [N] or None. Returns the ids' log probabilities, each row's entropy (nats) and
+    its top_k (at most 32) alternatives, largest first, ties to the lower id."""
+    N, V = logits.shape
+    fn, dev = "token_logprobs", logits.device
+    if logits.dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{fn}: logits are {logits.dtype}, bfloat16 or float32 is wanted")
+    if not 0 <= top_k <= min(32, V):
+        raise ValueError(f"{fn}: top_k is {top_k}, 0 .. min(32, {V}) is wanted")
+    _want(fn, "logits", logits, logits.dtype, (N, V), rows=True)
+    if ids is not None:
+        _want(fn, "ids", ids, torch.int32, (N,))
+    logprob = None if ids is None else torch.empty(N, dtype=torch.float32, device=dev)
+    entropy = torch.empty(N, dtype=torch.float32, device=dev)
+    top_ids = torch.empty(N, top_k, dtype=torch.int32, device=dev)
+    top_lp = torch.empty(N, top_k, dtype=torch.float32, device=dev)
+    _check("moe_token_logprobs", lib().moe_token_logprobs(
+        _p(logits), _FLOAT_TYPES[logits.dtype], _ld(logits), _p(ids), N, V, top_k, _p(logprob),
+        _p(entropy), _p(top_ids) if top_k else None, _p(top_lp) if top_k else None,
+        _stream(stream)))
+    return TokenLogprobs(logprob, entropy, top_ids, top_lp)
 
 
 FWD_DETERMINISTIC = 1
