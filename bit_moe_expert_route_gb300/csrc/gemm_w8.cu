@@ -1,0 +1,493 @@
+// Matrix product of 8-bit integers with a scale per token and per output
+// channel:  out[t][n] = a_scale[t] w_scale[n] sum_k a[t][k] w[n][k].
+//
+// The part's 8-bit integer tensor rate is far below its f16 rate, and every
+// int8 is exact in f16 (as is every product, in fp32): so the codes are turned
+// into f16 on chip, in three integer operations and two subtractions for four
+// codes (the byte with its sign bit flipped under 0x64 is the f16 of 1152 + b),
+// and multiplied by the f16 tensor cores with fp32 sums, which are exact while
+// they stay below 2^24 in magnitude (always for K <= 1024). Weights stay 8-bit
+// in memory.
+//
+// Two kernels, by the number of tokens:
+//
+// Up to 32 tokens: bound by the weights' bytes. A block owns 16 M weight rows
+// and splits K over its 8 warps; a lane loads 16 consecutive codes of two
+// rows per m16n8k16 product quadruple (the order of k is free as long as both
+// operands agree, so the fragments need no shuffling), and the warps' sums
+// meet in shared memory.
+//
+// More tokens: tcgen05. The MMA's M side is 128 weight rows, its N side up to
+// 256 tokens. TMA brings the packed weight codes, converter warps write them as
+// f16 straight into tensor memory (the A operand), so shared memory carries
+// only the tokens' operand to the MMA. The tokens' codes (far fewer) are
+// widened to f16 in the workspace by a first kernel; its launch lets the
+// product's start early, and the product's weight stream does not wait for it.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// Four int8 codes as two f16 pairs, in order.
+MOE_DEVINL uint2 widen4(uint32_t w) {
+  const uint32_t u = w ^ 0x80808080u;  // 128 + code
+  uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 bias = __floats2half2_rn(1152.f, 1152.f);  // 1024 + 128
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+MOE_DEVINL void store_out(void* out, int f32, int64_t at, float v) {
+  if (f32)
+    static_cast<float*>(out)[at] = v;
+  else
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------- few tokens
+constexpr int kFewWarps = 8;
+
+MOE_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 M weight rows x 8 NT tokens a block.
+template <int M, int NT>
+__global__ void __launch_bounds__(32 * kFewWarps) gemm_w8_few_kernel(const GemmW8Params p) {
+  constexpr int U = M == 1 ? 4 : M == 2 ? 2 : 1;  // 64-code steps in flight (8 weight loads a lane)
+  constexpr int kPitch = 16 * M + 4;
+  __shared__ float red[kFewWarps][8 * NT][kPitch];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * M);
+  const int steps = (p.K + 63) / 64, per = (steps + kFewWarps - 1) / kFewWarps;
+  const int s0 = warp * per, s1 = min(steps, s0 + per);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  float acc[M][NT][4];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+  const int8_t* wrow[M][2];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // rows past the end repeat the last one and are not stored
+      wrow[m][h] = p.w + min(n0 + 16 * m + 8 * h + g, (int64_t)p.N - 1) * p.K;
+  const int8_t* arow[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) arow[j] = p.a + (int64_t)min(8 * j + g, p.T - 1) * p.lda;
+#pragma unroll 1
+  for (int s = s0; s < s1; s += U) {
+    uint4 wv[U][M][2], av[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + u) * 64 + 16 * t;
+      const bool in = s + u < s1 && k < p.K;  // K is a multiple of 16
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          wv[u][m][h] = in ? __ldcs(reinterpret_cast<const uint4*>(wrow[m][h] + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        av[u][j] = in ? __ldg(reinterpret_cast<const uint4*>(arow[j] + k)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        auto word = [&](const uint4& v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
+        uint2 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = widen4(word(av[u][j]));
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const uint2 lo = widen4(word(wv[u][m][0])), hi = widen4(word(wv[u][m][1]));
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_16816(acc[m][j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+        }
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][8 * j + 2 * t + (i & 1)][16 * m + g + 8 * (i >> 1)] = acc[m][j][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * M * 8 * NT; i += 32 * kFewWarps) {
+    const int r = i % (16 * M), c = i / (16 * M);
+    const int64_t n = n0 + r;
+    if (c < p.T && n < p.N) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) v += red[w][c][r];
+      store_out(p.out, p.f32, (int64_t)c * p.ldo + n, v * __ldg(p.a_scale + c) * __ldg(p.w_scale + n));
+    }
+  }
+}
+
+template <int M, int NT>
+cudaError_t few_launch(const GemmW8Params& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.N + 16 * M - 1) / (16 * M)));
+  cfg.blockDim = dim3(32 * kFewWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_w8_few_kernel<M, NT>, p);
+}
+template <int M>
+cudaError_t few_launch_nt(const GemmW8Params& p, cudaStream_t s) {
+  switch ((p.T + 7) / 8) {
+    case 1: return few_launch<M, 1>(p, s);
+    case 2: return few_launch<M, 2>(p, s);
+    case 3: return few_launch<M == 4 ? 2 : M, 3>(p, s);
+    default: return few_launch<M == 4 ? 2 : M, 4>(p, s);
+  }
+}
+
+// ---------------------------------------------------------------- many tokens
+// The tokens' codes as f16 rows of K, contiguous; clears the status word.
+__global__ void __launch_bounds__(256) widen_kernel(const GemmW8Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int vecs = p.K / 16;
+  if (i == 0) *p.status = 0;
+  if (i >= (int64_t)p.T * vecs) return;
+  const int64_t row = i / vecs;
+  const int k = (int)(i - row * vecs) * 16;
+  const uint4 v = *reinterpret_cast<const uint4*>(p.a + row * p.lda + k);
+  const uint2 a = widen4(v.x), b = widen4(v.y), c = widen4(v.z), d = widen4(v.w);
+  uint4* dst = reinterpret_cast<uint4*>(p.a16 + row * p.K + k);
+  dst[0] = make_uint4(a.x, a.y, b.x, b.y);
+  dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+constexpr int kTileN = 128;               // weight rows a tile (the MMA's M)
+constexpr int kKB = 128;                  // codes a k-block
+constexpr int kQStage = kTileN * kKB;     // packed codes of a stage: 16 KB
+constexpr int kManyThreads = 640;         // 20 warps, by role below
+constexpr int kConvWarps = 8, kEpiWarps = 8;
+
+template <int BN>
+struct CfgW8 {
+  static constexpr int kSQ = BN == 256 ? 2 : 4;  // packed-code stages
+  static constexpr int kSA = 4;                  // f16 weight stages in tensor memory, 64 columns each
+  static constexpr int kSB = BN == 256 ? 3 : BN == 128 ? 4 : 6;  // token stages
+  static constexpr int kSD = kSA > kSB ? kSA : kSB;
+  static constexpr int kBBytes = BN * kKB * 2;
+  static constexpr int kAcc = BN == 256 ? 1 : 2;  // accumulators: 256 columns in all at 256 and 128
+  static constexpr int kACol = kAcc * BN;
+  static constexpr int kOffB = 0;
+  static constexpr int kOffQ = kSB * kBBytes;
+  static constexpr int kOffBar = kOffQ + kSQ * kQStage;
+  static constexpr int kBars = 2 * kSQ + kSA + kSB + kSD + 2 + 2 + 1;
+  static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
+  static_assert(kACol + kSA * (kKB / 2) <= 512, "tensor memory exceeded");
+  static_assert(kSmem <= 232448, "shared memory exceeded");
+};
+
+struct W8Args {
+  CUtensorMap tm_w;  // packed weights [N][K] bytes, box 128 x 128
+  CUtensorMap tm_a;  // f16 tokens [T][K], box 64 x BN
+  GemmW8Params g;
+};
+
+// Roles: warp 0 streams the packed weights, warp 1 issues the MMAs, warp 2
+// streams the tokens' operand, warps 4-11 convert, warps 12-19 write out.
+// Tiles of 128 weight rows by BN tokens, weights fastest, one CTA an SM.
+template <int BN>
+__global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_constant__ W8Args args) {
+  using C = CfgW8<BN>;
+  const GemmW8Params& g = args.g;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_empty = q_full + C::kSQ;
+  uint64_t* a_full = q_empty + C::kSQ;
+  uint64_t* b_full = a_full + C::kSA;
+  // done[i % kSD]: the MMAs of k-block i have read their operands. One commit
+  // frees both: the converters of k-block i wait for k-block i - kSA, the
+  // token stream for i - kSB; the MMA cannot get kSD k-blocks past either.
+  uint64_t* done = b_full + C::kSB;
+  uint64_t* acc_full = done + C::kSD;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int MT = (g.N + kTileN - 1) / kTileN, TT = (g.T + BN - 1) / BN, KB = (g.K + kKB - 1) / kKB;
+  const int64_t units = (int64_t)MT * TT;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], kConvWarps);
+    }
+    for (int i = 0; i < C::kSA; ++i) mbar_init(&a_full[i], kConvWarps);
+    for (int i = 0; i < C::kSB; ++i) mbar_init(&b_full[i], 1);
+    for (int i = 0; i < C::kSD; ++i) mbar_init(&done[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tm_w);
+    tma_prefetch_desc(&args.tm_a);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // The weights were there before the widening kernel ran (it waited for
+    // what came before it): only the f16 tokens are waited for, in warp 2.
+    if (lane == 0) {
+      const uint64_t policy = l2_policy_evict_normal();
+      uint32_t it = 0;
+      bool alive = true;
+      for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
+        const int row = (int)(u % MT) * kTileN;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::kSQ;
+          if (!mbar_wait(&q_empty[s], ((it / C::kSQ) & 1) ^ 1, abort_flag, g.status, 61)) {
+            alive = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[s], kQStage);
+          tma_load_2d(smem + C::kOffQ + s * kQStage, &args.tm_w, kb * kKB, row, &q_full[s], policy);
+        }
+      }
+      for (uint32_t j = it > (uint32_t)C::kSQ ? it - C::kSQ : 0; j < it; ++j)  // every load lands before the CTA ends
+        mbar_wait(&q_full[j % C::kSQ], (j / C::kSQ) & 1, abort_flag, g.status, 62);
+    }
+  } else if (warp == 2) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (lane == 0) {
+      const uint64_t policy = l2_policy_evict_last();
+      uint32_t it = 0;
+      bool alive = true;
+      for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
+        const int row = (int)(u / MT) * BN;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::kSB;
+          if (it >= (uint32_t)C::kSB &&
+              !mbar_wait(&done[(it - C::kSB) % C::kSD], ((it - C::kSB) / C::kSD) & 1, abort_flag, g.status, 63)) {
+            alive = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&b_full[s], C::kBBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // (columns and rows past the ends read as zero)
+            tma_load_2d(smem + C::kOffB + s * C::kBBytes + h * (C::kBBytes / 2), &args.tm_a, kb * kKB + h * 64, row,
+                        &b_full[s], policy);
+        }
+      }
+      for (uint32_t j = it > (uint32_t)C::kSB ? it - C::kSB : 0; j < it; ++j)
+        mbar_wait(&b_full[j % C::kSB], (j / C::kSB) & 1, abort_flag, g.status, 62);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(kTileN, BN);
+      uint32_t it = 0, tile = 0;
+      bool alive = true;
+      for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x, ++tile) {
+        const uint32_t buf = tile % C::kAcc;
+        if (!mbar_wait(&acc_empty[buf], ((tile / C::kAcc) & 1) ^ 1, abort_flag, g.status, 64)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::kSA, sb = it % C::kSB;
+          if (!mbar_wait(&b_full[sb], (it / C::kSB) & 1, abort_flag, g.status, 65) ||
+              !mbar_wait(&a_full[s], (it / C::kSA) & 1, abort_flag, g.status, 66)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t b_addr = smem_u32(smem + C::kOffB + sb * C::kBBytes);
+          const uint32_t a_tmem = tmem + C::kACol + s * (kKB / 2);
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk)
+            tc_mma_ts(tmem + buf * BN, a_tmem + kk * 8,
+                      smem_desc_sw128(b_addr + (kk / 4) * (C::kBBytes / 2) + (kk % 4) * 32), idesc, (kb | kk) != 0);
+          tc_commit(&done[it % C::kSD]);
+        }
+        if (!alive) break;
+        tc_commit(&acc_full[buf]);
+      }
+      tc_commit(drain);  // all MMAs complete before tensor memory is freed
+      mbar_wait(drain, 0, abort_flag, g.status, 67);
+    }
+  } else if (warp >= 4 && warp < 4 + kConvWarps) {
+    // thread = 64 codes of one weight row of each k-block
+    const int m = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
+    uint32_t it = 0;
+    bool alive = true;
+    for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int sq = it % C::kSQ, sa = it % C::kSA;
+        if (!mbar_wait(&q_full[sq], (it / C::kSQ) & 1, abort_flag, g.status, 68)) {
+          alive = false;
+          break;
+        }
+        uint4 q[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)  // 16-byte chunk index XOR (row % 8), as TMA wrote it
+          q[c] = *reinterpret_cast<const uint4*>(smem + C::kOffQ + sq * kQStage + m * 128 + (((half * 4 + c) ^ (m & 7)) << 4));
+        if (it >= (uint32_t)C::kSA &&
+            !mbar_wait(&done[(it - C::kSA) % C::kSD], ((it - C::kSA) / C::kSD) & 1, abort_flag, g.status, 69)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[16];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t w[4] = {q[2 * h + c].x, q[2 * h + c].y, q[2 * h + c].z, q[2 * h + c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint2 v = widen4(w[i]);
+              r[8 * c + 2 * i] = v.x;
+              r[8 * c + 2 * i + 1] = v.y;
+            }
+          }
+          tmem_st_32x32b_x16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kACol + sa * (kKB / 2) + half * 32 + h * 16, r);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(&a_full[sa]);
+        mbar_arrive_warp(&q_empty[sq]);  // (after its codes were consumed)
+      }
+    }
+  } else if (warp >= 12) {
+    // lanes of quarter warp % 4 = 32 weight rows; the two groups of four warps take half the tokens each
+    const int quarter = warp & 3, group = (warp - 12) >> 2;
+    constexpr int kCols = BN / 2;
+    uint32_t tile = 0;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
+      const uint32_t buf = tile % C::kAcc;
+      const int64_t n = (u % MT) * kTileN + quarter * 32 + lane;
+      const int t0 = (int)(u / MT) * BN + group * kCols;
+      const float ws = n < g.N ? __ldg(g.w_scale + n) : 0.f;
+      if (!mbar_wait(&acc_full[buf], (tile / C::kAcc) & 1, abort_flag, g.status, 70)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + group * kCols;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c0, v);
+        const int t = t0 + c0;
+        const float as = t + lane < g.T ? __ldg(g.a_scale + t + lane) : 0.f;
+        tc_wait_ld();
+        if (c0 + 32 == kCols) {  // the accumulator is in registers: the next tile may start
+          tc_fence_before();
+          mbar_arrive_warp(&acc_empty[buf]);
+        }
+        const int live = min(32, g.T - t);
+        const int64_t at = (int64_t)t * g.ldo + n;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float y = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, as, i) * ws;
+          if (i < live && n < g.N) store_out(g.out, g.f32, at + (int64_t)i * g.ldo, y);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+bool encode_2d(CUtensorMap* tm, CUtensorMapDataType type, int esize, const void* p, int64_t rows, int64_t cols, int box_cols,
+               int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(tm, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
+  using C = CfgW8<BN>;
+  W8Args args;
+  memset(&args, 0, sizeof args);
+  args.g = p;
+  if (!encode_2d(&args.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, p.N, p.K, kKB, kTileN) ||
+      !encode_2d(&args.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.a16, p.T, p.K, 64, BN))
+    return cudaErrorInvalidValue;
+  static const cudaError_t smem_set =
+      cudaFuncSetAttribute(gemm_w8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (smem_set != cudaSuccess) return smem_set;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(((int64_t)p.T * (p.K / 16) + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cudaError_t err = cudaLaunchKernelEx(&cfg, widen_kernel, p);
+  if (err != cudaSuccess) return err;
+  const int64_t units = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.T + BN - 1) / BN);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, units));
+  cfg.blockDim = dim3(kManyThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  return cudaLaunchKernelEx(&cfg, gemm_w8_kernel<BN>, args);
+}
+
+}  // namespace
+
+cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
+  if (p.T <= kW8FewTokens) {
+    // more rows a block reuse the tokens' fragments; fewer fill the machine
+    const int nt = (p.T + 7) / 8;
+    if (nt <= 2 && p.N >= 64 * 4 * sms) return few_launch_nt<4>(p, s);
+    if (p.N >= 32 * 4 * sms) return few_launch_nt<2>(p, s);
+    return few_launch_nt<1>(p, s);
+  }
+  // The token width whose waves cost least: cycles of a k-block's eight MMAs
+  // (at most 64 tokens cost as much as 128 nearly: the issue rate bounds them).
+  const int64_t MT = (p.N + kTileN - 1) / kTileN;
+  auto cost = [&](int bn, int cycles) { return (MT * ((p.T + bn - 1) / bn) + sms - 1) / sms * cycles; };
+  const int64_t c64 = cost(64, 576), c128 = cost(128, 608), c256 = cost(256, 1120);
+  if (c256 <= c128 && c256 <= c64) return many_launch<256>(p, sms, s);
+  return c128 <= c64 ? many_launch<128>(p, sms, s) : many_launch<64>(p, sms, s);
+}
+
+}  // namespace moe

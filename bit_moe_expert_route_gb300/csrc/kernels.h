@@ -269,4 +269,20 @@ struct LogprobParams {
 };
 cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- 8-bit integer product
+constexpr int kW8FewTokens = 32;  // up to here no workspace beyond the status word
+struct GemmW8Params {
+  const int8_t* a;           // [T], rows lda apart
+  int64_t lda;
+  const float* a_scale;      // [T]
+  const int8_t* w;           // [N][K]
+  const float* w_scale;      // [N]
+  int T, N, K, f32;
+  void* out;                 // bf16 or fp32, rows ldo apart
+  int64_t ldo;
+  uint16_t* a16;             // scratch f16 [T][K] (T > kW8FewTokens)
+  int32_t* status;
+};
+cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
+
 }  // namespace moe

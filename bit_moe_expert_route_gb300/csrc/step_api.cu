@@ -73,6 +73,43 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
   return cuda_status(moe::norm_launch(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
+size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K) {
+  if (T < 0 || N < 1 || K < 16 || K > 65536 || K % 16 != 0) return 0;
+  // the status word, then the tokens' codes as f16
+  return 256 + (T > moe::kW8FewTokens ? ((size_t)T * K * 2 + 255) / 256 * 256 : 0);
+}
+
+int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
+                  const float* w_scale, int T, int N, int K, int type, void* out, int64_t ldo,
+                  void* ws, size_t ws_bytes, void* stream) {
+  const size_t need = moe_gemm_w8a8_workspace_bytes(T, N, K);
+  if (need == 0 || lda < K || lda % 16 != 0 || ldo < N) return MOE_ERR_SHAPE;
+  if (type != MOE_BF16 && type != MOE_F32) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return MOE_ERR_NULL;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+      !aligned(out, type == MOE_F32 ? 4 : 2))
+    return MOE_ERR_ALIGN;
+  if (!ws || !aligned(ws, 256) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
+  moe::GemmW8Params p;
+  p.a = a;
+  p.lda = lda;
+  p.a_scale = a_scale;
+  p.w = w;
+  p.w_scale = w_scale;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.f32 = type == MOE_F32;
+  p.out = out;
+  p.ldo = ldo;
+  p.status = static_cast<int32_t*>(ws);
+  p.a16 = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + 256);
+  return cuda_status(moe::gemm_w8_launch(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
 int moe_token_logprobs(const void* logits, int type, int64_t ld, const int32_t* ids, int N, int V,
                        int k, float* logprob, float* entropy, int32_t* top_ids,
                        float* top_logprobs, void* stream) {

@@ -115,6 +115,9 @@ def lib():
         L.moe_decode_batch_w4.argtypes = [vp, vp, vp, vp, vp, sz, vp]
         L.moe_add_rmsnorm_q8.argtypes = [vp, i64, vp, vp, i32, i32, ctypes.c_float, i32, vp, vp, vp,
                                          vp, vp]
+        L.moe_gemm_w8a8_workspace_bytes.restype = sz
+        L.moe_gemm_w8a8_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_gemm_w8a8.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, sz, vp]
         L.moe_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int32)]
         L.moe_debug_decode_fault.argtypes = [ctypes.c_uint64, i32]
@@ -364,6 +367,38 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
         _p(x), _ld(x), _p(residual), _p(weight), T, d, eps, code, _p(residual_out), _p(q),
         _p(scale), _p(vals), _stream(stream)))
     return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
+
+
+def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+              ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """moe_gemm_w8a8 (include/step.h): a int8 [T, K] (rows may be strided) with a_scale fp32
+    [T], w int8 [N, K] with w_scale fp32 [N]. Returns out [T, N], bf16 or fp32 (`dtype`, or
+    `out`'s own type; out's rows may be strided)."""
+    T, K = a.shape
+    N = w.shape[0]
+    fn, dev = "gemm_w8a8", a.device
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{fn}: the output is {dtype}, bfloat16 or float32 is wanted")
+    _want(fn, "a", a, torch.int8, (T, K), rows=True)
+    _want(fn, "a_scale", a_scale, torch.float32, (T,))
+    _want(fn, "w", w, torch.int8, (N, K))
+    _want(fn, "w_scale", w_scale, torch.float32, (N,))
+    if out is None:
+        out = torch.empty(T, N, dtype=dtype, device=dev)
+    else:
+        _want(fn, "out", out, dtype, (T, N), rows=True)
+    if ws is None:
+        nbytes = lib().moe_gemm_w8a8_workspace_bytes(T, N, K)
+        if nbytes == 0:
+            raise MoeError("moe_gemm_w8a8_workspace_bytes", -3)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check("moe_gemm_w8a8", lib().moe_gemm_w8a8(
+        _p(a), _ld(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _FLOAT_TYPES[dtype], _p(out),
+        _ld(out), _p(ws), ws.numel(), _stream(stream)))
+    return out
 
 
 class TokenLogprobs(NamedTuple):

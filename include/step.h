@@ -20,6 +20,9 @@
 extern "C" {
 #endif
 
+/* Element types of moe_gemm_w8a8's output and moe_token_logprobs' logits. */
+enum moe_float_type { MOE_BF16 = 0, MOE_F32 = 1 };
+
 /* 8-bit output formats of moe_add_rmsnorm_q8. */
 enum moe_q8_format {
   MOE_Q8_INT8 = 0, /* whole numbers -127 .. 127                                */
@@ -53,8 +56,25 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
                        uint16_t* residual_out, void* q, float* scale, uint16_t* values,
                        void* stream);
 
-/* Element types of moe_token_logprobs' logits and moe_gemm_w8a8's output. */
-enum moe_float_type { MOE_BF16 = 0, MOE_F32 = 1 };
+/*
+ * moe_gemm_w8a8: product of 8-bit integers with scales,
+ *   out[t][n] = a_scale[t] * w_scale[n] * sum_k a[t][k] * w[n][k]
+ *   a        int8 [T][K], rows lda bytes apart (lda >= K, multiple of 16)
+ *   a_scale  fp32 [T];  w int8 [N][K];  w_scale fp32 [N]
+ *   out      bf16 or fp32 (`type`, moe_float_type) [T][N], rows ldo >= N
+ *            elements apart
+ *   ws       256-byte aligned, >= moe_gemm_w8a8_workspace_bytes(T, N, K) bytes
+ *            (no initialisation needed), holds the status word
+ * a and w 16-byte aligned; T >= 0 (0 launches nothing), N >= 1, K a multiple of
+ * 16, 16 <= K <= 65536. The integer sum is exact while its partial sums stay
+ * below 2^24 in magnitude (always for K <= 1024), else it carries fp32
+ * rounding; the scales multiply it in fp32 and the result is rounded once. Up
+ * to 32 tokens one launch, else two.
+ */
+size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K);
+int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
+                  const float* w_scale, int T, int N, int K, int type, void* out, int64_t ldo,
+                  void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_token_logprobs: per row of logits z [V], with lse = log sum exp(z):
