@@ -285,4 +285,25 @@ struct GemmW8Params {
 };
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- attention over a shared prefix
+constexpr int kPrefixMaxSms = 160;  // bounds the slices, and so the workspace
+struct PrefixParams {
+  const uint16_t* q;         // [B][Hq][d]
+  const uint16_t *kp, *vp;   // prefix, positions ld_prefix apart
+  const uint16_t *ks, *vs;   // own positions, ld_suffix apart, sequences seq_suffix apart
+  int64_t ld_prefix, ld_suffix, seq_suffix;
+  const int32_t* lens;       // [B]
+  int B, P, S, Hq, Hkv, d;
+  float scale_log2;          // scale * log2 e
+  // the plan
+  int row_warps, prefix_slice, prefix_splits, prefix_blocks, suffix_slice, suffix_splits;
+  float* part_o;             // [prefix_splits + suffix_splits][B Hq][d]
+  float2* part_ml;           // [prefix_splits + suffix_splits][B Hq]: reference (log2), sum
+  uint16_t* out;             // bf16 [B][Hq][d]
+};
+bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d);
+// Fills the plan from the sizes (slices of whole 64-key tiles).
+void prefix_plan(PrefixParams& p, int sms);
+cudaError_t prefix_launch(const PrefixParams& p, cudaStream_t s);
+
 }  // namespace moe

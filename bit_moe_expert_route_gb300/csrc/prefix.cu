@@ -1,0 +1,423 @@
+// Decode attention for a batch whose sequences share a prefix.
+//
+//   o_{b,h} = sum_j softmax_j(scale q_{b,h} . k_j) v_j  over the shared prefix's
+//   positions and then sequence b's own.
+//
+// The prefix's keys and values are the same for every sequence, so the queries
+// of all sequences that read one KV head (B G rows, G query heads a KV head)
+// form one matrix: each K and V tile is read once for all of them, and the
+// products go to the tensor cores. Softmax over the two parts is joined from
+// partial states (m, l, o): a block takes one KV head, a tile of rows and a
+// slice of the prefix, or one sequence's own positions; a second kernel merges
+// a row's partials.
+//
+// A block: 4 warps, WM of them over 16-row tiles and 4 / WM over the keys of
+// each 64-key tile, so that a few rows still use every warp. K and V tiles
+// come through a ring of cp.async stages; m16n8k16 products with fp32 sums,
+// the weights rounded to bf16 for the second product (their rounding, 2^-9
+// each, averages out over the positions; the sum l adds them unrounded). The
+// running maximum moves only when a score passes it by 2^8, which fp32 and
+// bf16 hold without loss, so the output is rarely rescaled.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kPfThreads = 128;
+constexpr int kTileKeys = 64;
+constexpr float kLazyLog2 = 8.f;
+
+MOE_DEVINL float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+MOE_DEVINL void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+MOE_DEVINL void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+MOE_DEVINL void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+MOE_DEVINL uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of D bf16 a row: chunks
+// XORed with the row, so that eight rows' chunks lie in different banks.
+template <int D>
+MOE_DEVINL uint32_t tile_off(int r, int c) {
+  return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+template <int D>
+struct PfCfg {
+  static constexpr int kStages = 3;
+  static constexpr int kTile = kTileKeys * D * 2;  // K or V of one stage
+  static constexpr int kQ = 64 * D * 2;
+  static constexpr int kSmem = kStages * 2 * kTile + kQ;
+  static_assert(kSmem <= 232448, "shared memory exceeded");
+};
+
+// One block's work: `rows` query rows (row r: sequence b0 + r / G, head
+// h G + r % G) against the keys k0 .. k1 - 1 at K, V (rows ld elements apart).
+struct PfItem {
+  int h, row0, rows, b0;
+  const uint16_t *K, *V;
+  int64_t ld;
+  int k0, k1, slot;
+};
+
+template <int D, int WM>
+MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
+  using C = PfCfg<D>;
+  constexpr int WK = 4 / WM, KS = kTileKeys / WK, NT = KS / 8;
+  constexpr int kChunks = D / 8;  // 16-byte chunks a row
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wm = warp % WM, wk = warp / WM;
+  const int G = p.Hq / p.Hkv, g = lane >> 2, t = lane & 3;
+  uint8_t* qs = smem + C::kStages * 2 * C::kTile;
+  auto query_row = [&](int r) { return (int64_t)(it.b0 + r / G) * p.Hq + it.h * G + r % G; };  // of B Hq
+  // queries: rows past the end as zeros
+  for (int i = tid; i < 16 * WM * kChunks; i += kPfThreads) {
+    const int r = i / kChunks, c = i % kChunks;
+    const bool in = r < it.rows;
+    cp_async_16(smem_u32(qs + tile_off<D>(r, c)), p.q + (in ? query_row(it.row0 + r) * D + c * 8 : 0), in ? 16u : 0u);
+  }
+  auto load_stage = [&](int s, int key) {
+    if (key < it.k1) {
+      uint8_t* ks = smem + s * 2 * C::kTile;
+#pragma unroll 4
+      for (int i = tid; i < kTileKeys * kChunks; i += kPfThreads) {
+        const int r = i / kChunks, c = i % kChunks;
+        const bool in = key + r < it.k1;  // keys past the end as zeros: their weight is 0 too
+        const int64_t at = in ? (int64_t)(key + r) * it.ld + c * 8 : 0;
+        cp_async_16(smem_u32(ks + tile_off<D>(r, c)), it.K + at, in ? 16u : 0u);
+        cp_async_16(smem_u32(ks + C::kTile + tile_off<D>(r, c)), it.V + at, in ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) load_stage(s, it.k0 + s * kTileKeys);
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+  const float scale = p.scale_log2;
+  int stage = 0;
+#pragma unroll 1
+  for (int key = it.k0; key < it.k1; key += kTileKeys) {
+    cp_async_wait<C::kStages - 2>();
+    __syncthreads();
+    {
+      const int ahead = stage + C::kStages - 1;
+      load_stage(ahead % C::kStages, key + (C::kStages - 1) * kTileKeys);
+    }
+    const uint8_t* ks = smem + stage * 2 * C::kTile;
+    const uint8_t* vs = ks + C::kTile;
+    float s[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+#pragma unroll 4
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t a[4];
+      ldsm4(a, smem_u32(qs + tile_off<D>(wm * 16 + (lane & 15), 2 * kk + (lane >> 4))));
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {
+        uint32_t b[4];
+        ldsm4(b, smem_u32(ks + tile_off<D>(wk * KS + j * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1))));
+        mma_bf16(s[j], a, b[0], b[1]);
+        mma_bf16(s[j + 1], a, b[2], b[3]);
+      }
+    }
+    const int first = key + wk * KS + 2 * t;  // this lane's first key
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = first + j * 8 + (i & 1) < it.k1;
+        s[j][i] = in ? s[j][i] * scale : -INFINITY;
+        mx[i >> 1] = fmaxf(mx[i >> 1], s[j][i]);
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+    }
+    const bool move = mx[0] > m[0] + kLazyLog2 || mx[1] > m[1] + kLazyLog2;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float nm = fmaxf(m[r], mx[r]);
+        const float f = nm == -INFINITY ? 1.f : ex2(m[r] - nm);  // (m -infinity: 0)
+        l[r] *= f;
+        m[r] = nm;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][2 * r] *= f;
+          o[j][2 * r + 1] *= f;
+        }
+      }
+    }
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[j][i] = ex2(s[j][i] - ref[i >> 1]);
+        l[i >> 1] += s[j][i];
+      }
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      const uint32_t a[4] = {pack_bf16(s[j][0], s[j][1]), pack_bf16(s[j][2], s[j][3]),
+                             pack_bf16(s[j + 1][0], s[j + 1][1]), pack_bf16(s[j + 1][2], s[j + 1][3])};
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t b[4];
+        ldsm4_t(b, smem_u32(vs + tile_off<D>(wk * KS + j * 8 + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * c + (lane >> 4))));
+        mma_bf16(o[2 * c], a, b[0], b[1]);
+        mma_bf16(o[2 * c + 1], a, b[2], b[3]);
+      }
+    }
+    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  cp_async_wait<0>();
+  const int64_t slot = (int64_t)it.slot * p.B * p.Hq;
+  if constexpr (WK == 1) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = wm * 16 + g + 8 * r;
+      if (row < it.rows) {
+        const int64_t at = slot + query_row(it.row0 + row);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2*>(p.part_o + at * D + j * 8 + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+        if (t == 0) p.part_ml[at] = make_float2(m[r], l[r]);
+      }
+    }
+  } else {
+    // the key groups' states of a row tile meet in shared memory
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);                // [4 warps][16][D]
+    float2* sml = reinterpret_cast<float2*>(smem + 64 * D * 4);  // [4 warps][16]
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<float2*>(so + (warp * 16 + row) * D + j * 8 + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+      if (t == 0) sml[warp * 16 + row] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    for (int i = tid; i < 16 * WM * (D / 4); i += kPfThreads) {
+      const int row = i / (D / 4), c = i % (D / 4), tile = row / 16, r = row % 16;
+      if (row >= it.rows) break;  // (rows rise with i)
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) M = fmaxf(M, sml[(k * WM + tile) * 16 + r].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const int w = (k * WM + tile) * 16 + r;
+        const float2 ml = sml[w];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(so + w * D + c * 4);
+        L += f * ml.y;
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      const int64_t at = slot + query_row(it.row0 + row);
+      *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = acc;
+      if (c == 0) p.part_ml[at] = make_float2(M, L);
+    }
+  }
+}
+
+// Blocks 0 .. prefix_blocks - 1: (slice, row tile, KV head) of the prefix, KV
+// head fastest; then (slice, sequence, KV head) of the sequences' own positions.
+template <int D, int WM>
+__global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p) {
+  extern __shared__ __align__(128) uint8_t pf_smem[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  const int G = p.Hq / p.Hkv, R = p.B * G;
+  PfItem it;
+  int i = blockIdx.x;
+  if (i < p.prefix_blocks) {
+    it.h = i % p.Hkv;
+    i /= p.Hkv;
+    const int tiles = (R + 16 * WM - 1) / (16 * WM), tile = i % tiles, split = i / tiles;
+    it.row0 = tile * 16 * WM;
+    it.rows = min(16 * WM, R - it.row0);
+    it.b0 = 0;
+    it.K = p.kp + (int64_t)it.h * D;
+    it.V = p.vp + (int64_t)it.h * D;
+    it.ld = p.ld_prefix;
+    it.k0 = min(p.P, split * p.prefix_slice);
+    it.k1 = min(p.P, it.k0 + p.prefix_slice);
+    it.slot = split;
+    attend<D, WM>(p, it, pf_smem);
+  } else {
+    i -= p.prefix_blocks;
+    it.h = i % p.Hkv;
+    i /= p.Hkv;
+    const int b = i % p.B, split = i / p.B;
+    const int len = max(0, min(p.lens[b], p.S));
+    it.row0 = 0;
+    it.rows = G;
+    it.b0 = b;
+    it.K = p.ks + (int64_t)b * p.seq_suffix + (int64_t)it.h * D;
+    it.V = p.vs + (int64_t)b * p.seq_suffix + (int64_t)it.h * D;
+    it.ld = p.ld_suffix;
+    it.k0 = min(len, split * p.suffix_slice);
+    it.k1 = min(len, it.k0 + p.suffix_slice);
+    it.slot = p.prefix_splits + split;
+    if (it.k0 == it.k1) {  // nothing here: only the state has to say so
+      for (int r = threadIdx.x; r < G; r += kPfThreads)
+        p.part_ml[(int64_t)it.slot * p.B * p.Hq + (int64_t)b * p.Hq + it.h * G + r] = make_float2(-INFINITY, 0.f);
+      return;
+    }
+    attend<D, 1>(p, it, pf_smem);
+  }
+}
+
+// One query row a block: merges its partial states.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams p) {
+  constexpr int kCols = D / 4, kGroups = 256 / kCols;
+  __shared__ float4 acc_s[kGroups][kCols];
+  __shared__ float l_s[kGroups];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.Hq;
+  const int c = threadIdx.x % kCols, grp = threadIdx.x / kCols, n = p.prefix_splits + p.suffix_splits;
+  float M = -INFINITY;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, p.part_ml[s * rows + row].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+#pragma unroll 4
+  for (int s = grp; s < n; s += kGroups) {
+    const float2 ml = p.part_ml[s * rows + row];
+    if (ml.x == -INFINITY) continue;  // (its output was not written)
+    const float f = ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * rows + row) * D + c * 4);
+    L += f * ml.y;
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  acc_s[grp][c] = acc;
+  if (c == 0) l_s[grp] = L;
+  __syncthreads();
+  if (grp == 0) {
+    for (int k = 1; k < kGroups; ++k) {
+      const float4 v = acc_s[k][c];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+      L += l_s[k];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // no position at all: zeros
+    *reinterpret_cast<uint2*>(p.out + row * D + c * 4) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int D, int WM>
+cudaError_t prefix_launch_t(const PrefixParams& p, cudaStream_t s) {
+  using C = PfCfg<D>;
+  static const cudaError_t smem_set =
+      cudaFuncSetAttribute(prefix_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (smem_set != cudaSuccess) return smem_set;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int64_t blocks = p.prefix_blocks + (int64_t)p.suffix_splits * p.B * p.Hkv;
+  if (blocks > 0) {
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kPfThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, prefix_kernel<D, WM>, p);
+    if (err != cudaSuccess) return err;
+  }
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hq));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prefix_combine_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t prefix_launch_d(const PrefixParams& p, cudaStream_t s) {
+  switch (p.row_warps) {
+    case 1: return prefix_launch_t<D, 1>(p, s);
+    case 2: return prefix_launch_t<D, 2>(p, s);
+    default: return prefix_launch_t<D, 4>(p, s);
+  }
+}
+
+}  // namespace
+
+bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d) {
+  return B >= 0 && B <= 65535 && P >= 0 && S >= 0 && P <= 1 << 28 && S <= 1 << 28 && (d == 64 || d == 128 || d == 256) &&
+         Hkv >= 1 && Hkv <= 1024 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 16;
+}
+
+void prefix_plan(PrefixParams& p, int sms) {
+  const int R = p.B * (p.Hq / p.Hkv);
+  const int per_sm = p.d == 256 ? 1 : p.d == 128 ? 2 : 4;
+  const int64_t room = (int64_t)std::min(sms, kPrefixMaxSms) * per_sm;
+  // 16, 32 or 64 rows a block: the fewest row tiles, so that a slice is read
+  // as few times as its rows allow
+  p.row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  const int tiles = (R + 16 * p.row_warps - 1) / (16 * p.row_warps);
+  // one wave of blocks over the prefix, slices of whole 64-key tiles
+  auto slices = [&](int len, int64_t others, int& slice, int& splits) {
+    const int64_t kt = (len + kTileKeys - 1) / kTileKeys;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kt, room / std::max<int64_t>(1, others)));
+    slice = (int)((kt + want - 1) / want) * kTileKeys;
+    splits = len ? (len + slice - 1) / slice : 0;
+  };
+  slices(p.P, (int64_t)p.Hkv * tiles, p.prefix_slice, p.prefix_splits);
+  slices(p.S, (int64_t)p.Hkv * p.B, p.suffix_slice, p.suffix_splits);
+  p.prefix_blocks = p.prefix_splits * p.Hkv * tiles;
+}
+
+cudaError_t prefix_launch(const PrefixParams& p, cudaStream_t s) {
+  if (p.d == 256) return prefix_launch_d<256>(p, s);
+  if (p.d == 128) return prefix_launch_d<128>(p, s);
+  return prefix_launch_d<64>(p, s);
+}
+
+}  // namespace moe

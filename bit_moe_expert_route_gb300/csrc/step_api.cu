@@ -1,11 +1,12 @@
-// C ABI of the operators around the layer (include/step.h): argument checks
-// and launches.
+// C ABI of the operators around the layer (include/step.h, and attention over
+// a shared prefix in include/attn.h): argument checks and launches.
 #include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "attn.h"
 #include "step.h"
 
 namespace {
@@ -37,6 +38,15 @@ int device_sms() {
   const int r = major == 10 && minor == 3 ? sms : MOE_ERR_ARCH;
   if (dev >= 0 && dev < kMaxDev) known[dev].store(r, std::memory_order_relaxed);
   return r;
+}
+
+// Lays the partial states out in the workspace; returns its bytes.
+size_t prefix_carve(moe::PrefixParams& p, void* ws) {
+  const size_t states = (size_t)(p.prefix_splits + p.suffix_splits) * p.B * p.Hq;
+  p.part_ml = static_cast<float2*>(ws);
+  const size_t off = (states * sizeof(float2) + 255) / 256 * 256;
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off);
+  return off + states * p.d * sizeof(float) + 256;
 }
 
 }  // namespace
@@ -137,6 +147,67 @@ int moe_token_logprobs(const void* logits, int type, int64_t ld, const int32_t* 
   p.top_ids = top_ids;
   p.top_logprobs = top_logprobs;
   return cuda_status(moe::logprob_launch(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, int n_kv_heads, int d) {
+  if (!moe::prefix_shape_supported(B, P, S, n_q_heads, n_kv_heads, d)) return 0;
+  moe::PrefixParams p;
+  memset(&p, 0, sizeof p);
+  p.B = B;
+  p.P = P;
+  p.S = S;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.d = d;
+  // the device's SM count decides the slices; the largest count has the most
+  moe::prefix_plan(p, moe::kPrefixMaxSms);
+  return prefix_carve(p, nullptr);
+}
+
+int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
+                         int64_t ld_prefix, const uint16_t* k_suffix, const uint16_t* v_suffix,
+                         int64_t seq_suffix, int64_t ld_suffix, const int32_t* lens, int B, int P,
+                         int S, int n_q_heads, int n_kv_heads, int d, float scale, uint16_t* out,
+                         void* ws, size_t ws_bytes, void* stream) {
+  if (!moe::prefix_shape_supported(B, P, S, n_q_heads, n_kv_heads, d)) return MOE_ERR_SHAPE;
+  const int64_t width = (int64_t)n_kv_heads * d;
+  if (P > 0 && (ld_prefix < width || ld_prefix % 8 != 0)) return MOE_ERR_SHAPE;
+  if (S > 0 && (ld_suffix < width || ld_suffix % 8 != 0 || seq_suffix < 0 || seq_suffix % 8 != 0))
+    return MOE_ERR_SHAPE;
+  if (std::isnan(scale) || std::isinf(scale)) return MOE_ERR_SHAPE;
+  if (B == 0) return MOE_OK;
+  if (!q || !out || (P > 0 && (!k_prefix || !v_prefix)) || (S > 0 && (!k_suffix || !v_suffix || !lens)))
+    return MOE_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) ||
+      !aligned(k_suffix, 16) || !aligned(v_suffix, 16) || !aligned(lens, 4))
+    return MOE_ERR_ALIGN;
+  moe::PrefixParams p;
+  memset(&p, 0, sizeof p);
+  p.q = q;
+  p.kp = k_prefix;
+  p.vp = v_prefix;
+  p.ks = k_suffix;
+  p.vs = v_suffix;
+  p.ld_prefix = ld_prefix;
+  p.ld_suffix = ld_suffix;
+  p.seq_suffix = seq_suffix;
+  p.lens = lens;
+  p.B = B;
+  p.P = P;
+  p.S = S;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.d = d;
+  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf((float)d)) * 1.4426950408889634f;
+  p.out = out;
+  if (!ws || !aligned(ws, 256) ||
+      ws_bytes < moe_prefix_attention_workspace_bytes(B, P, S, n_q_heads, n_kv_heads, d))
+    return MOE_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
+  moe::prefix_plan(p, sms);
+  prefix_carve(p, ws);
+  return cuda_status(moe::prefix_launch(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

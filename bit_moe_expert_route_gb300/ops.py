@@ -119,6 +119,10 @@ def lib():
         L.moe_gemm_w8a8_workspace_bytes.argtypes = [i32, i32, i32]
         L.moe_gemm_w8a8.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, sz, vp]
         L.moe_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.moe_prefix_attention_workspace_bytes.restype = sz
+        L.moe_prefix_attention_workspace_bytes.argtypes = [i32] * 6
+        L.moe_prefix_attention.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, vp] + [i32] * 6 + [
+            ctypes.c_float, vp, vp, sz, vp]
         L.moe_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int32)]
         L.moe_debug_decode_fault.argtypes = [ctypes.c_uint64, i32]
         _lib = L
@@ -398,6 +402,53 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     _check("moe_gemm_w8a8", lib().moe_gemm_w8a8(
         _p(a), _ld(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _FLOAT_TYPES[dtype], _p(out),
         _ld(out), _p(ws), ws.numel(), _stream(stream)))
+    return out
+
+
+def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
+                     k_suffix: torch.Tensor | None = None, v_suffix: torch.Tensor | None = None,
+                     lens: torch.Tensor | None = None, scale: float = 0.0,
+                     out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """moe_prefix_attention (include/attn.h): q bf16 [B, Hq, d]; the shared prefix K, V bf16
+    [P, Hkv, d]; the sequences' own K, V bf16 [B, S, Hkv, d] (or None) of which lens int32 [B]
+    positions count. Positions and sequences may be strided (K and V alike). scale <= 0 means
+    1/sqrt(d). Returns out bf16 [B, Hq, d]."""
+    B, Hq, d = q.shape
+    P, Hkv = k_prefix.shape[0], k_prefix.shape[1]
+    fn, bf = "prefix_attention", torch.bfloat16
+    _want(fn, "q", q, bf, (B, Hq, d))
+
+    def strided(name, k, v, shape):
+        for n, t in (("k_" + name, k), ("v_" + name, v)):
+            if t.dtype != bf or t.shape != shape or not t.is_cuda:
+                raise ValueError(f"{fn}: {n} is {t.dtype} {tuple(t.shape)} on {t.device}, {bf} {tuple(shape)} on the GPU is wanted")
+            if t.numel() and t.stride()[-2:] != (d, 1):
+                raise ValueError(f"{fn}: the heads of {n} are not contiguous")
+        if k.numel() and k.stride() != v.stride():
+            raise ValueError(f"{fn}: k_{name} and v_{name} have different strides")
+    strided("prefix", k_prefix, v_prefix, (P, Hkv, d))
+    S = 0
+    if k_suffix is not None:
+        S = k_suffix.shape[1]
+        strided("suffix", k_suffix, v_suffix, (B, S, Hkv, d))
+        _want(fn, "lens", lens, torch.int32, (B,))
+    if out is None:
+        out = torch.empty(B, Hq, d, dtype=bf, device=q.device)
+    else:
+        _want(fn, "out", out, bf, (B, Hq, d))
+    if ws is None:
+        nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
+        if nbytes == 0:
+            raise MoeError("moe_prefix_attention_workspace_bytes", -3)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    width = Hkv * d
+    _check("moe_prefix_attention", lib().moe_prefix_attention(
+        _p(q), _p(k_prefix), _p(v_prefix), k_prefix.stride(0) if P > 1 else width,
+        _p(k_suffix) if S else None, _p(v_suffix) if S else None,
+        k_suffix.stride(0) if S and B > 1 else 0, k_suffix.stride(1) if S > 1 else width,
+        _p(lens) if S else None, B, P, S, Hq, Hkv, d, float(scale), _p(out), _p(ws), ws.numel(),
+        _stream(stream)))
     return out
 
 

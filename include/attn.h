@@ -49,6 +49,40 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
                          int n_q_heads, int n_kv_heads, int d, float scale, float* out, void* ws,
                          size_t ws_bytes, void* stream);
 
+/*
+ * moe_prefix_attention: decode attention of one new token for each of B
+ * sequences that share a prefix of P cached positions and have len[b] positions
+ * of their own after it. The prefix is read once for all sequences.
+ *   o_{b,h} = sum_j softmax_j(scale * q_{b,h} . k_{g,j}) v_{g,j}
+ * over the prefix's positions and sequence b's own, g = h / (n_q_heads / n_kv_heads).
+ *   q                   bf16 [B][n_q_heads][d]
+ *   k_prefix, v_prefix  bf16 [P][n_kv_heads][d], positions ld_prefix elements
+ *                       apart (at least n_kv_heads * d); may be NULL when P == 0
+ *   k_suffix, v_suffix  bf16 [B][S][n_kv_heads][d], positions ld_suffix and
+ *                       sequences seq_suffix elements apart; NULL when S == 0.
+ *                       Positions from len[b] on are not read.
+ *   lens                int32 [B] device, 0 .. S (others are clamped); NULL when S == 0
+ *   scale               multiplies every score; <= 0 means 1 / sqrt(d)
+ *   out                 bf16 [B][n_q_heads][d]; zeros for a sequence without any
+ *                       position (P == 0 and len[b] == 0)
+ *   ws                  256-byte aligned, >= moe_prefix_attention_workspace_bytes
+ *                       (no initialisation needed)
+ * All pointers but lens (4 bytes) 16-byte aligned, strides multiples of 8
+ * elements. 0 <= B <= 65535 (0 launches nothing), P and S up to 2^28, d in {64,
+ * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a
+ * KV head. Scores and softmax in fp32; the softmax weights are rounded to bf16
+ * before they multiply the values (fp32 sums). Two launches: partial states
+ * over slices of the prefix and of the sequences' own positions, then their
+ * merge in a fixed order. Each is a programmatic dependent of the launch before
+ * it on the stream.
+ */
+size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, int n_kv_heads, int d);
+int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
+                         int64_t ld_prefix, const uint16_t* k_suffix, const uint16_t* v_suffix,
+                         int64_t seq_suffix, int64_t ld_suffix, const int32_t* lens, int B, int P,
+                         int S, int n_q_heads, int n_kv_heads, int d, float scale, uint16_t* out,
+                         void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
