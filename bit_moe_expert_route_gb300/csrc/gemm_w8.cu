@@ -64,7 +64,7 @@ MOE_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, 
 
 // 16 M weight rows x 8 NT tokens a block.
 template <int M, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps) gemm_w8_few_kernel(const GemmW8Params p) {
+__global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_few_kernel(const GemmW8Params p) {
   constexpr int U = M == 1 ? 4 : M == 2 ? 2 : 1;  // 64-code steps in flight (8 weight loads a lane)
   constexpr int kPitch = 16 * M + 4;
   __shared__ float red[kFewWarps][8 * NT][kPitch];
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) gemm_w8_few_kernel(const GemmW
   for (int j = 0; j < NT; ++j) arow[j] = p.a + (int64_t)min(8 * j + g, p.T - 1) * p.lda;
 #pragma unroll 1
   for (int s = s0; s < s1; s += U) {
-    uint4 wv[U][M][2], av[U][NT];
+    uint4 wv[U][M][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (s + u) * 64 + 16 * t;
@@ -103,18 +103,21 @@ __global__ void __launch_bounds__(32 * kFewWarps) gemm_w8_few_kernel(const GemmW
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           wv[u][m][h] = in ? __ldcs(reinterpret_cast<const uint4*>(wrow[m][h] + k)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        av[u][j] = in ? __ldg(reinterpret_cast<const uint4*>(arow[j] + k)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + u) * 64 + 16 * t;
+      const bool in = s + u < s1 && k < p.K;
+      uint4 av[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        av[j] = in ? __ldg(reinterpret_cast<const uint4*>(arow[j] + k)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         auto word = [&](const uint4& v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
         uint2 b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) b[j] = widen4(word(av[u][j]));
+        for (int j = 0; j < NT; ++j) b[j] = widen4(word(av[j]));
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           const uint2 lo = widen4(word(wv[u][m][0])), hi = widen4(word(wv[u][m][1]));
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) gemm_w8_few_kernel(const GemmW
           for (int j = 0; j < NT; ++j) mma_16816(acc[m][j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
         }
       }
+    }
   }
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -186,16 +190,22 @@ __global__ void __launch_bounds__(256) widen_kernel(const GemmW8Params p) {
 constexpr int kTileN = 128;               // weight rows a tile (the MMA's M)
 constexpr int kKB = 128;                  // codes a k-block
 constexpr int kQStage = kTileN * kKB;     // packed codes of a stage: 16 KB
-constexpr int kManyThreads = 640;         // 20 warps, by role below
-constexpr int kConvWarps = 8, kEpiWarps = 8;
+constexpr int kConvGroups = 4;             // four warps each; group i converts k-blocks i, i + 4, ...
+constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4 + 4 * kConvGroups;
+constexpr int kManyThreads = 32 * (kEpiWarp0 + kEpiWarps);  // by role, below
 
 template <int BN>
 struct CfgW8 {
-  static constexpr int kSQ = BN == 256 ? 2 : 4;  // packed-code stages
-  static constexpr int kSA = 4;                  // f16 weight stages in tensor memory, 64 columns each
-  static constexpr int kSB = BN == 256 ? 3 : BN == 128 ? 4 : 6;  // token stages
+  static constexpr int kSQ = 4;                  // packed-code stages
+  static constexpr int kSA = kConvGroups;        // f16 weight stages in tensor memory, 64 columns each
+  // Token stages of kBK codes. 256 tokens leave room for 160 KB of them beside
+  // the packed codes: five stages of half a k-block.
+  static constexpr int kBK = BN == 256 ? 64 : 128;
+  static constexpr int kBSteps = kKB / kBK;      // token stages a k-block
+  static constexpr int kSB = BN == 256 ? 5 : BN == 128 ? 4 : 6;
   static constexpr int kSD = kSA > kSB ? kSA : kSB;
-  static constexpr int kBBytes = BN * kKB * 2;
+  static constexpr int kBBytes = BN * kBK * 2;
   static constexpr int kAcc = BN == 256 ? 1 : 2;  // accumulators: 256 columns in all at 256 and 128
   static constexpr int kACol = kAcc * BN;
   static constexpr int kOffB = 0;
@@ -205,6 +215,10 @@ struct CfgW8 {
   static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
   static_assert(kACol + kSA * (kKB / 2) <= 512, "tensor memory exceeded");
   static_assert(kSmem <= 232448, "shared memory exceeded");
+  // A group waits for its k-block's stage while earlier k-blocks may still be
+  // loading: with fewer stages than groups it would wait on a barrier that is
+  // two phases behind, whose parity looks like the phase it wants.
+  static_assert(kSQ >= kConvGroups, "every converter group needs a stage of its own");
 };
 
 struct W8Args {
@@ -213,8 +227,21 @@ struct W8Args {
   GemmW8Params g;
 };
 
+// mbar_wait by a whole warp: every lane gets one answer, and the lanes are
+// together again after it. (A lane may see the phase complete a poll later than
+// another; tcgen05.ld and .st need the warp undivided, and an arrival on
+// behalf of the warp must happen once.)
+MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
+}
+MOE_DEVINL void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+
 // Roles: warp 0 streams the packed weights, warp 1 issues the MMAs, warp 2
-// streams the tokens' operand, warps 4-11 convert, warps 12-19 write out.
+// streams the tokens' operand, warps 4-19 convert, warps 20-27 write out.
 // Tiles of 128 weight rows by BN tokens, weights fastest, one CTA an SM.
 template <int BN>
 __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_constant__ W8Args args) {
@@ -228,7 +255,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
   uint64_t* b_full = a_full + C::kSA;
   // done[i % kSD]: the MMAs of k-block i have read their operands. One commit
   // frees both: the converters of k-block i wait for k-block i - kSA, the
-  // token stream for i - kSB; the MMA cannot get kSD k-blocks past either.
+  // token stream's stage j for the k-block of stage j - kSB; the MMA cannot get
+  // kSD k-blocks past either.
   uint64_t* done = b_full + C::kSB;
   uint64_t* acc_full = done + C::kSD;
   uint64_t* acc_empty = acc_full + 2;
@@ -242,9 +270,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSQ; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], kConvWarps);
+      mbar_init(&q_empty[i], 4);
     }
-    for (int i = 0; i < C::kSA; ++i) mbar_init(&a_full[i], kConvWarps);
+    for (int i = 0; i < C::kSA; ++i) mbar_init(&a_full[i], 4);
     for (int i = 0; i < C::kSB; ++i) mbar_init(&b_full[i], 1);
     for (int i = 0; i < C::kSD; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -297,17 +325,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       bool alive = true;
       for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
         const int row = (int)(u / MT) * BN;
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        for (int ks = 0; ks < KB * C::kBSteps; ++ks, ++it) {
           const int s = it % C::kSB;
+          const uint32_t before = (it - C::kSB) / C::kBSteps;  // the k-block that used this stage
           if (it >= (uint32_t)C::kSB &&
-              !mbar_wait(&done[(it - C::kSB) % C::kSD], ((it - C::kSB) / C::kSD) & 1, abort_flag, g.status, 63)) {
+              !mbar_wait(&done[before % C::kSD], (before / C::kSD) & 1, abort_flag, g.status, 63)) {
             alive = false;
             break;
           }
           mbar_arrive_expect_tx(&b_full[s], C::kBBytes);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)  // (columns and rows past the ends read as zero)
-            tma_load_2d(smem + C::kOffB + s * C::kBBytes + h * (C::kBBytes / 2), &args.tm_a, kb * kKB + h * 64, row,
+          for (int h = 0; h < C::kBK / 64; ++h)  // (columns and rows past the ends read as zero)
+            tma_load_2d(smem + C::kOffB + s * C::kBBytes + h * (BN * 128), &args.tm_a, ks * C::kBK + h * 64, row,
                         &b_full[s], policy);
         }
       }
@@ -317,27 +346,34 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16_f32(kTileN, BN);
-      uint32_t it = 0, tile = 0;
+      uint32_t it = 0, itb = 0, tile = 0;
       bool alive = true;
       for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x, ++tile) {
         const uint32_t buf = tile % C::kAcc;
         if (!mbar_wait(&acc_empty[buf], ((tile / C::kAcc) & 1) ^ 1, abort_flag, g.status, 64)) break;
         tc_fence_after();
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = it % C::kSA, sb = it % C::kSB;
-          if (!mbar_wait(&b_full[sb], (it / C::kSB) & 1, abort_flag, g.status, 65) ||
-              !mbar_wait(&a_full[s], (it / C::kSA) & 1, abort_flag, g.status, 66)) {
+        for (int kb = 0; kb < KB && alive; ++kb, ++it) {
+          const int s = it % C::kSA;
+          if (!mbar_wait(&a_full[s], (it / C::kSA) & 1, abort_flag, g.status, 66)) {
             alive = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t b_addr = smem_u32(smem + C::kOffB + sb * C::kBBytes);
           const uint32_t a_tmem = tmem + C::kACol + s * (kKB / 2);
 #pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk)
-            tc_mma_ts(tmem + buf * BN, a_tmem + kk * 8,
-                      smem_desc_sw128(b_addr + (kk / 4) * (C::kBBytes / 2) + (kk % 4) * 32), idesc, (kb | kk) != 0);
-          tc_commit(&done[it % C::kSD]);
+          for (int h = 0; h < C::kBSteps; ++h, ++itb) {
+            const int sb = itb % C::kSB;
+            if (!mbar_wait(&b_full[sb], (itb / C::kSB) & 1, abort_flag, g.status, 65)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t b_addr = smem_u32(smem + C::kOffB + sb * C::kBBytes);
+#pragma unroll
+            for (int kk = 0; kk < C::kBK / 16; ++kk)
+              tc_mma_ts(tmem + buf * BN, a_tmem + (h * (C::kBK / 16) + kk) * 8,
+                        smem_desc_sw128(b_addr + (kk / 4) * (BN * 128) + (kk % 4) * 32), idesc, (kb | h | kk) != 0);
+          }
+          if (alive) tc_commit(&done[it % C::kSD]);
         }
         if (!alive) break;
         tc_commit(&acc_full[buf]);
@@ -345,52 +381,47 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
       mbar_wait(drain, 0, abort_flag, g.status, 67);
     }
-  } else if (warp >= 4 && warp < 4 + kConvWarps) {
-    // thread = 64 codes of one weight row of each k-block
-    const int m = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
-    uint32_t it = 0;
-    bool alive = true;
-    for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int sq = it % C::kSQ, sa = it % C::kSA;
-        if (!mbar_wait(&q_full[sq], (it / C::kSQ) & 1, abort_flag, g.status, 68)) {
-          alive = false;
-          break;
-        }
-        uint4 q[4];
+  } else if (warp >= 4 && warp < kEpiWarp0) {
+    // thread = one weight row of every kConvGroups-th k-block: a k-block takes
+    // its group about 1000 cycles from wait to signal, most of it latency, so
+    // several are under way at once
+    const int m = (warp & 3) * 32 + lane, group = (warp - 4) >> 2;
+    const uint32_t a_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kACol + group * (kKB / 2);
+    const int64_t mine = blockIdx.x < units ? ((units - 1 - blockIdx.x) / gridDim.x + 1) * KB : 0;  // this CTA's k-blocks
+    for (int64_t it = group; it < mine; it += kConvGroups) {
+      const int sq = (int)(it % C::kSQ);
+      if (!warp_wait(&q_full[sq], (uint32_t)(it / C::kSQ) & 1, abort_flag, g.status, 68)) break;
+      uint4 q[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)  // 16-byte chunk index XOR (row % 8), as TMA wrote it
-          q[c] = *reinterpret_cast<const uint4*>(smem + C::kOffQ + sq * kQStage + m * 128 + (((half * 4 + c) ^ (m & 7)) << 4));
-        if (it >= (uint32_t)C::kSA &&
-            !mbar_wait(&done[(it - C::kSA) % C::kSD], ((it - C::kSA) / C::kSD) & 1, abort_flag, g.status, 69)) {
-          alive = false;
-          break;
-        }
-        tc_fence_after();
+      for (int c = 0; c < 8; ++c)  // 16-byte chunk index XOR (row % 8), as TMA wrote it
+        q[c] = *reinterpret_cast<const uint4*>(smem + C::kOffQ + sq * kQStage + m * 128 + ((c ^ (m & 7)) << 4));
+      if (it >= C::kSA &&
+          !warp_wait(&done[(it - C::kSA) % C::kSD], (uint32_t)((it - C::kSA) / C::kSD) & 1, abort_flag, g.status, 69))
+        break;
+      tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[16];
+      for (int h = 0; h < 4; ++h) {
+        uint32_t r[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t w[4] = {q[2 * h + c].x, q[2 * h + c].y, q[2 * h + c].z, q[2 * h + c].w};
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w[4] = {q[2 * h + c].x, q[2 * h + c].y, q[2 * h + c].z, q[2 * h + c].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint2 v = widen4(w[i]);
-              r[8 * c + 2 * i] = v.x;
-              r[8 * c + 2 * i + 1] = v.y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint2 v = widen4(w[i]);
+            r[8 * c + 2 * i] = v.x;
+            r[8 * c + 2 * i + 1] = v.y;
           }
-          tmem_st_32x32b_x16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kACol + sa * (kKB / 2) + half * 32 + h * 16, r);
         }
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive_warp(&a_full[sa]);
-        mbar_arrive_warp(&q_empty[sq]);  // (after its codes were consumed)
+        tmem_st_32x32b_x16(a_tmem + h * 16, r);
       }
+      warp_arrive(&q_empty[sq]);  // (its codes were consumed)
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(&a_full[group]);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= kEpiWarp0) {
     // lanes of quarter warp % 4 = 32 weight rows; the two groups of four warps take half the tokens each
-    const int quarter = warp & 3, group = (warp - 12) >> 2;
+    const int quarter = warp & 3, group = (warp - kEpiWarp0) >> 2;
     constexpr int kCols = BN / 2;
     uint32_t tile = 0;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
@@ -398,11 +429,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       const int64_t n = (u % MT) * kTileN + quarter * 32 + lane;
       const int t0 = (int)(u / MT) * BN + group * kCols;
       const float ws = n < g.N ? __ldg(g.w_scale + n) : 0.f;
-      if (!mbar_wait(&acc_full[buf], (tile / C::kAcc) & 1, abort_flag, g.status, 70)) break;
+      if (!warp_wait(&acc_full[buf], (tile / C::kAcc) & 1, abort_flag, g.status, 70)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + group * kCols;
 #pragma unroll 1
       for (int c0 = 0; c0 < kCols; c0 += 32) {
+        __syncwarp();  // (the stores of the chunk before part the lanes)
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c0, v);
         const int t = t0 + c0;
@@ -410,7 +442,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
         tc_wait_ld();
         if (c0 + 32 == kCols) {  // the accumulator is in registers: the next tile may start
           tc_fence_before();
-          mbar_arrive_warp(&acc_empty[buf]);
+          warp_arrive(&acc_empty[buf]);
         }
         const int live = min(32, g.T - t);
         const int64_t at = (int64_t)t * g.ldo + n;
@@ -422,6 +454,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       }
     }
   }
+  __syncwarp();  // the single-lane roles join their warps
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -11,9 +11,9 @@
 // row's sums are moved to the largest logit at the end, where neither
 // difference cancels. z - ref is taken in natural units before the
 // multiplication by log2 e, so that large logits lose nothing to the
-// constant's rounding. Two elements go through the packed fp32 add, multiply
-// and fused multiply-add at a time; what is left is one ex2 an element, the
-// nearest limit after HBM for bf16 logits.
+// constant's rounding. bf16 logits enter a mixed-precision add as they are, and
+// two elements at a time go through the packed fp32 multiply, add and fused
+// multiply-add: about four instructions an element with its ex2.
 //
 // Top k (k <= 32): a warp holds its best 32 in order, one a lane, and inserts
 // what reaches the block's threshold (a lower bound of the row's k-th best: the
@@ -141,20 +141,6 @@ MOE_DEVINL uint4 load_vec(const void* row, int64_t first, int V) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool F32>
-MOE_DEVINL void widen(const uint4& v, float (&z)[kVecElems<F32>]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (F32) {
-      z[i] = __uint_as_float(u[i]);
-    } else {
-      z[2 * i] = __uint_as_float(u[i] << 16);
-      z[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  }
-}
-
 // The vector's largest element (NaN if one is).
 template <bool F32>
 MOE_DEVINL float largest(const uint4& v) {
@@ -169,26 +155,50 @@ MOE_DEVINL float largest(const uint4& v) {
   }
 }
 
+// z - ref of a vector's elements. bf16 logits go through the mixed-precision
+// add, which takes them from their half of the word as they are.
+template <bool F32>
+MOE_DEVINL void distances(const uint4& v, float nref, float2 (&d)[kVecElems<F32> / 2]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      d[i] = __fadd2_rn(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), make_float2(nref, nref));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+          "add.rn.f32.bf16 %0, lo, %3;\n\tadd.rn.f32.bf16 %1, hi, %3;\n\t}"
+          : "=f"(d[i].x), "=f"(d[i].y)
+          : "r"(u[i]), "f"(nref));
+  }
+}
+
 template <bool F32>
 MOE_DEVINL void add_vec(Sums& s, const uint4& v, float vmax) {
   constexpr int E = kVecElems<F32>;
-  s.top = max_nan(s.top, vmax);
   if (vmax > s.ref + kLazy) rebase(s, vmax);  // (+infinity ends as NaN, as it should)
-  float z[E];
-  widen<F32>(v, z);
-  const float2 nref = make_float2(-s.ref, -s.ref), c = make_float2(kLog2e, kLog2e);
-  float2 S = make_float2(0.f, 0.f), U = make_float2(0.f, 0.f);
+  float2 d[E / 2], S = make_float2(0.f, 0.f), U = make_float2(0.f, 0.f);
+  distances<F32>(v, -s.ref, d);
+  const float2 c = make_float2(kLog2e, kLog2e);
 #pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    const float2 d = __fadd2_rn(make_float2(z[i], z[i + 1]), nref);
-    const float2 x = __fmul2_rn(d, c);
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 x = __fmul2_rn(d[i], c);
     const float2 e = make_float2(ex2(x.x), ex2(x.y));
     S = __fadd2_rn(S, e);
-    // -infinity: its weight is 0, and so is 0 * (a finite distance)
-    U = __ffma2_rn(e, make_float2(max_nan(d.x, kLowest), max_nan(d.y, kLowest)), U);
+    U = __ffma2_rn(e, d[i], U);
   }
   s.S += S.x + S.y;
-  s.U += U.x + U.y;
+  float u = U.x + U.y;
+  if (u != u) {  // -infinity among them (0 * infinity): its weight is 0, and so is 0 * (a finite distance)
+    u = 0.f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      u = fmaf(ex2(d[i].x * kLog2e), max_nan(d[i].x, kLowest), u);
+      u = fmaf(ex2(d[i].y * kLog2e), max_nan(d[i].y, kLowest), u);
+    }
+  }
+  s.U += u;
 }
 
 struct LpShared {
@@ -249,19 +259,26 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   s.top = -INFINITY;
   uint64_t mine = 0;  // this lane's entry of the warp's list, 0 = none
   uint32_t bar = 0;   // the rank that an element has to reach
-  for (int v = v0; v < v1; v += kUnroll * kLpThreads) {
-    uint4 w[kUnroll];
-    float vm[kUnroll], m = -INFINITY;
+  auto load = [&](int v, uint4 (&w)[kUnroll]) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int vi = v + i * kLpThreads + tid;
       w[i] = vi < v1 ? load_vec<F32>(base, (int64_t)vi * E - lead, p.V) : none_vec<F32>();
     }
+  };
+  uint4 w[kUnroll];
+  load(v0, w);
+#pragma unroll 1
+  for (int v = v0; v < v1; v += kUnroll * kLpThreads) {
+    uint4 next[kUnroll];
+    load(v + kUnroll * kLpThreads, next);  // in flight while these are summed
+    float vm[kUnroll], m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       vm[i] = largest<F32>(w[i]);
       m = max_nan(m, vm[i]);
     }
+    s.top = max_nan(s.top, m);
     if (v == v0) s.ref = fminf(fmaxf(m, kLowest), -kLowest);  // (NaN: the lowest)
     if (TOP && v == v0) {
       // the k-th largest of the threads' maxima bounds the k-th largest element
@@ -277,45 +294,43 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
     for (int i = 0; i < kUnroll; ++i) add_vec<F32>(s, w[i], vm[i]);
     if (TOP) {
       bar = max(bar, *reinterpret_cast<volatile uint32_t*>(&sh.threshold));
+      // (a NaN hides its vector's other elements: those are looked at)
+      if (__any_sync(0xffffffffu, m != m || rank_of(m) >= bar)) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int vi = v + i * kLpThreads + tid;
-        const int64_t first = (int64_t)vi * E - lead;
-        // (a NaN hides the vector's other elements: look at each)
-        const bool any = vi < v1 && (vm[i] != vm[i] || rank_of(vm[i]) >= bar);
-        if (__any_sync(0xffffffffu, any)) {
-          float z[E];
-          widen<F32>(w[i], z);
-          bool moved = false;
-#pragma unroll 1
-          for (int e = 0; e < E; ++e) {
-            float ze = z[0];
-#pragma unroll
-            for (int q = 1; q < E; ++q) ze = q == e ? z[q] : ze;
-            const int64_t index = first + e;
-            const uint64_t key = any && index >= 0 && index < p.V ? key_of(ze, (int)index) : 0ull;
+        for (int i = 0; i < kUnroll; ++i) {
+          const int vi = v + i * kLpThreads + tid;
+          unsigned hit = __ballot_sync(0xffffffffu, vi < v1 && (vm[i] != vm[i] || rank_of(vm[i]) >= bar));
+          while (hit) {  // one lane's vector at a time, an element a lane
+            const int src = __ffs(hit) - 1;
+            hit &= hit - 1;
+            const uint32_t u[4] = {__shfl_sync(0xffffffffu, w[i].x, src), __shfl_sync(0xffffffffu, w[i].y, src),
+                                   __shfl_sync(0xffffffffu, w[i].z, src), __shfl_sync(0xffffffffu, w[i].w, src)};
+            const int at4 = F32 ? lane : lane >> 1;
+            const uint32_t word = at4 == 0 ? u[0] : at4 == 1 ? u[1] : at4 == 2 ? u[2] : u[3];
+            const float z = __uint_as_float(F32 ? word : (lane & 1) ? word & 0xFFFF0000u : word << 16);
+            const int64_t index = (int64_t)(vi - lane + src) * E - lead + lane;
+            const uint64_t key = lane < E && index >= 0 && index < p.V ? key_of(z, (int)index) : 0ull;
             unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
             while (todo) {
-              const int src = __ffs(todo) - 1;
+              const uint64_t c = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
               todo &= todo - 1;
-              const uint64_t c = __shfl_sync(0xffffffffu, key, src);
               const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
               const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
               if (lane == at) mine = c;
               else if (lane > at) mine = up;
-              moved = true;
-            }
-          }
-          if (moved) {  // the warp's k-th best may raise the block's threshold
-            const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
-            if (kth > bar) {
-              bar = kth;
-              if (lane == 0) atomicMax(&sh.threshold, kth);
             }
           }
         }
+        // the warp's k-th best may raise the block's threshold
+        const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
+        if (kth > bar) {
+          bar = kth;
+          if (lane == 0) atomicMax(&sh.threshold, kth);
+        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) w[i] = next[i];
   }
   // the block's sums and list
 #pragma unroll

@@ -8,8 +8,8 @@
 // reduction carries both the largest |u| and the sum of squares, and the
 // codes follow from values that stayed in registers. u is a product of two
 // bf16 values, exact in fp32; u * (top / a) in fp32 is within 3 * 2^-24 of the
-// exact quotient (relative), so only a quotient that near a rounding border
-// is decided in 64 bits: every code is the correctly rounded one.
+// exact quotient (relative), so only a quotient that near a rounding border is
+// compared with it exactly: every code is the correctly rounded one.
 //
 // Bound by HBM: 7 bytes an element (x, residual in; residual, q out), 9 with
 // the bf16 values. A row belongs to G threads of NV 16-byte vectors each. Rows
@@ -66,6 +66,49 @@ MOE_DEVINL bool near_border_e4m3(float t) {
   const float n = (t + kRoundSub) - kRoundSub;
   const bool sub = !(fabsf(t - n) < 0x1p-10f - 1e-8f);
   return fabsf(t) >= 0x1p-6f ? cut : sub;
+}
+
+// A vector with a quotient near a border: the quotients moved to the border's
+// right side (or onto it: a tie). u and a have 16 significant bits, so
+// top |u| and border * a (borders have 8 bits at most) are exact in fp32 and
+// their comparison is the exact quotient's with the border. Out of line, for
+// the instruction cache: it is rarely taken.
+struct Quotients8 {
+  float t[8];
+};
+template <bool E4M3>
+__device__ __noinline__ Quotients8 settle(uint4 r, uint4 weight, float a, bool some) {
+  constexpr float kTop = E4M3 ? 448.f : 127.f;
+  // far from fp32's ends, by an exact factor: neither product overflows or loses bits
+  const float lift = a < 1e-20f ? 0x1p64f : a > 1e20f ? 0x1p-64f : 1.f, al = a * lift;
+  float f[8], w[8];
+  unpack8(r, f);
+  unpack8(weight, w);
+  Quotients8 c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float u = f[e] * w[e] * lift;
+    float t = some ? u * (kTop / al) : 0.f;
+    if (some && (E4M3 ? near_border_e4m3(t) : near_border_int8(t))) {
+      const float b = fabsf(t);
+      float border, below, above;  // the border and values that round to either side of it
+      if (!E4M3 || b < 0x1p-6f) {
+        const float unit = E4M3 ? 0x1p-9f : 1.f;
+        below = floorf(b / unit) * unit;
+        above = below + unit;
+        border = below + 0.5f * unit;
+      } else {
+        const uint32_t mid = (__float_as_uint(b) & ~0xFFFFFu) | 0x80000u;
+        border = __uint_as_float(mid);
+        below = __uint_as_float(mid - 1);
+        above = __uint_as_float(mid + 1);
+      }
+      const float exact = kTop * fabsf(u), at = border * al;
+      t = copysignf(exact < at ? below : exact > at ? above : border, t);
+    }
+    c.t[e] = t;
+  }
+  return c;
 }
 
 template <int NV, bool E4M3>
@@ -149,7 +192,7 @@ __global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_ker
   const float scale = fine ? a / kTop / sqrtf(ss / (float)p.d + p.eps) : nan;
   if (lt == 0) p.scale[row] = scale;
   // Rows without a usable fp32 quotient (zeros, values that are not finite,
-  // and rows so small that top / a overflows) take the 64-bit path, as NaNs.
+  // and rows so small that top / a overflows) are settled apart, as NaNs.
   const bool some = fine && a > 0.f;
   const float inv = some && a > 1e-36f ? kTop / a : nan;
 #pragma unroll
@@ -157,8 +200,9 @@ __global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_ker
     const int v = lt + i * G;
     if (v < nvec) {
       float f[8], w[8], t[8];
+      const uint4 weight = __ldg(reinterpret_cast<const uint4*>(p.weight) + v);
       unpack8(r[i], f);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + v), w);
+      unpack8(weight, w);
       bool near = false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -166,19 +210,9 @@ __global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_ker
         near |= E4M3 ? near_border_e4m3(t[e]) : near_border_int8(t[e]);
       }
       if (near) {
+        const Quotients8 c = settle<E4M3>(r[i], weight, a, some);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!(E4M3 ? near_border_e4m3(t[e]) : near_border_int8(t[e]))) continue;
-          const double z = some ? (double)kTop * (double)(f[e] * w[e]) / (double)a : 0.0;
-          if constexpr (E4M3) {
-            // cut to fp32 with the last bit set when anything was cut off
-            // (round to odd), which the second rounding cannot mistake
-            const float c = __double2float_rz(z);
-            t[e] = (double)c == z ? c : __uint_as_float(__float_as_uint(c) | 1u);
-          } else {
-            t[e] = (float)rint(z);
-          }
-        }
+        for (int e = 0; e < 8; ++e) t[e] = c.t[e];
       }
       uint32_t word[2];
 #pragma unroll

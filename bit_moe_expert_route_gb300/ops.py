@@ -143,8 +143,11 @@ def _p(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle; by default the current device's current stream (asked for without
+    making a Stream object, which costs more than a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
@@ -330,14 +333,31 @@ class NormQ8(NamedTuple):
 
 
 def _want(fn, name, t, dtype, shape, rows=False):
-    """Refuses a tensor of another type, shape, device or layout than the call reads
-    (rows: only each row has to be contiguous)."""
+    """The address of a tensor of the type, shape and layout that the call reads (rows: only
+    each row has to be contiguous); refuses any other."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and (
+            t.is_contiguous() or rows and t.stride(-1) == 1):
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)}, {dtype} {tuple(shape)} is wanted")
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} is not on the GPU")
-    if not t.is_contiguous() and not (rows and t.stride(-1) == 1):
-        raise ValueError(f"{fn}: {name} is not contiguous")
+    raise ValueError(f"{fn}: {name} is not contiguous")
+
+
+def _want_cache(fn, name, k, v, shape):
+    """The addresses of a K and a V cache whose heads are contiguous, and their strides (which
+    have to be the same)."""
+    bf, st = torch.bfloat16, k.stride()
+    if (k.dtype is bf and v.dtype is bf and k.shape == shape and v.shape == shape and k.is_cuda
+            and v.is_cuda and (k.numel() == 0 or st == v.stride() and st[-1] == 1
+                               and (st[-2] == shape[-1] or shape[-2] == 1))):
+        return k.data_ptr(), v.data_ptr(), st
+    for n, t in (("k_" + name, k), ("v_" + name, v)):
+        if t.dtype != bf or t.shape != shape or not t.is_cuda:
+            raise ValueError(f"{fn}: {n} is {t.dtype} {tuple(t.shape)} on {t.device}, "
+                             f"{bf} {tuple(shape)} on the GPU is wanted")
+    raise ValueError(f"{fn}: k_{name} and v_{name} have different strides or scattered heads")
 
 
 def _ld(t):
@@ -356,20 +376,24 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
     if fmt not in Q8_FORMATS:
         raise ValueError(f"{fn}: fmt is {fmt!r}, 'int8' or 'e4m3' is wanted")
     code, dtype = Q8_FORMATS[fmt]
-    _want(fn, "x", x, bf, (T, d), rows=True)
-    _want(fn, "weight", weight, bf, (d,))
+    shape = (T, d)
+    px = _want(fn, "x", x, bf, shape, rows=True)
+    pw = _want(fn, "weight", weight, bf, (d,))
+    pr = po = pv = vals = None
     if residual is not None:
-        _want(fn, "residual", residual, bf, (T, d))
+        pr = _want(fn, "residual", residual, bf, shape)
         if residual_out is None:
-            residual_out = torch.empty(T, d, dtype=bf, device=dev)
+            residual_out = torch.empty(shape, dtype=bf, device=dev)
     if residual_out is not None:
-        _want(fn, "residual_out", residual_out, bf, (T, d))
-    q = torch.empty(T, d, dtype=dtype, device=dev)
+        po = _want(fn, "residual_out", residual_out, bf, shape)
+    q = torch.empty(shape, dtype=dtype, device=dev)
     scale = torch.empty(T, dtype=torch.float32, device=dev)
-    vals = torch.empty(T, d, dtype=bf, device=dev) if values else None
-    _check("moe_add_rmsnorm_q8", lib().moe_add_rmsnorm_q8(
-        _p(x), _ld(x), _p(residual), _p(weight), T, d, eps, code, _p(residual_out), _p(q),
-        _p(scale), _p(vals), _stream(stream)))
+    if values:
+        vals = torch.empty(shape, dtype=bf, device=dev)
+        pv = vals.data_ptr()
+    rc = lib().moe_add_rmsnorm_q8(px, _ld(x), pr, pw, T, d, eps, code, po, q.data_ptr(),
+                                  scale.data_ptr(), pv, _stream(stream))
+    _check("moe_add_rmsnorm_q8", rc)
     return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
 
 
@@ -381,27 +405,26 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     `out`'s own type; out's rows may be strided)."""
     T, K = a.shape
     N = w.shape[0]
-    fn, dev = "gemm_w8a8", a.device
+    fn, dev, f32 = "gemm_w8a8", a.device, torch.float32
     if out is not None:
         dtype = out.dtype
     if dtype not in _FLOAT_TYPES:
         raise ValueError(f"{fn}: the output is {dtype}, bfloat16 or float32 is wanted")
-    _want(fn, "a", a, torch.int8, (T, K), rows=True)
-    _want(fn, "a_scale", a_scale, torch.float32, (T,))
-    _want(fn, "w", w, torch.int8, (N, K))
-    _want(fn, "w_scale", w_scale, torch.float32, (N,))
+    pa = _want(fn, "a", a, torch.int8, (T, K), rows=True)
+    ps = _want(fn, "a_scale", a_scale, f32, (T,))
+    pw = _want(fn, "w", w, torch.int8, (N, K))
+    pt = _want(fn, "w_scale", w_scale, f32, (N,))
     if out is None:
-        out = torch.empty(T, N, dtype=dtype, device=dev)
-    else:
-        _want(fn, "out", out, dtype, (T, N), rows=True)
+        out = torch.empty((T, N), dtype=dtype, device=dev)
+    po = _want(fn, "out", out, dtype, (T, N), rows=True)
     if ws is None:
         nbytes = lib().moe_gemm_w8a8_workspace_bytes(T, N, K)
         if nbytes == 0:
             raise MoeError("moe_gemm_w8a8_workspace_bytes", -3)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check("moe_gemm_w8a8", lib().moe_gemm_w8a8(
-        _p(a), _ld(a), _p(a_scale), _p(w), _p(w_scale), T, N, K, _FLOAT_TYPES[dtype], _p(out),
-        _ld(out), _p(ws), ws.numel(), _stream(stream)))
+    rc = lib().moe_gemm_w8a8(pa, _ld(a), ps, pw, pt, T, N, K, _FLOAT_TYPES[dtype], po, _ld(out),
+                             ws.data_ptr(), ws.numel(), _stream(stream))
+    _check("moe_gemm_w8a8", rc)
     return out
 
 
@@ -415,40 +438,29 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     positions count. Positions and sequences may be strided (K and V alike). scale <= 0 means
     1/sqrt(d). Returns out bf16 [B, Hq, d]."""
     B, Hq, d = q.shape
-    P, Hkv = k_prefix.shape[0], k_prefix.shape[1]
-    fn, bf = "prefix_attention", torch.bfloat16
-    _want(fn, "q", q, bf, (B, Hq, d))
-
-    def strided(name, k, v, shape):
-        for n, t in (("k_" + name, k), ("v_" + name, v)):
-            if t.dtype != bf or t.shape != shape or not t.is_cuda:
-                raise ValueError(f"{fn}: {n} is {t.dtype} {tuple(t.shape)} on {t.device}, {bf} {tuple(shape)} on the GPU is wanted")
-            if t.numel() and t.stride()[-2:] != (d, 1):
-                raise ValueError(f"{fn}: the heads of {n} are not contiguous")
-        if k.numel() and k.stride() != v.stride():
-            raise ValueError(f"{fn}: k_{name} and v_{name} have different strides")
-    strided("prefix", k_prefix, v_prefix, (P, Hkv, d))
-    S = 0
+    P, Hkv = k_prefix.shape[:2]
+    fn, bf, dev = "prefix_attention", torch.bfloat16, q.device
+    pq = _want(fn, "q", q, bf, (B, Hq, d))
+    pk, pv, ld = _want_cache(fn, "prefix", k_prefix, v_prefix, (P, Hkv, d))
+    S, pks, pvs, lds, seq, pl = 0, None, None, (0, 0), 0, None
     if k_suffix is not None:
         S = k_suffix.shape[1]
-        strided("suffix", k_suffix, v_suffix, (B, S, Hkv, d))
-        _want(fn, "lens", lens, torch.int32, (B,))
+        pks, pvs, lds = _want_cache(fn, "suffix", k_suffix, v_suffix, (B, S, Hkv, d))
+        pl = _want(fn, "lens", lens, torch.int32, (B,))
     if out is None:
-        out = torch.empty(B, Hq, d, dtype=bf, device=q.device)
-    else:
-        _want(fn, "out", out, bf, (B, Hq, d))
+        out = torch.empty((B, Hq, d), dtype=bf, device=dev)
+    po = _want(fn, "out", out, bf, (B, Hq, d))
     if ws is None:
         nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
         if nbytes == 0:
             raise MoeError("moe_prefix_attention_workspace_bytes", -3)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    width = Hkv * d
-    _check("moe_prefix_attention", lib().moe_prefix_attention(
-        _p(q), _p(k_prefix), _p(v_prefix), k_prefix.stride(0) if P > 1 else width,
-        _p(k_suffix) if S else None, _p(v_suffix) if S else None,
-        k_suffix.stride(0) if S and B > 1 else 0, k_suffix.stride(1) if S > 1 else width,
-        _p(lens) if S else None, B, P, S, Hq, Hkv, d, float(scale), _p(out), _p(ws), ws.numel(),
-        _stream(stream)))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    width = Hkv * d  # the stride of an axis of one entry says nothing
+    rc = lib().moe_prefix_attention(
+        pq, pk, pv, ld[0] if P > 1 else width, pks, pvs, lds[0] if B > 1 else 0,
+        lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po, ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    _check("moe_prefix_attention", rc)
     return out
 
 
@@ -471,17 +483,20 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
         raise ValueError(f"{fn}: logits are {logits.dtype}, bfloat16 or float32 is wanted")
     if not 0 <= top_k <= min(32, V):
         raise ValueError(f"{fn}: top_k is {top_k}, 0 .. min(32, {V}) is wanted")
-    _want(fn, "logits", logits, logits.dtype, (N, V), rows=True)
+    pz = _want(fn, "logits", logits, logits.dtype, (N, V), rows=True)
+    pi = pl = pt = pp = logprob = None
     if ids is not None:
-        _want(fn, "ids", ids, torch.int32, (N,))
-    logprob = None if ids is None else torch.empty(N, dtype=torch.float32, device=dev)
+        pi = _want(fn, "ids", ids, torch.int32, (N,))
+        logprob = torch.empty(N, dtype=torch.float32, device=dev)
+        pl = logprob.data_ptr()
     entropy = torch.empty(N, dtype=torch.float32, device=dev)
-    top_ids = torch.empty(N, top_k, dtype=torch.int32, device=dev)
-    top_lp = torch.empty(N, top_k, dtype=torch.float32, device=dev)
-    _check("moe_token_logprobs", lib().moe_token_logprobs(
-        _p(logits), _FLOAT_TYPES[logits.dtype], _ld(logits), _p(ids), N, V, top_k, _p(logprob),
-        _p(entropy), _p(top_ids) if top_k else None, _p(top_lp) if top_k else None,
-        _stream(stream)))
+    top_ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
+    top_lp = torch.empty((N, top_k), dtype=torch.float32, device=dev)
+    if top_k:
+        pt, pp = top_ids.data_ptr(), top_lp.data_ptr()
+    rc = lib().moe_token_logprobs(pz, _FLOAT_TYPES[logits.dtype], _ld(logits), pi, N, V, top_k, pl,
+                                  entropy.data_ptr(), pt, pp, _stream(stream))
+    _check("moe_token_logprobs", rc)
     return TokenLogprobs(logprob, entropy, top_ids, top_lp)
 
 

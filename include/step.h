@@ -37,7 +37,7 @@ enum moe_q8_format {
  *   q = round(u * top / a),  scale = a / (top * rms),  top = 127 (int8) or 448 (e4m3)
  * so q * scale stands for r / rms * weight. Rounding is to nearest, ties to
  * even, of the exact quotient (u, a product of two bf16 values, is exact in
- * fp32; quotients next to a tie are decided in 64 bits).
+ * fp32; quotients next to a tie are compared with it exactly).
  *   x            bf16 [T][d], rows ldx elements apart (ldx >= d, multiple of 8)
  *   residual     bf16 [T][d] or NULL
  *   weight       bf16 [d]

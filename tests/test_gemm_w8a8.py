@@ -33,7 +33,8 @@ def exact(a, sa, w, sw):
 
 SHAPES = [(1, 1, 16, 0), (1, 4608, 2048, 0), (2, 100, 48, 16), (7, 333, 2048, 0), (8, 40001, 512, 0), (9, 65, 4096, 32), (17, 20011, 272, 0),
           (24, 33, 8192, 0), (32, 2048, 2048, 0), (33, 2048, 2048, 0), (33, 1, 16, 0), (64, 129, 144, 16), (65, 300, 1024, 0), (100, 40000, 256, 0),
-          (129, 4608, 2048, 0), (255, 127, 400, 0), (300, 5000, 1040, 0), (700, 8192, 640, 16), (1500, 4100, 2048, 0), (4097, 1029, 528, 0)]
+          (129, 4608, 2048, 0), (255, 127, 400, 0), (300, 5000, 1040, 0), (700, 8192, 640, 16), (1500, 4100, 2048, 0), (4097, 1029, 528, 0), (4000, 8100, 144, 0),
+          (8192, 4100, 1040, 0)]
 
 
 @gpu
