@@ -28,6 +28,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -210,7 +211,8 @@ struct CfgW8 {
   static constexpr int kACol = kAcc * BN;
   static constexpr int kOffB = 0;
   static constexpr int kOffQ = kSB * kBBytes;
-  static constexpr int kOffBar = kOffQ + kSQ * kQStage;
+  static constexpr int kOffScale = kOffQ + kSQ * kQStage;  // 32 token scales an epilogue warp
+  static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
   static constexpr int kBars = 2 * kSQ + kSA + kSB + kSD + 2 + 2 + 1;
   static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
   static_assert(kACol + kSA * (kKB / 2) <= 512, "tensor memory exceeded");
@@ -243,7 +245,7 @@ MOE_DEVINL void warp_arrive(uint64_t* bar) {
 // Roles: warp 0 streams the packed weights, warp 1 issues the MMAs, warp 2
 // streams the tokens' operand, warps 4-19 convert, warps 20-27 write out.
 // Tiles of 128 weight rows by BN tokens, weights fastest, one CTA an SM.
-template <int BN>
+template <int BN, bool F32>
 __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_constant__ W8Args args) {
   using C = CfgW8<BN>;
   const GemmW8Params& g = args.g;
@@ -346,37 +348,49 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16_f32(kTileN, BN);
-      uint32_t it = 0, itb = 0, tile = 0;
+      // Stage indices and phases are carried, not divided out of a counter, and
+      // descriptors are one add from a base: what this thread does between two
+      // k-blocks' MMAs is not hidden behind them when N is small (about 590 of
+      // 1020 cycles a k-block at 64 tokens before this).
+      const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem + C::kOffB));
+      uint32_t sa = 0, pa = 0, sb = 0, pb = 0, sd = 0, buf = 0, pacc = 1;
       bool alive = true;
-      for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x, ++tile) {
-        const uint32_t buf = tile % C::kAcc;
-        if (!mbar_wait(&acc_empty[buf], ((tile / C::kAcc) & 1) ^ 1, abort_flag, g.status, 64)) break;
+      for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
+        if (!mbar_wait(&acc_empty[buf], pacc, abort_flag, g.status, 64)) break;
         tc_fence_after();
-        for (int kb = 0; kb < KB && alive; ++kb, ++it) {
-          const int s = it % C::kSA;
-          if (!mbar_wait(&a_full[s], (it / C::kSA) & 1, abort_flag, g.status, 66)) {
+        const uint32_t d_tmem = tmem + buf * BN;
+        uint32_t accumulate = 0;
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&a_full[sa], pa, abort_flag, g.status, 66)) {
             alive = false;
             break;
           }
-          const uint32_t a_tmem = tmem + C::kACol + s * (kKB / 2);
+          const uint32_t a_tmem = tmem + C::kACol + sa * (kKB / 2);
 #pragma unroll
-          for (int h = 0; h < C::kBSteps; ++h, ++itb) {
-            const int sb = itb % C::kSB;
-            if (!mbar_wait(&b_full[sb], (itb / C::kSB) & 1, abort_flag, g.status, 65)) {
+          for (int h = 0; h < C::kBSteps; ++h) {
+            if (!mbar_wait(&b_full[sb], pb, abort_flag, g.status, 65)) {
               alive = false;
               break;
             }
             tc_fence_after();
-            const uint32_t b_addr = smem_u32(smem + C::kOffB + sb * C::kBBytes);
+            const uint64_t b_desc = b_desc0 + sb * (C::kBBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < C::kBK / 16; ++kk)
-              tc_mma_ts(tmem + buf * BN, a_tmem + (h * (C::kBK / 16) + kk) * 8,
-                        smem_desc_sw128(b_addr + (kk / 4) * (BN * 128) + (kk % 4) * 32), idesc, (kb | h | kk) != 0);
+            for (int kk = 0; kk < C::kBK / 16; ++kk) {
+              tc_mma_ts(d_tmem, a_tmem + (h * (C::kBK / 16) + kk) * 8,
+                        b_desc + (((kk / 4) * (BN * 128) + (kk % 4) * 32) >> 4), idesc, accumulate);
+              accumulate = 1;
+            }
+            if (++sb == C::kSB) sb = 0, pb ^= 1;
           }
-          if (alive) tc_commit(&done[it % C::kSD]);
+          if (!alive) break;
+          tc_commit(&done[sd]);
+          if (++sa == C::kSA) sa = 0, pa ^= 1;
+          if (++sd == C::kSD) sd = 0;
         }
         if (!alive) break;
         tc_commit(&acc_full[buf]);
+        if (++buf == C::kAcc) buf = 0, pacc ^= 1;
       }
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
       mbar_wait(drain, 0, abort_flag, g.status, 67);
@@ -423,6 +437,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
     // lanes of quarter warp % 4 = 32 weight rows; the two groups of four warps take half the tokens each
     const int quarter = warp & 3, group = (warp - kEpiWarp0) >> 2;
     constexpr int kCols = BN / 2;
+    using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    float4* scales = reinterpret_cast<float4*>(smem + C::kOffScale + (warp - kEpiWarp0) * 128);
     uint32_t tile = 0;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
       const uint32_t buf = tile % C::kAcc;
@@ -437,19 +453,38 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
         __syncwarp();  // (the stores of the chunk before part the lanes)
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c0, v);
-        const int t = t0 + c0;
-        const float as = t + lane < g.T ? __ldg(g.a_scale + t + lane) : 0.f;
+        const int t = t0 + c0, live = g.T - t;
+        reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
         tc_wait_ld();
         if (c0 + 32 == kCols) {  // the accumulator is in registers: the next tile may start
           tc_fence_before();
           warp_arrive(&acc_empty[buf]);
         }
-        const int live = min(32, g.T - t);
-        const int64_t at = (int64_t)t * g.ldo + n;
+        __syncwarp();
+        Out* dst = static_cast<Out*>(g.out) + (int64_t)t * g.ldo + n;
+        auto put = [&](uint32_t acc, float as) {
+          const float y = __uint_as_float(acc) * as * ws;
+          if constexpr (F32)
+            *dst = y;
+          else
+            *dst = __float2bfloat16_rn(y);
+          dst += g.ldo;
+        };
+        if (n < g.N) {  // one row of 32 outputs a store
+          if (live >= 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float y = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, as, i) * ws;
-          if (i < live && n < g.N) store_out(g.out, g.f32, at + (int64_t)i * g.ldo, y);
+            for (int i = 0; i < 8; ++i) {
+              const float4 as = scales[i];
+              put(v[4 * i], as.x);
+              put(v[4 * i + 1], as.y);
+              put(v[4 * i + 2], as.z);
+              put(v[4 * i + 3], as.w);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < live) put(v[i], reinterpret_cast<const float*>(scales)[i]);
+          }
         }
       }
     }
@@ -474,8 +509,8 @@ bool encode_2d(CUtensorMap* tm, CUtensorMapDataType type, int esize, const void*
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
+template <int BN, bool F32>
+cudaError_t many_launch_t(const GemmW8Params& p, int sms, cudaStream_t s) {
   using C = CfgW8<BN>;
   W8Args args;
   memset(&args, 0, sizeof args);
@@ -484,7 +519,7 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
       !encode_2d(&args.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.a16, p.T, p.K, 64, BN))
     return cudaErrorInvalidValue;
   static const cudaError_t smem_set =
-      cudaFuncSetAttribute(gemm_w8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      cudaFuncSetAttribute(gemm_w8_kernel<BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (smem_set != cudaSuccess) return smem_set;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -501,7 +536,11 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, units));
   cfg.blockDim = dim3(kManyThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  return cudaLaunchKernelEx(&cfg, gemm_w8_kernel<BN>, args);
+  return cudaLaunchKernelEx(&cfg, gemm_w8_kernel<BN, F32>, args);
+}
+template <int BN>
+cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
+  return p.f32 ? many_launch_t<BN, true>(p, sms, s) : many_launch_t<BN, false>(p, sms, s);
 }
 
 }  // namespace
