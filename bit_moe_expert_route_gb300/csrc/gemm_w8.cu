@@ -11,7 +11,7 @@
 //
 // Two kernels, by the number of tokens:
 //
-// Up to 32 tokens: bound by the weights' bytes. A block owns 16 M weight rows
+// Few tokens: bound by the weights' bytes. A block owns 16 M weight rows
 // and splits K over its 8 warps; a lane loads 16 consecutive codes of two
 // rows per m16n8k16 product quadruple (the order of k is free as long as both
 // operands agree, so the fragments need no shuffling), and the warps' sums
@@ -71,11 +71,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_f
   __shared__ float red[kFewWarps][8 * NT][kPitch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * M);
+  const int t0 = blockIdx.y * (8 * NT);  // the block's first token
   const int steps = (p.K + 63) / 64, per = (steps + kFewWarps - 1) / kFewWarps;
   const int s0 = warp * per, s1 = min(steps, s0 + per);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
   float acc[M][NT][4];
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_f
       wrow[m][h] = p.w + min(n0 + 16 * m + 8 * h + g, (int64_t)p.N - 1) * p.K;
   const int8_t* arow[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) arow[j] = p.a + (int64_t)min(8 * j + g, p.T - 1) * p.lda;
+  for (int j = 0; j < NT; ++j) arow[j] = p.a + (int64_t)min(t0 + 8 * j + g, p.T - 1) * p.lda;
 #pragma unroll 1
   for (int s = s0; s < s1; s += U) {
     uint4 wv[U][M][2];
@@ -136,13 +137,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_f
       for (int i = 0; i < 4; ++i) red[warp][8 * j + 2 * t + (i & 1)][16 * m + g + 8 * (i >> 1)] = acc[m][j][i];
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * M * 8 * NT; i += 32 * kFewWarps) {
-    const int r = i % (16 * M), c = i / (16 * M);
+    const int r = i % (16 * M), c = i / (16 * M), tok = t0 + c;
     const int64_t n = n0 + r;
-    if (c < p.T && n < p.N) {
+    if (tok < p.T && n < p.N) {
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += red[w][c][r];
-      store_out(p.out, p.f32, (int64_t)c * p.ldo + n, v * __ldg(p.a_scale + c) * __ldg(p.w_scale + n));
+      store_out(p.out, p.f32, (int64_t)tok * p.ldo + n, v * __ldg(p.a_scale + tok) * __ldg(p.w_scale + n));
     }
   }
 }
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_f
 template <int M, int NT>
 cudaError_t few_launch(const GemmW8Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.N + 16 * M - 1) / (16 * M)));
+  cfg.gridDim = dim3((unsigned)((p.N + 16 * M - 1) / (16 * M)), (unsigned)((p.T + 8 * NT - 1) / (8 * NT)));
   cfg.blockDim = dim3(32 * kFewWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -546,18 +547,26 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
-  if (p.T <= kW8FewTokens) {
+  // More than 32 tokens stay with the first kernel, 32 at a time, while its
+  // blocks of 16 weight rows fill the machine at most twice (once where K is
+  // short and a block has little to do): 64 tokens by 4608 x 2048 weights 7.9 us
+  // against 12.2, 64 by 2048 x 2048 4.6 against 12.2; past that the tensor
+  // memory kernel is ahead (128 by 4608 x 2048: 14.2 against 12.4).
+  const int64_t blocks = (p.N + 15) / 16 * (int64_t)((p.T + 31) / 32);
+  if (p.T <= kW8FewTokens || blocks <= (int64_t)sms * (p.K < 1024 ? 2 : 4)) {
     // more rows a block reuse the tokens' fragments; fewer fill the machine
     const int nt = (p.T + 7) / 8;
     if (nt <= 2 && p.N >= 64 * 4 * sms) return few_launch_nt<4>(p, s);
-    if (p.N >= 32 * 4 * sms) return few_launch_nt<2>(p, s);
+    if (p.T <= kW8FewTokens && p.N >= 32 * 4 * sms) return few_launch_nt<2>(p, s);
     return few_launch_nt<1>(p, s);
   }
-  // The token width whose waves cost least: cycles of a k-block's eight MMAs
-  // (at most 64 tokens cost as much as 128 nearly: the issue rate bounds them).
-  const int64_t MT = (p.N + kTileN - 1) / kTileN;
-  auto cost = [&](int bn, int cycles) { return (MT * ((p.T + bn - 1) / bn) + sms - 1) / sms * cycles; };
-  const int64_t c64 = cost(64, 576), c128 = cost(128, 608), c256 = cost(256, 1120);
+  // The token width whose waves cost least, by the measured time of a k-block
+  // (about 0.5, 0.56 and 0.72 us at 64, 128 and 256 tokens) and a tile's ends.
+  const int64_t MT = (p.N + kTileN - 1) / kTileN, kb = (p.K + kKB - 1) / kKB;
+  auto cost = [&](int bn, int64_t step, int64_t ends) {
+    return (MT * ((p.T + bn - 1) / bn) + sms - 1) / sms * (kb * step + ends);
+  };
+  const int64_t c64 = cost(64, 50, 50), c128 = cost(128, 56, 80), c256 = cost(256, 72, 150);
   if (c256 <= c128 && c256 <= c64) return many_launch<256>(p, sms, s);
   return c128 <= c64 ? many_launch<128>(p, sms, s) : many_launch<64>(p, sms, s);
 }
