@@ -296,14 +296,18 @@ struct PrefixParams {
   int B, P, S, Hq, Hkv, d;
   float scale_log2;          // scale * log2 e
   // the plan
+  int tc;                    // the prefix goes to prefix_tc_launch, 128 rows a block
   int row_warps, prefix_slice, prefix_splits, prefix_blocks, suffix_slice, suffix_splits;
+  int32_t* status;
   float* part_o;             // [prefix_splits + suffix_splits][B Hq][d]
   float2* part_ml;           // [prefix_splits + suffix_splits][B Hq]: reference (log2), sum
   uint16_t* out;             // bf16 [B][Hq][d]
 };
 bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d);
-// Fills the plan from the sizes (slices of whole 64-key tiles).
+// Fills the plan from the sizes (slices of whole key tiles).
 void prefix_plan(PrefixParams& p, int sms);
+// The prefix's partial states from tcgen05 products.
+cudaError_t prefix_tc_launch(const PrefixParams& p, cudaStream_t s);
 cudaError_t prefix_launch(const PrefixParams& p, cudaStream_t s);
 
 }  // namespace moe

@@ -17,7 +17,9 @@
 // the weights rounded to bf16 for the second product (their rounding, 2^-9
 // each, averages out over the positions; the sum l adds them unrounded). The
 // running maximum moves only when a score passes it by 2^8, which fp32 and
-// bf16 hold without loss, so the output is rarely rescaled.
+// bf16 hold without loss, so the output is rarely rescaled. (With more than 64
+// rows a KV head the prefix goes to prefix_tc.cu; the sequences' own positions
+// stay here.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,6 +31,7 @@ namespace {
 constexpr int kPfThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr float kLazyLog2 = 8.f;
+constexpr int kPrefixTcMin = 512;  // positions from which the tensor-memory kernel takes a prefix
 
 MOE_DEVINL float ex2(float x) {
   float r;
@@ -264,12 +267,19 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
 template <int D, int WM>
 __global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p) {
   extern __shared__ __align__(128) uint8_t pf_smem[];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // After the tensor-memory kernel (p.tc) these blocks run beside it: they
+  // start once all of its blocks have waited for what came before, need
+  // nothing that it writes, and wait for its end before their own, so that the
+  // merge finds both.
+  const bool beside = p.tc != 0;
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   const int G = p.Hq / p.Hkv, R = p.B * G;
+  const int prefix_blocks = beside ? 0 : p.prefix_blocks;
+  if (!beside && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   PfItem it;
   int i = blockIdx.x;
-  if (i < p.prefix_blocks) {
+  if (i < prefix_blocks) {
     it.h = i % p.Hkv;
     i /= p.Hkv;
     const int tiles = (R + 16 * WM - 1) / (16 * WM), tile = i % tiles, split = i / tiles;
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p
     it.slot = split;
     attend<D, WM>(p, it, pf_smem);
   } else {
-    i -= p.prefix_blocks;
+    i -= prefix_blocks;
     it.h = i % p.Hkv;
     i /= p.Hkv;
     const int b = i % p.B, split = i / p.B;
@@ -301,10 +311,11 @@ __global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p
     if (it.k0 == it.k1) {  // nothing here: only the state has to say so
       for (int r = threadIdx.x; r < G; r += kPfThreads)
         p.part_ml[(int64_t)it.slot * p.B * p.Hq + (int64_t)b * p.Hq + it.h * G + r] = make_float2(-INFINITY, 0.f);
-      return;
+    } else {
+      attend<D, 1>(p, it, pf_smem);
     }
-    attend<D, 1>(p, it, pf_smem);
   }
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One query row a block: merges its partial states.
@@ -364,7 +375,11 @@ cudaError_t prefix_launch_t(const PrefixParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int64_t blocks = p.prefix_blocks + (int64_t)p.suffix_splits * p.B * p.Hkv;
+  if (p.tc) {
+    const cudaError_t err = prefix_tc_launch(p, s);
+    if (err != cudaSuccess) return err;
+  }
+  const int64_t blocks = (p.tc ? 0 : p.prefix_blocks) + (int64_t)p.suffix_splits * p.B * p.Hkv;
   if (blocks > 0) {
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kPfThreads);
@@ -398,19 +413,22 @@ void prefix_plan(PrefixParams& p, int sms) {
   const int R = p.B * (p.Hq / p.Hkv);
   const int per_sm = p.d == 256 ? 1 : p.d == 128 ? 2 : 4;
   const int64_t room = (int64_t)std::min(sms, kPrefixMaxSms) * per_sm;
-  // 16, 32 or 64 rows a block: the fewest row tiles, so that a slice is read
-  // as few times as its rows allow
+  // More than 64 rows a KV head are bound by the products: tensor memory, 128
+  // rows a block, one block an SM. Else 16, 32 or 64 rows a block, the fewest
+  // row tiles, so that a slice is read as few times as its rows allow.
+  p.tc = R > 64 && p.P >= kPrefixTcMin;
   p.row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-  const int tiles = (R + 16 * p.row_warps - 1) / (16 * p.row_warps);
-  // one wave of blocks over the prefix, slices of whole 64-key tiles
-  auto slices = [&](int len, int64_t others, int& slice, int& splits) {
-    const int64_t kt = (len + kTileKeys - 1) / kTileKeys;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kt, room / std::max<int64_t>(1, others)));
-    slice = (int)((kt + want - 1) / want) * kTileKeys;
-    splits = len ? (len + slice - 1) / slice : 0;
+  const int tile_rows = p.tc ? 128 : 16 * p.row_warps, tiles = (R + tile_rows - 1) / tile_rows;
+  // one wave of blocks over the prefix, slices of whole key tiles
+  auto slices = [&](int len, int64_t blocks, int64_t others, int keys, int& slice, int& splits) {
+    const int64_t kt = ((int64_t)len + keys - 1) / keys;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kt, blocks / std::max<int64_t>(1, others)));
+    slice = (int)((kt + want - 1) / want) * keys;
+    splits = len ? (int)(((int64_t)len + slice - 1) / slice) : 0;
   };
-  slices(p.P, (int64_t)p.Hkv * tiles, p.prefix_slice, p.prefix_splits);
-  slices(p.S, (int64_t)p.Hkv * p.B, p.suffix_slice, p.suffix_splits);
+  slices(p.P, p.tc ? std::min(sms, kPrefixMaxSms) : room, (int64_t)p.Hkv * tiles, p.tc && p.d != 256 ? 128 : kTileKeys,
+         p.prefix_slice, p.prefix_splits);
+  slices(p.S, room, (int64_t)p.Hkv * p.B, kTileKeys, p.suffix_slice, p.suffix_splits);
   p.prefix_blocks = p.prefix_splits * p.Hkv * tiles;
 }
 

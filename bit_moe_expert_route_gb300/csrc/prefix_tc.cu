@@ -1,0 +1,352 @@
+// Attention over a shared prefix for many query rows (more than 64 a KV head):
+// the partial states of prefix.cu from tcgen05 products.
+//
+// A CTA takes one KV head, 128 query rows and one slice of the prefix. Per tile
+// of KT keys:  S = Q K^T (both in shared memory) into tensor memory; softmax
+// weights P = 2^(scale S - m) from there into tensor memory as bf16; O += P V
+// with P as the MMA's A operand and O kept in tensor memory through the slice.
+// The products of tile i + 1's scores are issued before tile i's weights are
+// waited for, so the tensor core works while the softmax warps do.
+//
+// K and V tiles come by TMA into one ring of slots in the order in which the
+// products use them (K0 K1 V0 K2 V1 ...); V is read as it lies (MN-major
+// operand, no transpose). Every query row of a KV head's sequences shares
+// these tiles: what bounds the kernel at head size 256 is the rate at which an
+// SM takes K and V in from L2 (64 KB for 64 keys, against 1312 cycles of MMAs).
+//
+// The reference m moves only when a score passes it by 2^8; then the warp waits
+// for the products before and rescales its rows of O in tensor memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTcRows = 128;
+constexpr int kTcThreads = 256;  // warp 0 TMA, warp 1 MMA, warps 4-7 softmax
+constexpr float kLazyLog2 = 8.f;
+
+MOE_DEVINL float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int D>
+struct TcCfg {
+  static constexpr int KT = D == 256 ? 64 : 128;    // keys a tile
+  static constexpr int kSlot = KT * D * 2;          // K or V of a tile
+  static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
+  static constexpr int kQ = kTcRows * D * 2;
+  static constexpr int kOffSlots = kQ;
+  static constexpr int kOffBar = kOffSlots + kSlots * kSlot;
+  static constexpr int kBars = 2 * kSlots + 1 + 2 + 2 + 2 + 1;
+  static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
+  // tensor memory: O, two score buffers, two weight buffers (two bf16 a column)
+  static constexpr int kColS = D;
+  static constexpr int kColP = D + 2 * KT;
+  static_assert(kColP + KT <= 512, "tensor memory exceeded");
+  static_assert(kSmem <= 232448, "shared memory exceeded");
+};
+
+struct TcArgs {
+  CUtensorMap tm_k, tm_v;  // [P][Hkv d], box 64 x KT
+  PrefixParams p;
+};
+
+// A wait by a whole warp; its lanes are together again after it.
+MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
+}
+MOE_DEVINL void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of N
+// a 128-byte row, one row a key; blocks of 64 N `block` bytes apart, groups of
+// 8 keys 1024 bytes apart.
+MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ TcArgs args) {
+  using C = TcCfg<D>;
+  constexpr int KT = C::KT, NS = C::kSlots;
+  const PrefixParams& p = args.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] a slot's tile has landed
+  uint64_t* empty = full + NS;                                      // [NS] its products are done
+  uint64_t* q_full = empty + NS;                                    // [1]
+  uint64_t* s_full = q_full + 1;                                    // [2] scores are complete
+  uint64_t* p_full = s_full + 2;                                    // [2] weights are written
+  uint64_t* pv_done = p_full + 2;                                   // [2] their product is complete
+  uint64_t* drain = pv_done + 2;                                    // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, R = p.B * G, tiles = (R + kTcRows - 1) / kTcRows;
+  const int h = blockIdx.x % p.Hkv, tile = (blockIdx.x / p.Hkv) % tiles, split = blockIdx.x / (p.Hkv * tiles);
+  const int row0 = tile * kTcRows, k0 = split * p.prefix_slice, k1 = min(p.P, k0 + p.prefix_slice);
+  const int n = (k1 - k0 + KT - 1) / KT;  // key tiles, at least 1
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&args.tm_k);
+    tma_prefetch_desc(&args.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t policy = l2_policy_evict_last();  // the other row tiles read the same tiles
+      int slot = 0, phase = 1, loads = 0;
+      bool alive = true;
+      auto load = [&](const CUtensorMap* tm, int key) {
+        if (!mbar_wait(&empty[slot], phase, abort_flag, p.status, 81)) return false;
+        mbar_arrive_expect_tx(&full[slot], C::kSlot);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)  // positions past the prefix's end read as zeros
+          tma_load_2d(smem + C::kOffSlots + slot * C::kSlot + c * (KT * 128), tm, h * D + c * 64, key, &full[slot], policy);
+        ++loads;
+        if (++slot == NS) slot = 0, phase ^= 1;
+        return true;
+      };
+      alive = load(&args.tm_k, k0);
+      for (int i = 0; i < n && alive; ++i) {
+        if (i + 1 < n) alive = load(&args.tm_k, k0 + (i + 1) * KT);
+        if (alive) alive = load(&args.tm_v, k0 + i * KT);
+      }
+      // every load lands before the CTA ends
+      for (int j = loads > NS ? loads - NS : 0; j < loads; ++j)
+        mbar_wait(&full[j % NS], (j / NS) & 1, abort_flag, p.status, 82);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kTcRows, KT);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kTcRows, D) | (1u << 16);  // B (V) is MN-major
+      const uint32_t slots = smem_u32(smem + C::kOffSlots);
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem));
+      int slot = 0, phase = 0;
+      auto next = [&]() {
+        if (++slot == NS) slot = 0, phase ^= 1;
+      };
+      auto scores = [&](int i) {
+        if (!mbar_wait(&full[slot], phase, abort_flag, p.status, 83)) return false;
+        tc_fence_after();
+        const uint64_t k_desc = smem_desc_sw128(slots + slot * C::kSlot);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(tmem + C::kColS + (i & 1) * KT, q_desc + ((c * (kTcRows * 128) + kk * 32) >> 4),
+                        k_desc + ((c * (KT * 128) + kk * 32) >> 4), idesc_s, (c | kk) != 0);
+        tc_commit(&empty[slot]);
+        tc_commit(&s_full[i & 1]);
+        next();
+        return true;
+      };
+      bool alive = mbar_wait(q_full, 0, abort_flag, p.status, 84) && scores(0);
+      for (int i = 0; i < n && alive; ++i) {
+        if (i + 1 < n && !scores(i + 1)) break;
+        if (!mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 85) ||
+            !mbar_wait(&full[slot], phase, abort_flag, p.status, 86))
+          break;
+        tc_fence_after();
+        const uint64_t v_desc = smem_desc_mn(slots + slot * C::kSlot, KT * 128);
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          tc_mma_ts(tmem, tmem + C::kColP + (i & 1) * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o, (i | kk) != 0);
+        tc_commit(&empty[slot]);
+        tc_commit(&pv_done[i & 1]);
+        next();
+      }
+      tc_commit(drain);  // all MMAs complete before tensor memory is freed
+      mbar_wait(drain, 0, abort_flag, p.status, 87);
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, r = quarter * 32 + lane;  // this thread's row of the tile
+    auto query_row = [&](int row) { return (int64_t)(row / G) * p.Hq + h * G + row % G; };  // of B Hq
+    {  // the queries into the swizzled K-major operand; rows past the end as zeros
+      constexpr int kChunks = D / 8;
+      for (int i = threadIdx.x - 128; i < kTcRows * kChunks; i += 128) {
+        const int row = i / kChunks, c = i % kChunks;
+        const uint4 v = row0 + row < R ? __ldg(reinterpret_cast<const uint4*>(p.q + query_row(row0 + row) * D + c * 8))
+                                       : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + (c / 8) * (kTcRows * 128) + sw128_offset(row, c % 8)) = v;
+      }
+      fence_proxy_async_smem();
+      warp_arrive(q_full);
+    }
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    float m = -INFINITY, l = 0.f;
+    bool alive = true;
+    for (int i = 0; i < n; ++i) {
+      if (!(alive = warp_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 88))) break;
+      tc_fence_after();
+      uint32_t s[KT / 32][32];
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(tmem + lanes + C::kColS + (i & 1) * KT + c * 32, s[c]);
+      tc_wait_ld();
+      const int left = k1 - (k0 + i * KT);  // keys of this tile inside the slice
+      if (left < KT) {
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c * 32 + j >= left) s[c][j] = 0xFF800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[c][j]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
+        const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.f : ex2(m - nm);  // (m -infinity: 0)
+        l *= f;
+        m = nm;
+        if (i > 0) {
+          // O is whole once the product before is complete (earlier ones are:
+          // this tile's scores were issued after them)
+          if (!(alive = warp_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.status, 89))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tmem + lanes + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st_32x32b_x16(tmem + lanes + c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float2 sc = make_float2(p.scale_log2, p.scale_log2), nr = make_float2(-ref, -ref);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), sc, nr);
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          sum = __fadd2_rn(sum, e);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
+          w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tmem_st_32x32b_x16(tmem + lanes + C::kColP + (i & 1) * (KT / 2) + c * 16, w);
+      }
+      l += sum.x + sum.y;
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(&p_full[i & 1]);
+    }
+    // the slice's state: every product is complete with the last one
+    if (alive && warp_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.status, 90)) {
+      tc_fence_after();
+      const bool mine = row0 + r < R;
+      const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);
+      if (mine) p.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        __syncwarp();
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tmem + lanes + c, o);
+        tc_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(p.part_o + at * D + c + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+    }
+  }
+  __syncwarp();  // the single-lane roles join their warps
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+bool encode_cache(CUtensorMap* tm, const uint16_t* base, const PrefixParams& p, int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.Hkv * p.d, (cuuint64_t)p.P};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.ld_prefix * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t prefix_tc_launch_t(const PrefixParams& p, cudaStream_t s) {
+  using C = TcCfg<D>;
+  TcArgs args;
+  memset(&args, 0, sizeof args);
+  args.p = p;
+  if (!encode_cache(&args.tm_k, p.kp, p, C::KT) || !encode_cache(&args.tm_v, p.vp, p, C::KT)) return cudaErrorInvalidValue;
+  static const cudaError_t smem_set =
+      cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (smem_set != cudaSuccess) return smem_set;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.prefix_blocks);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_tc_kernel<D>, args);
+}
+
+}  // namespace
+
+cudaError_t prefix_tc_launch(const PrefixParams& p, cudaStream_t s) {
+  if (p.d == 256) return prefix_tc_launch_t<256>(p, s);
+  if (p.d == 128) return prefix_tc_launch_t<128>(p, s);
+  return prefix_tc_launch_t<64>(p, s);
+}
+
+}  // namespace moe

@@ -43,10 +43,11 @@ int device_sms() {
 // Lays the partial states out in the workspace; returns its bytes.
 size_t prefix_carve(moe::PrefixParams& p, void* ws) {
   const size_t states = (size_t)(p.prefix_splits + p.suffix_splits) * p.B * p.Hq;
-  p.part_ml = static_cast<float2*>(ws);
-  const size_t off = (states * sizeof(float2) + 255) / 256 * 256;
+  p.status = static_cast<int32_t*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + 256);
+  const size_t off = 256 + (states * sizeof(float2) + 255) / 256 * 256;
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off);
-  return off + states * p.d * sizeof(float) + 256;
+  return off + states * p.d * sizeof(float);
 }
 
 }  // namespace

@@ -66,15 +66,16 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  *   out                 bf16 [B][n_q_heads][d]; zeros for a sequence without any
  *                       position (P == 0 and len[b] == 0)
  *   ws                  256-byte aligned, >= moe_prefix_attention_workspace_bytes
- *                       (no initialisation needed)
+ *                       (no initialisation needed), holds the status word
  * All pointers but lens (4 bytes) 16-byte aligned, strides multiples of 8
  * elements. 0 <= B <= 65535 (0 launches nothing), P and S up to 2^28, d in {64,
  * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a
  * KV head. Scores and softmax in fp32; the softmax weights are rounded to bf16
- * before they multiply the values (fp32 sums). Two launches: partial states
- * over slices of the prefix and of the sequences' own positions, then their
- * merge in a fixed order. Each is a programmatic dependent of the launch before
- * it on the stream.
+ * before they multiply the values (fp32 sums). Two or three launches: partial
+ * states over slices of the prefix and of the sequences' own positions (from
+ * more than 64 query rows a KV head the prefix has a launch of its own), then
+ * their merge in a fixed order. Each is a programmatic dependent of the launch
+ * before it on the stream.
  */
 size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, int n_kv_heads, int d);
 int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,

@@ -56,7 +56,10 @@ def check(got, o, mag):
 SHAPES = [(1, 1, 1, 2, 2, 64), (1, 0, 5, 16, 2, 256), (3, 64, 0, 16, 2, 128), (2, 700, 16, 16, 2, 256), (1, 65, 1, 4, 4, 64),
           (5, 129, 33, 12, 4, 128), (8, 8192, 200, 32, 8, 128), (9, 1000, 70, 16, 1, 64), (17, 333, 130, 8, 8, 64), (64, 2049, 65, 16, 2, 256),
           (33, 500, 9, 6, 2, 256), (2, 30000, 3, 3, 1, 128), (1, 20000, 3000, 16, 2, 256), (40, 0, 300, 8, 1, 128), (150, 90, 20, 16, 2, 64),
-          (4, 4096, 64, 16, 1, 256)]
+          (4, 4096, 64, 16, 1, 256),
+          # more than 64 rows a KV head and at least 512 shared positions: the tensor-memory kernel
+          (70, 512, 0, 3, 3, 64), (16, 513, 3, 16, 2, 128), (40, 1000, 30, 8, 2, 128), (13, 700, 10, 16, 1, 256), (20, 4099, 10, 12, 2, 256),
+          (65, 9000, 70, 2, 2, 128), (100, 30011, 9, 10, 1, 64), (64, 20000, 100, 16, 2, 256)]
 
 
 @gpu
@@ -64,7 +67,9 @@ SHAPES = [(1, 1, 1, 2, 2, 64), (1, 0, 5, 16, 2, 256), (3, 64, 0, 16, 2, 128), (2
 def test_matches_64_bits(B, P, S, Hq, Hkv, d):
     from bit_moe_expert_route_gb300 import ops
     x = inputs(B, P, S, Hq, Hkv, d, B + P + S + d)
-    got = ops.prefix_attention(*x)
+    ws = torch.empty(ops.lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    got = ops.prefix_attention(*x, ws=ws)
+    assert ops.device_status(ws) == 0
     check(got, *expected(*x))
     assert torch.equal(ops.prefix_attention(*x), got)  # the merge order is fixed
 
@@ -104,6 +109,12 @@ def test_strided_caches_and_scale(d):
     suf = torch.randn(B, S + 30, 2, Hkv, d, device="cuda").bfloat16()
     args = (q, pre[:, 0], pre[:, 1], suf[:, :S, 0], suf[:, :S, 1], ln)
     check(ops.prefix_attention(*args, scale=0.25), *expected(*args, scale=0.25))
+    B, P = 24, 900  # rows and positions enough for the tensor-memory kernel
+    q, _, _, _, _, ln = inputs(B, P, S, Hq, Hkv, d, 3)
+    pre = torch.randn(P, 2, Hkv, d, device="cuda").bfloat16()
+    suf = torch.randn(B, S + 30, 2, Hkv, d, device="cuda").bfloat16()
+    args = (q, pre[:, 0], pre[:, 1], suf[:, :S, 0], suf[:, :S, 1], ln)
+    check(ops.prefix_attention(*args, scale=0.25), *expected(*args, scale=0.25))
 
 
 @gpu
@@ -116,6 +127,20 @@ def test_late_large_scores_move_the_reference():
         kp[j, 0] = (c * u).bfloat16()
     ks[2, 80, 0] = (61.0 * u).bfloat16()
     kp[:, 1] -= 30 * q[1, 9].bfloat16() / 20
+    check(ops.prefix_attention(q, kp, vp, ks, vs, ln), *expected(q, kp, vp, ks, vs, ln))
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_late_large_scores_move_the_reference_of_many_rows(d):
+    """As above with rows enough for the tensor-memory kernel: its output is rescaled
+    where it lies, for some rows in some tiles."""
+    from bit_moe_expert_route_gb300 import ops
+    q, kp, vp, ks, vs, ln = inputs(40, 3001, 20, 16, 2, d, 4, [20] * 40)
+    for b, h, step in ((2, 3, 0), (17, 9, 1), (39, 15, 0)):
+        u = q[b, h].float() / q[b, h].float().norm()
+        for j, c in ((100, 20.0), (700, 28.0), (1500, 40.0), (2900, 60.0), (2901, 60.5)):
+            kp[j + step * 130, h // 8] = (c * u).bfloat16()
     check(ops.prefix_attention(q, kp, vp, ks, vs, ln), *expected(q, kp, vp, ks, vs, ln))
 
 
