@@ -286,7 +286,8 @@ struct GemmW8Params {
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- attention over a shared prefix
-constexpr int kPrefixMaxSms = 160;  // bounds the slices, and so the workspace
+constexpr int kPrefixMaxSms = 160;     // bounds the slices, and so the workspace
+constexpr int kPrefixMaxStates = 512;  // slices of the prefix, and of a sequence's own positions
 struct PrefixParams {
   const uint16_t* q;         // [B][Hq][d]
   const uint16_t *kp, *vp;   // prefix, positions ld_prefix apart

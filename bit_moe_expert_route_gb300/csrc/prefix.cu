@@ -318,43 +318,70 @@ __global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p
   if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// One query row a block: merges its partial states.
+// One query row a block: merges its partial states. First the weights of the
+// states (each thread some of them), then the weighted outputs, by groups of
+// D / 4 threads over every kGroups-th state.
+constexpr int kMaxStates = 2 * kPrefixMaxStates;
 template <int D>
 __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams p) {
   constexpr int kCols = D / 4, kGroups = 256 / kCols;
   __shared__ float4 acc_s[kGroups][kCols];
-  __shared__ float l_s[kGroups];
+  __shared__ float w_s[kMaxStates], red[2][8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.Hq;
-  const int c = threadIdx.x % kCols, grp = threadIdx.x / kCols, n = p.prefix_splits + p.suffix_splits;
+  const int tid = threadIdx.x, c = tid % kCols, grp = tid / kCols, n = p.prefix_splits + p.suffix_splits;
+  constexpr int kPer = (kMaxStates + 255) / 256;
+  float2 ml[kPer];
   float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, p.part_ml[s * rows + row].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = tid + i * 256;
+    ml[i] = s < n ? p.part_ml[s * rows + row] : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, ml[i].x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w]);
   float L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = tid + i * 256;
+    const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - M);
+    if (s < n) w_s[s] = f;
+    L = fmaf(f, ml[i].y, L);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if ((tid & 31) == 0) red[1][tid >> 5] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) L += red[1][w];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = grp; s < n; s += kGroups) {
-    const float2 ml = p.part_ml[s * rows + row];
-    if (ml.x == -INFINITY) continue;  // (its output was not written)
-    const float f = ex2(ml.x - M);
+    const float f = w_s[s];
+    if (f == 0.f) continue;  // (a state without positions has no output)
     const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * rows + row) * D + c * 4);
-    L += f * ml.y;
     acc.x = fmaf(f, v.x, acc.x);
     acc.y = fmaf(f, v.y, acc.y);
     acc.z = fmaf(f, v.z, acc.z);
     acc.w = fmaf(f, v.w, acc.w);
   }
   acc_s[grp][c] = acc;
-  if (c == 0) l_s[grp] = L;
   __syncthreads();
   if (grp == 0) {
+#pragma unroll
     for (int k = 1; k < kGroups; ++k) {
       const float4 v = acc_s[k][c];
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
       acc.w += v.w;
-      L += l_s[k];
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;  // no position at all: zeros
     *reinterpret_cast<uint2*>(p.out + row * D + c * 4) =
@@ -419,16 +446,18 @@ void prefix_plan(PrefixParams& p, int sms) {
   p.tc = R > 64 && p.P >= kPrefixTcMin;
   p.row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   const int tile_rows = p.tc ? 128 : 16 * p.row_warps, tiles = (R + tile_rows - 1) / tile_rows;
-  // one wave of blocks over the prefix, slices of whole key tiles
-  auto slices = [&](int len, int64_t blocks, int64_t others, int keys, int& slice, int& splits) {
+  // slices of whole key tiles, `least` of them or more, at most `blocks` blocks
+  auto slices = [&](int len, int64_t blocks, int64_t others, int keys, int least, int& slice, int& splits) {
     const int64_t kt = ((int64_t)len + keys - 1) / keys;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kt, blocks / std::max<int64_t>(1, others)));
+    int64_t want = std::min<int64_t>((kt + least - 1) / least, std::max<int64_t>(1, blocks / std::max<int64_t>(1, others)));
+    want = std::max<int64_t>(1, std::min<int64_t>(want, kPrefixMaxStates));
     slice = (int)((kt + want - 1) / want) * keys;
     splits = len ? (int)(((int64_t)len + slice - 1) / slice) : 0;
   };
-  slices(p.P, p.tc ? std::min(sms, kPrefixMaxSms) : room, (int64_t)p.Hkv * tiles, p.tc && p.d != 256 ? 128 : kTileKeys,
+  // the prefix in one wave of blocks; the sequences' own positions, ragged, in up to four of shorter ones
+  slices(p.P, p.tc ? std::min(sms, kPrefixMaxSms) : room, (int64_t)p.Hkv * tiles, p.tc && p.d != 256 ? 128 : kTileKeys, 1,
          p.prefix_slice, p.prefix_splits);
-  slices(p.S, room, (int64_t)p.Hkv * p.B, kTileKeys, p.suffix_slice, p.suffix_splits);
+  slices(p.S, 4 * room, (int64_t)p.Hkv * p.B, kTileKeys, 2, p.suffix_slice, p.suffix_splits);
   p.prefix_blocks = p.prefix_splits * p.Hkv * tiles;
 }
 

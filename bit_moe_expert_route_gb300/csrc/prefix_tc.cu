@@ -82,6 +82,12 @@ MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
   return d;
 }
 
+constexpr int kAhead = 6;  // tiles from which L2 is asked before the ring loads them
+MOE_DEVINL void prefetch_tile(const void* desc, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(desc)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ TcArgs args) {
   using C = TcCfg<D>;
@@ -148,8 +154,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         if (++slot == NS) slot = 0, phase ^= 1;
         return true;
       };
+      // The ring holds two and a half tiles, less than HBM's latency: tiles are
+      // asked into L2 ahead of it, each by one of the row tiles' CTAs that read it.
+      auto prefetch = [&](int i) {
+        if (i < n && i % tiles == tile) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            prefetch_tile(&args.tm_k, h * D + c * 64, k0 + i * KT);
+            prefetch_tile(&args.tm_v, h * D + c * 64, k0 + i * KT);
+          }
+        }
+      };
+      for (int i = 0; i < kAhead; ++i) prefetch(i);
       alive = load(&args.tm_k, k0);
       for (int i = 0; i < n && alive; ++i) {
+        prefetch(i + kAhead);
         if (i + 1 < n) alive = load(&args.tm_k, k0 + (i + 1) * KT);
         if (alive) alive = load(&args.tm_v, k0 + i * KT);
       }
