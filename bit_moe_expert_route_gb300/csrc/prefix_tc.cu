@@ -52,6 +52,7 @@ struct TcCfg {
   static constexpr int kColP = D + 2 * KT;
   static_assert(kColP + KT <= 512, "tensor memory exceeded");
   static_assert(kSmem <= 232448, "shared memory exceeded");
+  static_assert(kTcRows * (D * 4 + 16) <= kSlots * kSlot, "the output's rows do not fit the ring");
 };
 
 struct TcArgs {
@@ -224,12 +225,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     auto query_row = [&](int row) { return (int64_t)(row / G) * p.Hq + h * G + row % G; };  // of B Hq
     {  // the queries into the swizzled K-major operand; rows past the end as zeros
       constexpr int kChunks = D / 8;
-      for (int i = threadIdx.x - 128; i < kTcRows * kChunks; i += 128) {
-        const int row = i / kChunks, c = i % kChunks;
-        const uint4 v = row0 + row < R ? __ldg(reinterpret_cast<const uint4*>(p.q + query_row(row0 + row) * D + c * 8))
-                                       : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + (c / 8) * (kTcRows * 128) + sw128_offset(row, c % 8)) = v;
+#pragma unroll 4
+      for (int k = 0; k < kChunks; ++k) {  // all in flight at once
+        const int i = threadIdx.x - 128 + k * 128, row = i / kChunks, c = i % kChunks;
+        const bool in = row0 + row < R;
+        cp_async_16(smem_u32(smem + (c / 8) * (kTcRows * 128) + sw128_offset(row, c % 8)),
+                    p.q + (in ? query_row(row0 + row) * D + c * 8 : 0), in ? 16u : 0u);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       warp_arrive(q_full);
     }
@@ -304,17 +308,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       const bool mine = row0 + r < R;
       const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);
       if (mine) p.part_ml[at] = make_float2(m, l);
+      // through shared memory (the ring is free: every product is complete), so
+      // that a row goes out as one copy; rows 16 bytes further apart than they
+      // are long keep eight lanes' stores in different banks
+      float* out = reinterpret_cast<float*>(smem + C::kOffSlots + r * (D * 4 + 16));
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        __syncwarp();
         uint32_t o[32];
         tmem_ld_32x32b_x32(tmem + lanes + c, o);
         tc_wait_ld();
-        if (mine) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(p.part_o + at * D + c + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        }
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(out + c + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      }
+      fence_proxy_async_smem();
+      if (mine) {
+        bulk_store(p.part_o + at * D, out, D * 4);
+        bulk_commit();
+        bulk_wait_all();  // (before the CTA's shared memory goes)
       }
     }
   }
