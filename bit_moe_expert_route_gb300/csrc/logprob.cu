@@ -141,15 +141,23 @@ MOE_DEVINL uint4 load_vec(const void* row, int64_t first, int V) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The vector's largest element (NaN if one is).
-template <bool F32>
-MOE_DEVINL float largest(const uint4& v) {
+constexpr int kUnroll = 4;  // vectors a thread holds at a time
+
+// The largest element of the thread's vectors (NaN if one is).
+template <bool F32, int N>
+MOE_DEVINL float largest(const uint4* v) {
   if constexpr (F32) {
-    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
-                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    float m = __uint_as_float(v[0].x);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      m = max_nan(max_nan(m, max_nan(__uint_as_float(v[i].x), __uint_as_float(v[i].y))),
+                  max_nan(__uint_as_float(v[i].z), __uint_as_float(v[i].w)));
+    return m;
   } else {
-    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3]));
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(v);
+    __nv_bfloat162 m = b[0];
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i) m = __hmax2_nan(m, b[i]);
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
     return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
   }
@@ -174,28 +182,42 @@ MOE_DEVINL void distances(const uint4& v, float nref, float2 (&d)[kVecElems<F32>
   }
 }
 
+// Adds the thread's vectors, whose largest element is m.
 template <bool F32>
-MOE_DEVINL void add_vec(Sums& s, const uint4& v, float vmax) {
+MOE_DEVINL void add_vecs(Sums& s, const uint4 (&v)[kUnroll], float m) {
   constexpr int E = kVecElems<F32>;
-  if (vmax > s.ref + kLazy) rebase(s, vmax);  // (+infinity ends as NaN, as it should)
-  float2 d[E / 2], S = make_float2(0.f, 0.f), U = make_float2(0.f, 0.f);
-  distances<F32>(v, -s.ref, d);
+  s.top = max_nan(s.top, m);
+  if (m > s.ref + kLazy) rebase(s, m);  // (+infinity ends as NaN, as it should)
   const float2 c = make_float2(kLog2e, kLog2e);
+  float2 S[2] = {}, U[2] = {};
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    const float2 x = __fmul2_rn(d[i], c);
-    const float2 e = make_float2(ex2(x.x), ex2(x.y));
-    S = __fadd2_rn(S, e);
-    U = __ffma2_rn(e, d[i], U);
-  }
-  s.S += S.x + S.y;
-  float u = U.x + U.y;
-  if (u != u) {  // -infinity among them (0 * infinity): its weight is 0, and so is 0 * (a finite distance)
-    u = 0.f;
+  for (int k = 0; k < kUnroll; ++k) {
+    float2 d[E / 2];
+    distances<F32>(v[k], -s.ref, d);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-      u = fmaf(ex2(d[i].x * kLog2e), max_nan(d[i].x, kLowest), u);
-      u = fmaf(ex2(d[i].y * kLog2e), max_nan(d[i].y, kLowest), u);
+      const float2 x = __fmul2_rn(d[i], c);
+      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      S[i & 1] = __fadd2_rn(S[i & 1], e);
+      U[i & 1] = __ffma2_rn(e, d[i], U[i & 1]);
+    }
+  }
+  s.S += (S[0].x + S[0].y) + (S[1].x + S[1].y);
+  float u = (U[0].x + U[0].y) + (U[1].x + U[1].y);
+  if (u != u) {  // -infinity among them (0 * infinity): its weight is 0, and so is 0 * (a finite distance)
+    u = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < kUnroll; ++k) {
+      uint4 w = v[0];
+#pragma unroll
+      for (int q = 1; q < kUnroll; ++q) w = q == k ? v[q] : w;
+      float2 d[E / 2];
+      distances<F32>(w, -s.ref, d);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        u = fmaf(ex2(d[i].x * kLog2e), max_nan(d[i].x, kLowest), u);
+        u = fmaf(ex2(d[i].y * kLog2e), max_nan(d[i].y, kLowest), u);
+      }
     }
   }
   s.U += u;
@@ -235,9 +257,8 @@ MOE_DEVINL float remote_f32(uint32_t a) {
 }
 
 template <bool F32, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobParams p) {
   constexpr int E = kVecElems<F32>;
-  constexpr int kUnroll = 4;  // vectors a thread loads before it uses them
   __shared__ LpShared sh;
   uint32_t rank, ranks;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -258,12 +279,21 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   s.U = 0.f;
   s.top = -INFINITY;
   uint64_t mine = 0;  // this lane's entry of the warp's list, 0 = none
-  uint32_t bar = 0;   // the rank that an element has to reach
+  uint32_t bar = 0;   // the rank that an element has to reach, and its value
+  float bar_z = -INFINITY;
+  // vectors [in0, in1) lie inside the row: a pass of only those is plain loads
+  const int in0 = lead ? 1 : 0, in1 = (lead + p.V) / E;
+  const uint4* vecs = reinterpret_cast<const uint4*>(base - lead * (F32 ? 4 : 2));
   auto load = [&](int v, uint4 (&w)[kUnroll]) {
+    if (v >= in0 && v + kUnroll * kLpThreads <= min(v1, in1)) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int vi = v + i * kLpThreads + tid;
-      w[i] = vi < v1 ? load_vec<F32>(base, (int64_t)vi * E - lead, p.V) : none_vec<F32>();
+      for (int i = 0; i < kUnroll; ++i) w[i] = __ldg(vecs + v + tid + i * kLpThreads);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int vi = v + i * kLpThreads + tid;
+        w[i] = vi < v1 ? load_vec<F32>(base, (int64_t)vi * E - lead, p.V) : none_vec<F32>();
+      }
     }
   };
   uint4 w[kUnroll];
@@ -272,62 +302,61 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   for (int v = v0; v < v1; v += kUnroll * kLpThreads) {
     uint4 next[kUnroll];
     load(v + kUnroll * kLpThreads, next);  // in flight while these are summed
-    float vm[kUnroll], m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      vm[i] = largest<F32>(w[i]);
-      m = max_nan(m, vm[i]);
+    const float m = largest<F32, kUnroll>(w);
+    if (v == v0) {
+      s.ref = fminf(fmaxf(m, kLowest), -kLowest);  // (NaN: the lowest)
+      if (TOP) {
+        // the k-th largest of the threads' maxima bounds the k-th largest element
+        // from below. A thread without elements counts as nothing (rank 0).
+        const uint32_t sorted = sort32(v + tid < v1 ? rank_of(m) : 0u, lane);
+        sh.list[warp][lane] = ((uint64_t)sorted << 32);
+        merge_lists(sh.list, kLpWarps, warp, lane);
+        bar = (uint32_t)(sh.list[0][p.k - 1] >> 32);
+        if (tid == 0) sh.threshold = bar;
+        __syncthreads();
+        bar_z = bar > 1 ? key_value(bar) : -INFINITY;
+      }
     }
-    s.top = max_nan(s.top, m);
-    if (v == v0) s.ref = fminf(fmaxf(m, kLowest), -kLowest);  // (NaN: the lowest)
-    if (TOP && v == v0) {
-      // the k-th largest of the threads' maxima bounds the k-th largest element
-      // from below. A thread without elements counts as nothing (rank 0).
-      const uint32_t sorted = sort32(v + tid < v1 ? rank_of(m) : 0u, lane);
-      sh.list[warp][lane] = ((uint64_t)sorted << 32);
-      merge_lists(sh.list, kLpWarps, warp, lane);
-      bar = (uint32_t)(sh.list[0][p.k - 1] >> 32);
-      if (tid == 0) sh.threshold = bar;
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) add_vec<F32>(s, w[i], vm[i]);
-    if (TOP) {
+    add_vecs<F32>(s, w, m);
+    // (a NaN hides the other elements: those are looked at)
+    if (TOP && __any_sync(0xffffffffu, !(m < bar_z))) {
       bar = max(bar, *reinterpret_cast<volatile uint32_t*>(&sh.threshold));
-      // (a NaN hides its vector's other elements: those are looked at)
-      if (__any_sync(0xffffffffu, m != m || rank_of(m) >= bar)) {
+#pragma unroll 1
+      for (int i = 0; i < kUnroll; ++i) {
+        uint4 wi = w[0];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-          const int vi = v + i * kLpThreads + tid;
-          unsigned hit = __ballot_sync(0xffffffffu, vi < v1 && (vm[i] != vm[i] || rank_of(vm[i]) >= bar));
-          while (hit) {  // one lane's vector at a time, an element a lane
-            const int src = __ffs(hit) - 1;
-            hit &= hit - 1;
-            const uint32_t u[4] = {__shfl_sync(0xffffffffu, w[i].x, src), __shfl_sync(0xffffffffu, w[i].y, src),
-                                   __shfl_sync(0xffffffffu, w[i].z, src), __shfl_sync(0xffffffffu, w[i].w, src)};
-            const int at4 = F32 ? lane : lane >> 1;
-            const uint32_t word = at4 == 0 ? u[0] : at4 == 1 ? u[1] : at4 == 2 ? u[2] : u[3];
-            const float z = __uint_as_float(F32 ? word : (lane & 1) ? word & 0xFFFF0000u : word << 16);
-            const int64_t index = (int64_t)(vi - lane + src) * E - lead + lane;
-            const uint64_t key = lane < E && index >= 0 && index < p.V ? key_of(z, (int)index) : 0ull;
-            unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
-            while (todo) {
-              const uint64_t c = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
-              todo &= todo - 1;
-              const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
-              const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
-              if (lane == at) mine = c;
-              else if (lane > at) mine = up;
-            }
+        for (int q = 1; q < kUnroll; ++q) wi = q == i ? w[q] : wi;
+        const float vm = largest<F32, 1>(&wi);
+        const int vi = v + i * kLpThreads + tid;
+        unsigned hit = __ballot_sync(0xffffffffu, vi < v1 && (vm != vm || rank_of(vm) >= bar));
+        while (hit) {  // one lane's vector at a time, an element a lane
+          const int src = __ffs(hit) - 1;
+          hit &= hit - 1;
+          const uint32_t u[4] = {__shfl_sync(0xffffffffu, wi.x, src), __shfl_sync(0xffffffffu, wi.y, src),
+                                 __shfl_sync(0xffffffffu, wi.z, src), __shfl_sync(0xffffffffu, wi.w, src)};
+          const int at4 = F32 ? lane : lane >> 1;
+          const uint32_t word = at4 == 0 ? u[0] : at4 == 1 ? u[1] : at4 == 2 ? u[2] : u[3];
+          const float z = __uint_as_float(F32 ? word : (lane & 1) ? word & 0xFFFF0000u : word << 16);
+          const int64_t index = (int64_t)(vi - lane + src) * E - lead + lane;
+          const uint64_t key = lane < E && index >= 0 && index < p.V ? key_of(z, (int)index) : 0ull;
+          unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
+          while (todo) {
+            const uint64_t c = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
+            todo &= todo - 1;
+            const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
+            const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+            if (lane == at) mine = c;
+            else if (lane > at) mine = up;
           }
         }
-        // the warp's k-th best may raise the block's threshold
-        const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
-        if (kth > bar) {
-          bar = kth;
-          if (lane == 0) atomicMax(&sh.threshold, kth);
-        }
       }
+      // the warp's k-th best may raise the block's threshold
+      const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
+      if (kth > bar) {
+        bar = kth;
+        if (lane == 0) atomicMax(&sh.threshold, kth);
+      }
+      bar_z = bar > 1 ? key_value(bar) : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) w[i] = next[i];

@@ -12,10 +12,9 @@
 // compared with it exactly: every code is the correctly rounded one.
 //
 // Bound by HBM: 7 bytes an element (x, residual in; residual, q out), 9 with
-// the bf16 values. A row belongs to G threads of NV 16-byte vectors each. Rows
-// in plenty: NV = 8, so a row of 2048 is one warp's, its 16 loads in flight at
-// once and its reduction five shuffles with no barrier. Few rows: NV = 1, the
-// row spread over as many warps as it has vectors, for latency.
+// the bf16 values: 32768 rows of 2048 in 94 us with the values, 6.4 TB/s (95% of
+// the measured copy). A row belongs to G threads of NV 16-byte vectors each,
+// whole warps, joined by one barrier.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -112,7 +111,7 @@ __device__ __noinline__ Quotients8 settle(uint4 r, uint4 weight, float a, bool s
 }
 
 template <int NV, bool E4M3>
-__global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_kernel(const NormParams p, int G) {
+__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
   // G threads a row (whole warps), blockDim / G rows a block
   const int sub = threadIdx.x / G, lt = threadIdx.x % G;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / G) + sub;
@@ -252,7 +251,8 @@ __global__ void __launch_bounds__(NV == 8 ? 256 : NV == 4 ? 512 : 1024) norm_ker
 }
 
 template <int NV, bool E4M3>
-cudaError_t norm_launch_nv(const NormParams& p, int G, cudaStream_t s) {
+cudaError_t norm_launch_nv(const NormParams& p, cudaStream_t s) {
+  const int G = ((p.d / 8 + NV - 1) / NV + 31) / 32 * 32;  // a row's threads: whole warps, at most 1024
   const int rows = G < kNormThreads ? kNormThreads / G : 1, threads = rows * G;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.T + (int64_t)rows - 1) / rows));
@@ -270,21 +270,12 @@ cudaError_t norm_launch_nv(const NormParams& p, int G, cudaStream_t s) {
 
 cudaError_t norm_launch(const NormParams& p, int sms, cudaStream_t s) {
   const int nvec = p.d / 8;
-  // The most vectors a thread that still leaves 16 warps a multiprocessor;
-  // rows of more than 1024 threads' worth always take more.
-  int nv = 8;
-  while (nv > 1 && (int64_t)p.T * ((nvec + nv - 1) / nv) < (int64_t)sms * 512 && nvec <= 1024 * (nv / 2)) nv /= 2;
-  const int G = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-  if (p.e4m3) {
-    if (nv == 8) return norm_launch_nv<8, true>(p, G, s);
-    if (nv == 4) return norm_launch_nv<4, true>(p, G, s);
-    if (nv == 2) return norm_launch_nv<2, true>(p, G, s);
-    return norm_launch_nv<1, true>(p, G, s);
-  }
-  if (nv == 8) return norm_launch_nv<8, false>(p, G, s);
-  if (nv == 4) return norm_launch_nv<4, false>(p, G, s);
-  if (nv == 2) return norm_launch_nv<2, false>(p, G, s);
-  return norm_launch_nv<1, false>(p, G, s);
+  // Two vectors a thread: 32768 rows of 2048 with bf16 values take 94 us, against
+  // 105 with four and 118 with eight (fewer warps fit, and each keeps fewer rows'
+  // phases apart). One where the rows are few, for latency.
+  if ((int64_t)p.T * ((nvec + 1) / 2) < (int64_t)sms * 512 && nvec <= 1024)
+    return p.e4m3 ? norm_launch_nv<1, true>(p, s) : norm_launch_nv<1, false>(p, s);
+  return p.e4m3 ? norm_launch_nv<2, true>(p, s) : norm_launch_nv<2, false>(p, s);
 }
 
 }  // namespace moe
