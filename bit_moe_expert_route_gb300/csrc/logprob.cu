@@ -228,6 +228,7 @@ struct LpShared {
   Sums sums[kLpWarps];
   uint64_t row_list[32];  // the block's results, read by the cluster's first block
   Sums row_sums;
+  uint4 scratch[kLpWarps][kUnroll];  // a lane's vectors, looked at by its warp
   uint32_t threshold;     // rank that an element has to reach
 };
 
@@ -321,33 +322,31 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
     // (a NaN hides the other elements: those are looked at)
     if (TOP && __any_sync(0xffffffffu, !(m < bar_z))) {
       bar = max(bar, *reinterpret_cast<volatile uint32_t*>(&sh.threshold));
-#pragma unroll 1
-      for (int i = 0; i < kUnroll; ++i) {
-        uint4 wi = w[0];
+      unsigned hit = __ballot_sync(0xffffffffu, m != m || rank_of(m) >= bar);
+      while (hit) {  // one lane's vectors at a time, through shared memory: an element a lane
+        const int src = __ffs(hit) - 1;
+        hit &= hit - 1;
+        if (lane == src) {
 #pragma unroll
-        for (int q = 1; q < kUnroll; ++q) wi = q == i ? w[q] : wi;
-        const float vm = largest<F32, 1>(&wi);
-        const int vi = v + i * kLpThreads + tid;
-        unsigned hit = __ballot_sync(0xffffffffu, vi < v1 && (vm != vm || rank_of(vm) >= bar));
-        while (hit) {  // one lane's vector at a time, an element a lane
-          const int src = __ffs(hit) - 1;
-          hit &= hit - 1;
-          const uint32_t u[4] = {__shfl_sync(0xffffffffu, wi.x, src), __shfl_sync(0xffffffffu, wi.y, src),
-                                 __shfl_sync(0xffffffffu, wi.z, src), __shfl_sync(0xffffffffu, wi.w, src)};
-          const int at4 = F32 ? lane : lane >> 1;
-          const uint32_t word = at4 == 0 ? u[0] : at4 == 1 ? u[1] : at4 == 2 ? u[2] : u[3];
-          const float z = __uint_as_float(F32 ? word : (lane & 1) ? word & 0xFFFF0000u : word << 16);
-          const int64_t index = (int64_t)(vi - lane + src) * E - lead + lane;
-          const uint64_t key = lane < E && index >= 0 && index < p.V ? key_of(z, (int)index) : 0ull;
-          unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
-          while (todo) {
-            const uint64_t c = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
-            todo &= todo - 1;
-            const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
-            const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
-            if (lane == at) mine = c;
-            else if (lane > at) mine = up;
-          }
+          for (int i = 0; i < kUnroll; ++i) sh.scratch[warp][i] = w[i];
+        }
+        __syncwarp();
+        const int vi = v + (lane / E) * kLpThreads + warp * 32 + src;
+        const int64_t index = (int64_t)vi * E - lead + lane % E;
+        uint64_t key = 0;
+        if (lane < kUnroll * E && vi < v1 && index >= 0 && index < p.V) {
+          const float z = F32 ? reinterpret_cast<const float*>(sh.scratch[warp])[lane & 15]
+                              : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(sh.scratch[warp])[lane]);
+          key = key_of(z, (int)index);
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, key != 0 && (uint32_t)(key >> 32) >= bar);
+        while (todo) {
+          const uint64_t c = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
+          todo &= todo - 1;
+          const int at = __popc(__ballot_sync(0xffffffffu, mine > c));  // entries above it
+          const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+          if (lane == at) mine = c;
+          else if (lane > at) mine = up;
         }
       }
       // the warp's k-th best may raise the block's threshold
