@@ -161,16 +161,6 @@ cudaError_t few_launch(const GemmW8Params& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, gemm_w8_few_kernel<M, NT>, p);
 }
-template <int M>
-cudaError_t few_launch_nt(const GemmW8Params& p, cudaStream_t s) {
-  switch ((p.T + 7) / 8) {
-    case 1: return few_launch<M, 1>(p, s);
-    case 2: return few_launch<M, 2>(p, s);
-    case 3: return few_launch<M == 4 ? 2 : M, 3>(p, s);
-    default: return few_launch<M == 4 ? 2 : M, 4>(p, s);
-  }
-}
-
 // ---------------------------------------------------------------- many tokens
 // The tokens' codes as f16 rows of K, contiguous; clears the status word.
 __global__ void __launch_bounds__(256) widen_kernel(const GemmW8Params p) {
@@ -208,12 +198,19 @@ struct CfgW8 {
   static constexpr int kSB = BN == 256 ? 5 : BN == 128 ? 4 : 6;
   static constexpr int kSD = kSA > kSB ? kSA : kSB;
   static constexpr int kBBytes = BN * kBK * 2;
-  static constexpr int kAcc = BN == 256 ? 1 : 2;  // accumulators: 256 columns in all at 256 and 128
-  static constexpr int kACol = kAcc * BN;
+  static constexpr int kAcc = BN == 256 ? 1 : 2;  // tiles in tensor memory: 256 columns in all
   static constexpr int kOffB = 0;
   static constexpr int kOffQ = kSB * kBBytes;
   static constexpr int kOffScale = kOffQ + kSQ * kQStage;  // 32 token scales an epilogue warp
   static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
+  // Threads that issue MMAs. What one does between two k-blocks (waits, a
+  // commit) is not hidden behind the MMAs of 64 tokens (400 cycles of about
+  // 1000): there two take k-blocks in turn, each with an accumulator of its
+  // own that the epilogue adds.
+  static constexpr int kIssuers = BN == 64 ? 2 : 1;
+  static constexpr int kAccCols = kIssuers * BN;  // of one tile
+  static constexpr int kACol = kAcc * kAccCols;
+  static_assert(kSA % kIssuers == 0 && kSB % (kIssuers * kBSteps) == 0 && kSD % kIssuers == 0 || kIssuers == 1, "an issuer's stages come round to it");
   static constexpr int kBars = 2 * kSQ + kSA + kSB + kSD + 2 + 2 + 1;
   static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
   static_assert(kACol + kSA * (kKB / 2) <= 512, "tensor memory exceeded");
@@ -279,10 +276,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
     for (int i = 0; i < C::kSB; ++i) mbar_init(&b_full[i], 1);
     for (int i = 0; i < C::kSD; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_full[i], C::kIssuers);
       mbar_init(&acc_empty[i], kEpiWarps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, C::kIssuers);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&args.tm_w);
@@ -346,23 +343,25 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       for (uint32_t j = it > (uint32_t)C::kSB ? it - C::kSB : 0; j < it; ++j)
         mbar_wait(&b_full[j % C::kSB], (j / C::kSB) & 1, abort_flag, g.status, 62);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || (C::kIssuers == 2 && warp == 3)) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16_f32(kTileN, BN);
       // Stage indices and phases are carried, not divided out of a counter, and
-      // descriptors are one add from a base: what this thread does between two
-      // k-blocks' MMAs is not hidden behind them when N is small (about 590 of
-      // 1020 cycles a k-block at 64 tokens before this).
+      // descriptors are one add from a base: this thread's own work paces small N.
+      constexpr uint32_t kI = C::kIssuers;
+      const uint32_t me = kI == 2 ? warp >> 1 : 0;  // takes k-blocks me, me + kI, ... of all the CTA's
       const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem + C::kOffB));
-      uint32_t sa = 0, pa = 0, sb = 0, pb = 0, sd = 0, buf = 0, pacc = 1;
+      uint32_t sa = me, pa = 0, sb = me * C::kBSteps, pb = 0, sd = me, buf = 0, pacc = 1;
+      int skip = (int)me;  // k-blocks of the next tile before this thread's first
       bool alive = true;
       for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
         if (!mbar_wait(&acc_empty[buf], pacc, abort_flag, g.status, 64)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + buf * BN;
+        const uint32_t d_tmem = tmem + buf * C::kAccCols + me * BN;
         uint32_t accumulate = 0;
+        int kb = skip;
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb) {
+        for (; kb < KB; kb += kI) {
           if (!mbar_wait(&a_full[sa], pa, abort_flag, g.status, 66)) {
             alive = false;
             break;
@@ -382,14 +381,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
                         b_desc + (((kk / 4) * (BN * 128) + (kk % 4) * 32) >> 4), idesc, accumulate);
               accumulate = 1;
             }
-            if (++sb == C::kSB) sb = 0, pb ^= 1;
+            sb += h + 1 < C::kBSteps ? 1 : 1 + (kI - 1) * C::kBSteps;
+            if (sb >= C::kSB) sb -= C::kSB, pb ^= 1;
           }
           if (!alive) break;
           tc_commit(&done[sd]);
-          if (++sa == C::kSA) sa = 0, pa ^= 1;
-          if (++sd == C::kSD) sd = 0;
+          if ((sa += kI) >= C::kSA) sa -= C::kSA, pa ^= 1;
+          if ((sd += kI) >= C::kSD) sd -= C::kSD;
         }
         if (!alive) break;
+        skip = kb - KB;
         tc_commit(&acc_full[buf]);
         if (++buf == C::kAcc) buf = 0, pacc ^= 1;
       }
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
   } else if (warp >= kEpiWarp0) {
     // lanes of quarter warp % 4 = 32 weight rows; the two groups of four warps take half the tokens each
     const int quarter = warp & 3, group = (warp - kEpiWarp0) >> 2;
-    constexpr int kCols = BN / 2;
+    constexpr int kCols = BN / 2, kChunk = C::kIssuers == 2 ? 16 : 32;
     using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
     float4* scales = reinterpret_cast<float4*>(smem + C::kOffScale + (warp - kEpiWarp0) * 128);
     uint32_t tile = 0;
@@ -448,19 +449,33 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       const float ws = n < g.N ? __ldg(g.w_scale + n) : 0.f;
       if (!warp_wait(&acc_full[buf], (tile / C::kAcc) & 1, abort_flag, g.status, 70)) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + group * kCols;
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + buf * C::kAccCols + group * kCols;
+      // a tile of one k-block has one issuer's sums only: those of the tile's turn
+      const uint32_t single = KB == 1 ? (tile & 1) * BN : 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
+      for (int c0 = 0; c0 < kCols; c0 += kChunk) {
         __syncwarp();  // (the stores of the chunk before part the lanes)
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + c0, v);
-        const int t = t0 + c0, live = g.T - t;
-        reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
-        tc_wait_ld();
-        if (c0 + 32 == kCols) {  // the accumulator is in registers: the next tile may start
+        uint32_t v[kChunk];
+        if constexpr (C::kIssuers == 2) {
+          uint32_t v2[kChunk];
+          tmem_ld_32x32b_x16(taddr + single + c0, v);
+          tmem_ld_32x32b_x16(taddr + BN + c0, v2);
+          tc_wait_ld();
+          if (KB > 1) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(v2[i]));
+          }
+        } else {
+          tmem_ld_32x32b_x32(taddr + c0, v);
+          tc_wait_ld();
+        }
+        if (c0 + kChunk == kCols) {  // the accumulator is in registers: the next tile may start
           tc_fence_before();
           warp_arrive(&acc_empty[buf]);
         }
+        const int t = t0 + c0, live = g.T - t;
+        __syncwarp();
+        reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
         __syncwarp();
         Out* dst = static_cast<Out*>(g.out) + (int64_t)t * g.ldo + n;
         auto put = [&](uint32_t acc, float as) {
@@ -472,9 +487,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
           dst += g.ldo;
         };
         if (n < g.N) {  // one row of 32 outputs a store
-          if (live >= 32) {
+          if (live >= kChunk) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kChunk / 4; ++i) {
               const float4 as = scales[i];
               put(v[4 * i], as.x);
               put(v[4 * i + 1], as.y);
@@ -483,7 +498,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kChunk; ++i)
               if (i < live) put(v[i], reinterpret_cast<const float*>(scales)[i]);
           }
         }
@@ -547,26 +562,33 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
+  const int64_t blocks = (p.N + 15) / 16 * (int64_t)((p.T + 31) / 32);
+  const int nt = (p.T + 7) / 8;
+  const bool many_rows = p.N >= 32 * 4 * sms;  // several blocks an SM even with 32 or 64 rows each
+  // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
+  // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 49 and 55 us with
+  // 32 rows at 16 and 24, against 62 and 56 in tensor memory, which is ahead
+  // from 25 (48 against 63 at 32).
+  if (many_rows && nt <= 3) {
+    if (nt == 1) return few_launch<4, 1>(p, s);
+    return nt == 2 ? few_launch<2, 2>(p, s) : few_launch<2, 3>(p, s);
+  }
   // More than 32 tokens stay with the first kernel, 32 at a time, while its
   // blocks of 16 weight rows fill the machine at most twice (once where K is
   // short and a block has little to do): 64 tokens by 4608 x 2048 weights 7.9 us
-  // against 12.2, 64 by 2048 x 2048 4.6 against 12.2; past that the tensor
-  // memory kernel is ahead (128 by 4608 x 2048: 14.2 against 12.4).
-  const int64_t blocks = (p.N + 15) / 16 * (int64_t)((p.T + 31) / 32);
-  if (p.T <= kW8FewTokens || blocks <= (int64_t)sms * (p.K < 1024 ? 2 : 4)) {
-    // more rows a block reuse the tokens' fragments; fewer fill the machine
-    const int nt = (p.T + 7) / 8;
-    if (nt <= 2 && p.N >= 64 * 4 * sms) return few_launch_nt<4>(p, s);
-    if (p.T <= kW8FewTokens && p.N >= 32 * 4 * sms) return few_launch_nt<2>(p, s);
-    return few_launch_nt<1>(p, s);
+  // against 12.2, 64 by 2048 x 2048 4.6 against 12.2.
+  if (nt <= 3 || blocks <= (int64_t)sms * (p.K < 1024 ? 2 : 4)) {
+    if (nt == 1) return few_launch<1, 1>(p, s);
+    if (nt == 2) return few_launch<1, 2>(p, s);
+    return nt == 3 ? few_launch<1, 3>(p, s) : few_launch<1, 4>(p, s);
   }
   // The token width whose waves cost least, by the measured time of a k-block
-  // (about 0.5, 0.56 and 0.72 us at 64, 128 and 256 tokens) and a tile's ends.
+  // (about 0.48, 0.56 and 0.72 us at 64, 128 and 256 tokens) and a tile's ends.
   const int64_t MT = (p.N + kTileN - 1) / kTileN, kb = (p.K + kKB - 1) / kKB;
   auto cost = [&](int bn, int64_t step, int64_t ends) {
     return (MT * ((p.T + bn - 1) / bn) + sms - 1) / sms * (kb * step + ends);
   };
-  const int64_t c64 = cost(64, 50, 50), c128 = cost(128, 56, 80), c256 = cost(256, 72, 150);
+  const int64_t c64 = cost(64, 48, 50), c128 = cost(128, 56, 80), c256 = cost(256, 72, 150);
   if (c256 <= c128 && c256 <= c64) return many_launch<256>(p, sms, s);
   return c128 <= c64 ? many_launch<128>(p, sms, s) : many_launch<64>(p, sms, s);
 }

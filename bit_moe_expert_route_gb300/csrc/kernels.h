@@ -270,7 +270,7 @@ struct LogprobParams {
 cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integer product
-constexpr int kW8FewTokens = 32;  // up to here no workspace beyond the status word
+constexpr int kW8FewTokens = 24;  // up to here no workspace beyond the status word
 struct GemmW8Params {
   const int8_t* a;           // [T], rows lda apart
   int64_t lda;

@@ -31,7 +31,7 @@ def exact(a, sa, w, sw):
     return (a.double() @ w.double().t()) * sa.double()[:, None] * sw.double()
 
 
-SHAPES = [(1, 1, 16, 0), (1, 4608, 2048, 0), (2, 100, 48, 16), (7, 333, 2048, 0), (8, 40001, 512, 0), (9, 65, 4096, 32), (17, 20011, 272, 0),
+SHAPES = [(1, 1, 16, 0), (1, 4608, 2048, 0), (2, 100, 48, 16), (7, 333, 2048, 0), (8, 40001, 512, 0), (3, 20480, 16, 0), (31, 30001, 1104, 0), (13, 25000, 8192, 16), (9, 65, 4096, 32), (17, 20011, 272, 0),
           (24, 33, 8192, 0), (32, 2048, 2048, 0), (33, 2048, 2048, 0), (33, 1, 16, 0), (64, 129, 144, 16), (65, 300, 1024, 0), (100, 40000, 256, 0),
           (129, 4608, 2048, 0), (255, 127, 400, 0), (300, 5000, 1040, 0), (700, 8192, 640, 16), (1500, 4100, 2048, 0), (4097, 1029, 528, 0), (4000, 8100, 144, 0),
           (8192, 4100, 1040, 0)]
