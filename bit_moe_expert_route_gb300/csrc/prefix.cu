@@ -101,16 +101,26 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
     const bool in = r < it.rows;
     cp_async_16(smem_u32(qs + tile_off<D>(r, c)), p.q + (in ? query_row(it.row0 + r) * D + c * 8 : 0), in ? 16u : 0u);
   }
+  // A thread copies one 16-byte chunk of every kStep-th row of a tile, so that
+  // addresses are one add apart (with 4 rows a step, the swizzle alternates).
+  constexpr int kStep = kPfThreads / kChunks;
+  const int lr = tid / kChunks, lc = tid % kChunks;
+  const uint16_t* kbase = it.K + lc * 8;
+  const uint16_t* vbase = it.V + lc * 8;
+  const uint32_t dst[2] = {smem_u32(smem) + tile_off<D>(lr, lc), smem_u32(smem) + tile_off<D>(lr + kStep, lc) - kStep * (D * 2)};
   auto load_stage = [&](int s, int key) {
     if (key < it.k1) {
-      uint8_t* ks = smem + s * 2 * C::kTile;
-#pragma unroll 4
-      for (int i = tid; i < kTileKeys * kChunks; i += kPfThreads) {
-        const int r = i / kChunks, c = i % kChunks;
-        const bool in = key + r < it.k1;  // keys past the end as zeros: their weight is 0 too
-        const int64_t at = in ? (int64_t)(key + r) * it.ld + c * 8 : 0;
-        cp_async_16(smem_u32(ks + tile_off<D>(r, c)), it.K + at, in ? 16u : 0u);
-        cp_async_16(smem_u32(ks + C::kTile + tile_off<D>(r, c)), it.V + at, in ? 16u : 0u);
+      const uint32_t at = s * 2 * C::kTile;
+      int64_t src = (int64_t)(key + lr) * it.ld;
+      const int left = it.k1 - key - lr;
+#pragma unroll 8
+      for (int j = 0; j < kTileKeys / kStep; ++j) {
+        const bool in = j * kStep < left;  // keys past the end as zeros: their weight is 0 too
+        const int64_t from = in ? src : 0;
+        const uint32_t to = dst[j & 1] + at + j * kStep * (D * 2);
+        cp_async_16(to, kbase + from, in ? 16u : 0u);
+        cp_async_16(to + C::kTile, vbase + from, in ? 16u : 0u);
+        src += kStep * it.ld;
       }
     }
     cp_async_commit();

@@ -5,8 +5,8 @@
 // of KT keys:  S = Q K^T (both in shared memory) into tensor memory; softmax
 // weights P = 2^(scale S - m) from there into tensor memory as bf16; O += P V
 // with P as the MMA's A operand and O kept in tensor memory through the slice.
-// The products of tile i + 1's scores are issued before tile i's weights are
-// waited for, so the tensor core works while the softmax warps do.
+// One thread issues the scores' products, up to two tiles ahead of the weights,
+// another the outputs', so the tensor core works while the softmax warps do.
 //
 // K and V tiles come by TMA into one ring of slots in the order in which the
 // products use them (K0 K1 V0 K2 V1 ...); V is read as it lies (MN-major
@@ -28,7 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 256;  // warp 0 TMA, warp 1 MMA, warps 4-7 softmax
+constexpr int kTcThreads = 256;  // warp 0 TMA, warps 1 and 2 MMA, warps 4-7 softmax
 constexpr float kLazyLog2 = 8.f;
 
 MOE_DEVINL float ex2(float x) {
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&args.tm_k);
@@ -177,45 +177,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       for (int j = loads > NS ? loads - NS : 0; j < loads; ++j)
         mbar_wait(&full[j % NS], (j / NS) & 1, abort_flag, p.status, 82);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
+    // Warp 1 issues the scores' products, warp 2 the outputs': what one does
+    // between two tiles (waits, commits) runs beside the other's MMAs.
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kTcRows, KT);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kTcRows, D) | (1u << 16);  // B (V) is MN-major
       const uint32_t slots = smem_u32(smem + C::kOffSlots);
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem));
       int slot = 0, phase = 0;
-      auto next = [&]() {
-        if (++slot == NS) slot = 0, phase ^= 1;
+      auto advance = [&](int by) {
+        if ((slot += by) >= NS) slot -= NS, phase ^= 1;
       };
-      auto scores = [&](int i) {
-        if (!mbar_wait(&full[slot], phase, abort_flag, p.status, 83)) return false;
-        tc_fence_after();
-        const uint64_t k_desc = smem_desc_sw128(slots + slot * C::kSlot);
+      if (warp == 1) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kTcRows, KT);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem));
+        bool alive = mbar_wait(q_full, 0, abort_flag, p.status, 84);
+        for (int i = 0; i < n && alive; ++i) {
+          // the scores two tiles before have been read once their weights are written
+          if ((i >= 2 && !mbar_wait(&p_full[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, 91)) ||
+              !mbar_wait(&full[slot], phase, abort_flag, p.status, 83))
+            break;
+          tc_fence_after();
+          const uint64_t k_desc = smem_desc_sw128(slots + slot * C::kSlot);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
+          for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(tmem + C::kColS + (i & 1) * KT, q_desc + ((c * (kTcRows * 128) + kk * 32) >> 4),
-                        k_desc + ((c * (KT * 128) + kk * 32) >> 4), idesc_s, (c | kk) != 0);
-        tc_commit(&empty[slot]);
-        tc_commit(&s_full[i & 1]);
-        next();
-        return true;
-      };
-      bool alive = mbar_wait(q_full, 0, abort_flag, p.status, 84) && scores(0);
-      for (int i = 0; i < n && alive; ++i) {
-        if (i + 1 < n && !scores(i + 1)) break;
-        if (!mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 85) ||
-            !mbar_wait(&full[slot], phase, abort_flag, p.status, 86))
-          break;
-        tc_fence_after();
-        const uint64_t v_desc = smem_desc_mn(slots + slot * C::kSlot, KT * 128);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(tmem + C::kColS + (i & 1) * KT, q_desc + ((c * (kTcRows * 128) + kk * 32) >> 4),
+                          k_desc + ((c * (KT * 128) + kk * 32) >> 4), idesc_s, (c | kk) != 0);
+          tc_commit(&empty[slot]);
+          tc_commit(&s_full[i & 1]);
+          advance(i == 0 ? 1 : 2);  // K0 K1 V0 K2 V1 ...
+        }
+      } else {
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kTcRows, D) | (1u << 16);  // B (V) is MN-major
+        advance(n > 1 ? 2 : 1);
+        for (int i = 0; i < n; ++i) {
+          if (!mbar_wait(&full[slot], phase, abort_flag, p.status, 86) ||
+              !mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 85))
+            break;
+          tc_fence_after();
+          const uint64_t v_desc = smem_desc_mn(slots + slot * C::kSlot, KT * 128);
 #pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)
-          tc_mma_ts(tmem, tmem + C::kColP + (i & 1) * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o, (i | kk) != 0);
-        tc_commit(&empty[slot]);
-        tc_commit(&pv_done[i & 1]);
-        next();
+          for (int kk = 0; kk < KT / 16; ++kk)
+            tc_mma_ts(tmem, tmem + C::kColP + (i & 1) * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o, (i | kk) != 0);
+          tc_commit(&empty[slot]);
+          tc_commit(&pv_done[i & 1]);
+          advance(i + 2 < n ? 2 : 1);  // the last V follows the one before it
+        }
       }
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
       mbar_wait(drain, 0, abort_flag, p.status, 87);
@@ -266,8 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         l *= f;
         m = nm;
         if (i > 0) {
-          // O is whole once the product before is complete (earlier ones are:
-          // this tile's scores were issued after them)
+          // O is whole once the product before is complete
           if (!(alive = warp_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.status, 89))) break;
           tc_fence_after();
 #pragma unroll 1
@@ -281,6 +287,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
           }
         }
       }
+      // the weights two tiles before have been multiplied: their columns are free
+      if (i >= 2 && !(alive = warp_wait(&pv_done[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, 92))) break;
+      tc_fence_after();
       const float ref = m == -INFINITY ? 0.f : m;
       const float2 sc = make_float2(p.scale_log2, p.scale_log2), nr = make_float2(-ref, -ref);
       float2 sum = make_float2(0.f, 0.f);
