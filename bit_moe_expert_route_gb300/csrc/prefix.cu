@@ -13,11 +13,11 @@
 //
 // A block: 4 warps, WM of them over 16-row tiles and 4 / WM over the keys of
 // each 64-key tile, so that a few rows still use every warp. K and V tiles
-// come through a ring of cp.async stages; m16n8k16 products with fp32 sums,
+// come through a ring of cp.async slots; m16n8k16 products with fp32 sums,
 // the weights rounded to bf16 for the second product (their rounding, 2^-9
 // each, averages out over the positions; the sum l adds them unrounded). The
 // running maximum moves only when a score passes it by 2^8, which fp32 and
-// bf16 hold without loss, so the output is rarely rescaled. (With more than 64
+// bf16 hold without loss, so the output is rarely rescaled. (With more than 32
 // rows a KV head the prefix goes to prefix_tc.cu; the sequences' own positions
 // stay here.)
 #include <algorithm>
@@ -31,7 +31,7 @@ namespace {
 constexpr int kPfThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr float kLazyLog2 = 8.f;
-constexpr int kPrefixTcMin = 512;  // positions from which the tensor-memory kernel takes a prefix
+constexpr int kPrefixTcMin = 256;  // positions from which the tensor-memory kernel takes a prefix
 
 MOE_DEVINL float ex2(float x) {
   float r;
@@ -70,11 +70,16 @@ MOE_DEVINL uint32_t tile_off(int r, int c) {
 
 template <int D>
 struct PfCfg {
-  static constexpr int kStages = 3;
-  static constexpr int kTile = kTileKeys * D * 2;  // K or V of one stage
-  static constexpr int kQ = 64 * D * 2;
-  static constexpr int kSmem = kStages * 2 * kTile + kQ;
-  static_assert(kSmem <= 232448, "shared memory exceeded");
+  // Three slots of one K or one V tile each, filled two ahead (K0 V0 K1 V1 ...):
+  // at head size 256 two blocks fit an SM, and one's loads and merges pass
+  // beside the other's products.
+  static constexpr int kSlots = 3;
+  static constexpr int kTile = kTileKeys * D * 2;
+  static constexpr int kMaxRows = 32;
+  static constexpr int kSmem = kSlots * kTile + kMaxRows * D * 2;
+  static constexpr int kBlocks = D == 256 ? 2 : D == 128 ? 3 : 4;  // an SM's
+  static_assert(kBlocks * (kSmem + 1024) <= 233472, "shared memory exceeded");
+  static_assert(64 * D * 4 + 64 * 8 <= kSlots * kTile, "the warps' states do not fit the ring");
 };
 
 // One block's work: `rows` query rows (row r: sequence b0 + r / G, head
@@ -93,7 +98,7 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
   constexpr int kChunks = D / 8;  // 16-byte chunks a row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wm = warp % WM, wk = warp / WM;
   const int G = p.Hq / p.Hkv, g = lane >> 2, t = lane & 3;
-  uint8_t* qs = smem + C::kStages * 2 * C::kTile;
+  uint8_t* qs = smem + C::kSlots * C::kTile;
   auto query_row = [&](int r) { return (int64_t)(it.b0 + r / G) * p.Hq + it.h * G + r % G; };  // of B Hq
   // queries: rows past the end as zeros
   for (int i = tid; i < 16 * WM * kChunks; i += kPfThreads) {
@@ -105,45 +110,43 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
   // addresses are one add apart (with 4 rows a step, the swizzle alternates).
   constexpr int kStep = kPfThreads / kChunks;
   const int lr = tid / kChunks, lc = tid % kChunks;
-  const uint16_t* kbase = it.K + lc * 8;
-  const uint16_t* vbase = it.V + lc * 8;
   const uint32_t dst[2] = {smem_u32(smem) + tile_off<D>(lr, lc), smem_u32(smem) + tile_off<D>(lr + kStep, lc) - kStep * (D * 2)};
-  auto load_stage = [&](int s, int key) {
+  int fill = 0;  // the next slot to fill
+  auto load_tile = [&](const uint16_t* base, int key) {
     if (key < it.k1) {
-      const uint32_t at = s * 2 * C::kTile;
-      int64_t src = (int64_t)(key + lr) * it.ld;
+      const uint32_t at = fill * C::kTile;
+      int64_t src = (int64_t)(key + lr) * it.ld + lc * 8;
       const int left = it.k1 - key - lr;
 #pragma unroll 8
       for (int j = 0; j < kTileKeys / kStep; ++j) {
         const bool in = j * kStep < left;  // keys past the end as zeros: their weight is 0 too
-        const int64_t from = in ? src : 0;
-        const uint32_t to = dst[j & 1] + at + j * kStep * (D * 2);
-        cp_async_16(to, kbase + from, in ? 16u : 0u);
-        cp_async_16(to + C::kTile, vbase + from, in ? 16u : 0u);
+        cp_async_16(dst[j & 1] + at + j * kStep * (D * 2), base + (in ? src : 0), in ? 16u : 0u);
         src += kStep * it.ld;
       }
     }
     cp_async_commit();
+    fill = fill + 1 == C::kSlots ? 0 : fill + 1;
   };
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) load_stage(s, it.k0 + s * kTileKeys);
+  load_tile(it.K, it.k0);
+  load_tile(it.V, it.k0);
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < D / 8; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
   const float scale = p.scale_log2;
-  int stage = 0;
+  int slot = 0;
+  auto next_slot = [&]() -> const uint8_t* {  // the oldest tile, once it has landed and the one before is used up
+    cp_async_wait<1>();
+    __syncthreads();
+    const uint8_t* at = smem + slot * C::kTile;
+    slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+    return at;
+  };
 #pragma unroll 1
   for (int key = it.k0; key < it.k1; key += kTileKeys) {
-    cp_async_wait<C::kStages - 2>();
-    __syncthreads();
-    {
-      const int ahead = stage + C::kStages - 1;
-      load_stage(ahead % C::kStages, key + (C::kStages - 1) * kTileKeys);
-    }
-    const uint8_t* ks = smem + stage * 2 * C::kTile;
-    const uint8_t* vs = ks + C::kTile;
+    const uint8_t* ks = next_slot();
+    load_tile(it.K, key + kTileKeys);
     float s[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -199,6 +202,8 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
         s[j][i] = ex2(s[j][i] - ref[i >> 1]);
         l[i >> 1] += s[j][i];
       }
+    const uint8_t* vs = next_slot();
+    load_tile(it.V, key + kTileKeys);
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
       const uint32_t a[4] = {pack_bf16(s[j][0], s[j][1]), pack_bf16(s[j][2], s[j][3]),
@@ -211,7 +216,6 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
         mma_bf16(o[2 * c + 1], a, b[2], b[3]);
       }
     }
-    stage = stage + 1 == C::kStages ? 0 : stage + 1;
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -219,68 +223,55 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
   }
   cp_async_wait<0>();
-  const int64_t slot = (int64_t)it.slot * p.B * p.Hq;
-  if constexpr (WK == 1) {
+  const int64_t state = (int64_t)it.slot * p.B * p.Hq;
+  // the key groups' states of a row tile meet in shared memory
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(smem);                // [4 warps][16][D]
+  float2* sml = reinterpret_cast<float2*>(smem + 64 * D * 4);  // [4 warps][16]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = wm * 16 + g + 8 * r;
-      if (row < it.rows) {
-        const int64_t at = slot + query_row(it.row0 + row);
+  for (int r = 0; r < 2; ++r) {
+    const int row = g + 8 * r;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2*>(p.part_o + at * D + j * 8 + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
-        if (t == 0) p.part_ml[at] = make_float2(m[r], l[r]);
-      }
+    for (int j = 0; j < D / 8; ++j)
+      *reinterpret_cast<float2*>(so + (warp * 16 + row) * D + j * 8 + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+    if (t == 0) sml[warp * 16 + row] = make_float2(m[r], l[r]);
+  }
+  __syncthreads();
+  for (int i = tid; i < 16 * WM * (D / 4); i += kPfThreads) {
+    const int row = i / (D / 4), c = i % (D / 4), tile = row / 16, r = row % 16;
+    if (row >= it.rows) break;  // (rows rise with i)
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < WK; ++k) M = fmaxf(M, sml[(k * WM + tile) * 16 + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < WK; ++k) {
+      const int w = (k * WM + tile) * 16 + r;
+      const float2 ml = sml[w];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      const float4 v = *reinterpret_cast<const float4*>(so + w * D + c * 4);
+      L += f * ml.y;
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
     }
-  } else {
-    // the key groups' states of a row tile meet in shared memory
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);                // [4 warps][16][D]
-    float2* sml = reinterpret_cast<float2*>(smem + 64 * D * 4);  // [4 warps][16]
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<float2*>(so + (warp * 16 + row) * D + j * 8 + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
-      if (t == 0) sml[warp * 16 + row] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    for (int i = tid; i < 16 * WM * (D / 4); i += kPfThreads) {
-      const int row = i / (D / 4), c = i % (D / 4), tile = row / 16, r = row % 16;
-      if (row >= it.rows) break;  // (rows rise with i)
-      float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) M = fmaxf(M, sml[(k * WM + tile) * 16 + r].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < WK; ++k) {
-        const int w = (k * WM + tile) * 16 + r;
-        const float2 ml = sml[w];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        const float4 v = *reinterpret_cast<const float4*>(so + w * D + c * 4);
-        L += f * ml.y;
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-      }
-      const int64_t at = slot + query_row(it.row0 + row);
-      *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = acc;
-      if (c == 0) p.part_ml[at] = make_float2(M, L);
-    }
+    const int64_t at = state + query_row(it.row0 + row);
+    *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = acc;
+    if (c == 0) p.part_ml[at] = make_float2(M, L);
   }
 }
 
 // Blocks 0 .. prefix_blocks - 1: (slice, row tile, KV head) of the prefix, KV
 // head fastest; then (slice, sequence, KV head) of the sequences' own positions.
 template <int D, int WM>
-__global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_kernel(const PrefixParams p) {
   extern __shared__ __align__(128) uint8_t pf_smem[];
   // After the tensor-memory kernel (p.tc) these blocks run beside it: they
-  // start once all of its blocks have waited for what came before, need
-  // nothing that it writes, and wait for its end before their own, so that the
-  // merge finds both.
+  // start once all of its blocks have waited for what came before and need
+  // nothing that it writes. The last one waits for its end, so that this launch
+  // ends after it and the merge finds both (each block waiting would hold the
+  // SMs from the rest).
   const bool beside = p.tc != 0;
   if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
@@ -325,7 +316,7 @@ __global__ void __launch_bounds__(kPfThreads) prefix_kernel(const PrefixParams p
       attend<D, 1>(p, it, pf_smem);
     }
   }
-  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One query row a block: merges its partial states. First the weights of the
@@ -434,8 +425,7 @@ template <int D>
 cudaError_t prefix_launch_d(const PrefixParams& p, cudaStream_t s) {
   switch (p.row_warps) {
     case 1: return prefix_launch_t<D, 1>(p, s);
-    case 2: return prefix_launch_t<D, 2>(p, s);
-    default: return prefix_launch_t<D, 4>(p, s);
+    default: return prefix_launch_t<D, 2>(p, s);
   }
 }
 
@@ -448,13 +438,13 @@ bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d) {
 
 void prefix_plan(PrefixParams& p, int sms) {
   const int R = p.B * (p.Hq / p.Hkv);
-  const int per_sm = p.d == 256 ? 1 : p.d == 128 ? 2 : 4;
+  const int per_sm = p.d == 64 ? 4 : 2;  // blocks an SM over which a prefix is cut
   const int64_t room = (int64_t)std::min(sms, kPrefixMaxSms) * per_sm;
-  // More than 64 rows a KV head are bound by the products: tensor memory, 128
-  // rows a block, one block an SM. Else 16, 32 or 64 rows a block, the fewest
-  // row tiles, so that a slice is read as few times as its rows allow.
-  p.tc = R > 64 && p.P >= kPrefixTcMin;
-  p.row_warps = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  // More than 32 rows a KV head go to tensor memory, 128 rows a block, one block
+  // an SM (32768 positions, 2 KV heads of 256: 23.6 us at 72 rows, against 29 at
+  // 64 with the warps' products; 24.8 at 32). Else 16 or 32 rows a block.
+  p.tc = R > 32 && p.P >= kPrefixTcMin;
+  p.row_warps = R <= 16 ? 1 : 2;
   const int tile_rows = p.tc ? 128 : 16 * p.row_warps, tiles = (R + tile_rows - 1) / tile_rows;
   // slices of whole key tiles, `least` of them or more, at most `blocks` blocks
   auto slices = [&](int len, int64_t blocks, int64_t others, int keys, int least, int& slice, int& splits) {
@@ -464,8 +454,16 @@ void prefix_plan(PrefixParams& p, int sms) {
     slice = (int)((kt + want - 1) / want) * keys;
     splits = len ? (int)(((int64_t)len + slice - 1) / slice) : 0;
   };
+  // The tensor-memory kernel leaves SMs to the blocks that run beside it: by the
+  // work of both (a 64-key tile of one sequence takes about as long as one of 128
+  // rows; lengths are taken to be half of S).
+  int64_t tc_sms = std::min(sms, kPrefixMaxSms);
+  if (p.tc) {
+    const double own = 0.5 * p.S * p.B, shared = (double)p.P * tiles;
+    tc_sms = std::max<int64_t>(tc_sms / 2, (int64_t)(tc_sms * (shared / (own + shared))));
+  }
   // the prefix in one wave of blocks; the sequences' own positions, ragged, in up to four of shorter ones
-  slices(p.P, p.tc ? std::min(sms, kPrefixMaxSms) : room, (int64_t)p.Hkv * tiles, p.tc && p.d != 256 ? 128 : kTileKeys, 1,
+  slices(p.P, p.tc ? tc_sms : room, (int64_t)p.Hkv * tiles, p.tc && p.d != 256 ? 128 : kTileKeys, 1,
          p.prefix_slice, p.prefix_splits);
   slices(p.S, 4 * room, (int64_t)p.Hkv * p.B, kTileKeys, 2, p.suffix_slice, p.suffix_splits);
   p.prefix_blocks = p.prefix_splits * p.Hkv * tiles;

@@ -1,4 +1,4 @@
-// Attention over a shared prefix for many query rows (more than 64 a KV head):
+// Attention over a shared prefix for many query rows (more than 32 a KV head):
 // the partial states of prefix.cu from tcgen05 products.
 //
 // A CTA takes one KV head, 128 query rows and one slice of the prefix. Per tile

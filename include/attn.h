@@ -72,8 +72,8 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a
  * KV head. Scores and softmax in fp32; the softmax weights are rounded to bf16
  * before they multiply the values (fp32 sums). Two or three launches: partial
- * states over slices of the prefix and of the sequences' own positions (from
- * more than 64 query rows a KV head the prefix has a launch of its own), then
+ * states over slices of the prefix and of the sequences' own positions (with
+ * more than 32 query rows a KV head the prefix has a launch of its own), then
  * their merge in a fixed order. Each is a programmatic dependent of the launch
  * before it on the stream.
  */

@@ -57,9 +57,9 @@ SHAPES = [(1, 1, 1, 2, 2, 64), (1, 0, 5, 16, 2, 256), (3, 64, 0, 16, 2, 128), (2
           (5, 129, 33, 12, 4, 128), (8, 8192, 200, 32, 8, 128), (9, 1000, 70, 16, 1, 64), (17, 333, 130, 8, 8, 64), (64, 2049, 65, 16, 2, 256),
           (33, 500, 9, 6, 2, 256), (2, 30000, 3, 3, 1, 128), (1, 20000, 3000, 16, 2, 256), (40, 0, 300, 8, 1, 128), (150, 90, 20, 16, 2, 64),
           (4, 4096, 64, 16, 1, 256),
-          # more than 64 rows a KV head and at least 512 shared positions: the tensor-memory kernel
+          # more than 32 rows a KV head and at least 256 shared positions: the tensor-memory kernel
           (70, 512, 0, 3, 3, 64), (16, 513, 3, 16, 2, 128), (40, 1000, 30, 8, 2, 128), (13, 700, 10, 16, 1, 256), (20, 4099, 10, 12, 2, 256),
-          (65, 9000, 70, 2, 2, 128), (100, 30011, 9, 10, 1, 64), (64, 20000, 100, 16, 2, 256)]
+          (65, 9000, 70, 2, 2, 128), (100, 30011, 9, 10, 1, 64), (64, 20000, 100, 16, 2, 256), (5, 256, 40, 16, 2, 128), (33, 257, 0, 2, 2, 64), (5, 700, 70, 16, 2, 256)]
 
 
 @gpu
