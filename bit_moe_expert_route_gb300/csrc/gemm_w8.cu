@@ -65,8 +65,11 @@ MOE_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, 
 
 // 16 M weight rows x 8 NT tokens a block.
 template <int M, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_few_kernel(const GemmW8Params p) {
-  constexpr int U = M == 1 ? 4 : M == 2 ? 2 : 1;  // 64-code steps in flight (8 weight loads a lane)
+__global__ void __launch_bounds__(32 * kFewWarps, M > 1 || NT <= 2 ? 3 : 2) gemm_w8_few_kernel(const GemmW8Params p) {
+  // 64-code steps in flight. Blocks of many rows hide their loads behind each
+  // other: three an SM with one step each beat two with two (52 us against 56 for
+  // 24 tokens by 100003 x 2048 weights, 42 against 47 for 16).
+  constexpr int U = M == 1 ? 4 : 1;
   constexpr int kPitch = 16 * M + 4;
   __shared__ float red[kFewWarps][8 * NT][kPitch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, M * NT <= 2 ? 3 : 2) gemm_w8_f
   const int s0 = warp * per, s1 = min(steps, s0 + per);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status) *p.status = 0;
   float acc[M][NT][4];
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -566,7 +569,7 @@ cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
   const int nt = (p.T + 7) / 8;
   const bool many_rows = p.N >= 32 * 4 * sms;  // several blocks an SM even with 32 or 64 rows each
   // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
-  // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 49 and 55 us with
+  // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
   // 32 rows at 16 and 24, against 62 and 56 in tensor memory, which is ahead
   // from 25 (48 against 63 at 32).
   if (many_rows && nt <= 3) {

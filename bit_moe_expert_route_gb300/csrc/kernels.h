@@ -270,7 +270,7 @@ struct LogprobParams {
 cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integer product
-constexpr int kW8FewTokens = 24;  // up to here no workspace beyond the status word
+constexpr int kW8FewTokens = 24;  // up to here no scratch, and no wait that could fail
 struct GemmW8Params {
   const int8_t* a;           // [T], rows lda apart
   int64_t lda;
@@ -281,7 +281,7 @@ struct GemmW8Params {
   void* out;                 // bf16 or fp32, rows ldo apart
   int64_t ldo;
   uint16_t* a16;             // scratch f16 [T][K] (T > kW8FewTokens)
-  int32_t* status;
+  int32_t* status;           // or null (T <= kW8FewTokens)
 };
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
 

@@ -13,10 +13,10 @@
 //
 // A block: 4 warps, WM of them over 16-row tiles and 4 / WM over the keys of
 // each 64-key tile, so that a few rows still use every warp. K and V tiles
-// come through a ring of cp.async slots; m16n8k16 products with fp32 sums,
-// the weights rounded to bf16 for the second product (their rounding, 2^-9
-// each, averages out over the positions; the sum l adds them unrounded). The
-// running maximum moves only when a score passes it by 2^8, which fp32 and
+// come through a ring of cp.async slots; m16n8k16 products with fp32 sums. The
+// weights enter the second product as two bf16 parts: with one, a row of few
+// positions would carry its weights' rounding (2^-8 each) to the output, and
+// these products wait for memory anyway. The running maximum moves only when a score passes it by 2^8, which fp32 and
 // bf16 hold without loss, so the output is rarely rescaled. (With more than 32
 // rows a KV head the prefix goes to prefix_tc.cu; the sequences' own positions
 // stay here.)
@@ -59,6 +59,12 @@ MOE_DEVINL void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uin
 MOE_DEVINL uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Two values as bf16, and what that leaves of them as bf16 too (2^-17 in all).
+MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x, y);
+  lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of D bf16 a row: chunks
@@ -206,14 +212,17 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
     load_tile(it.V, key + kTileKeys);
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
-      const uint32_t a[4] = {pack_bf16(s[j][0], s[j][1]), pack_bf16(s[j][2], s[j][3]),
-                             pack_bf16(s[j + 1][0], s[j + 1][1]), pack_bf16(s[j + 1][2], s[j + 1][3])};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_bf16(s[j + (q >> 1)][2 * (q & 1)], s[j + (q >> 1)][2 * (q & 1) + 1], hi[q], lo[q]);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t b[4];
         ldsm4_t(b, smem_u32(vs + tile_off<D>(wk * KS + j * 8 + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * c + (lane >> 4))));
-        mma_bf16(o[2 * c], a, b[0], b[1]);
-        mma_bf16(o[2 * c + 1], a, b[2], b[3]);
+        mma_bf16(o[2 * c], hi, b[0], b[1]);
+        mma_bf16(o[2 * c + 1], hi, b[2], b[3]);
+        mma_bf16(o[2 * c], lo, b[0], b[1]);
+        mma_bf16(o[2 * c + 1], lo, b[2], b[3]);
       }
     }
   }

@@ -14,6 +14,10 @@
 // these tiles: what bounds the kernel at head size 256 is the rate at which an
 // SM takes K and V in from L2 (64 KB for 64 keys, against 1312 cycles of MMAs).
 //
+// The weights are rounded to bf16 once (2^-8 of each at most; with hundreds of
+// positions the roundings average out, to about the output's own): a second
+// part would make the outputs' products, half of all, twice as many.
+//
 // The reference m moves only when a score passes it by 2^8; then the warp waits
 // for the products before and rescales its rows of O in tensor memory.
 #include <cuda.h>

@@ -84,6 +84,8 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
   return cuda_status(moe::norm_launch(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
+static_assert(moe::kW8FewTokens == MOE_W8A8_NO_WORKSPACE_T, "the header's promise");
+
 size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K) {
   if (T < 0 || N < 1 || K < 16 || K > 65536 || K % 16 != 0) return 0;
   // the status word, then the tokens' codes as f16
@@ -101,7 +103,7 @@ int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
       !aligned(out, type == MOE_F32 ? 4 : 2))
     return MOE_ERR_ALIGN;
-  if (!ws || !aligned(ws, 256) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (ws ? !aligned(ws, 256) || ws_bytes < need : T > moe::kW8FewTokens) return MOE_ERR_WORKSPACE;
   const int sms = device_sms();
   if (sms < 0) return sms;
   moe::GemmW8Params p;
@@ -117,7 +119,7 @@ int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8
   p.out = out;
   p.ldo = ldo;
   p.status = static_cast<int32_t*>(ws);
-  p.a16 = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + 256);
+  p.a16 = ws ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + 256) : nullptr;
   return cuda_status(moe::gemm_w8_launch(p, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -384,7 +384,8 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
         pr = _want(fn, "residual", residual, bf, shape)
         if residual_out is None:
             residual_out = torch.empty(shape, dtype=bf, device=dev)
-    if residual_out is not None:
+            po = residual_out.data_ptr()
+    if residual_out is not None and po is None:
         po = _want(fn, "residual_out", residual_out, bf, shape)
     q = torch.empty(shape, dtype=dtype, device=dev)
     scale = torch.empty(T, dtype=torch.float32, device=dev)
@@ -395,6 +396,9 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
                                   scale.data_ptr(), pv, _stream(stream))
     _check("moe_add_rmsnorm_q8", rc)
     return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
+
+
+W8A8_NO_WORKSPACE_T = 24
 
 
 def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -416,14 +420,20 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     pt = _want(fn, "w_scale", w_scale, f32, (N,))
     if out is None:
         out = torch.empty((T, N), dtype=dtype, device=dev)
-    po = _want(fn, "out", out, dtype, (T, N), rows=True)
-    if ws is None:
+        po = out.data_ptr()
+    else:
+        po = _want(fn, "out", out, dtype, (T, N), rows=True)
+    pws, nbytes = None, 0
+    if ws is not None:
+        pws, nbytes = ws.data_ptr(), ws.numel()
+    elif T > W8A8_NO_WORKSPACE_T:
         nbytes = lib().moe_gemm_w8a8_workspace_bytes(T, N, K)
         if nbytes == 0:
             raise MoeError("moe_gemm_w8a8_workspace_bytes", -3)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        pws = ws.data_ptr()
     rc = lib().moe_gemm_w8a8(pa, _ld(a), ps, pw, pt, T, N, K, _FLOAT_TYPES[dtype], po, _ld(out),
-                             ws.data_ptr(), ws.numel(), _stream(stream))
+                             pws, nbytes, _stream(stream))
     _check("moe_gemm_w8a8", rc)
     return out
 
@@ -449,7 +459,9 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         pl = _want(fn, "lens", lens, torch.int32, (B,))
     if out is None:
         out = torch.empty((B, Hq, d), dtype=bf, device=dev)
-    po = _want(fn, "out", out, bf, (B, Hq, d))
+        po = out.data_ptr()
+    else:
+        po = _want(fn, "out", out, bf, (B, Hq, d))
     if ws is None:
         nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
         if nbytes == 0:

@@ -64,13 +64,15 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
  *   out      bf16 or fp32 (`type`, moe_float_type) [T][N], rows ldo >= N
  *            elements apart
  *   ws       256-byte aligned, >= moe_gemm_w8a8_workspace_bytes(T, N, K) bytes
- *            (no initialisation needed), holds the status word
+ *            (no initialisation needed), holds the status word; may be NULL
+ *            for up to MOE_W8A8_NO_WORKSPACE_T tokens
  * a and w 16-byte aligned; T >= 0 (0 launches nothing), N >= 1, K a multiple of
  * 16, 16 <= K <= 65536. The integer sum is exact while its partial sums stay
  * below 2^24 in magnitude (always for K <= 1024), else it carries fp32
  * rounding; the scales multiply it in fp32 and the result is rounded once. One
  * launch for few tokens or little work, else two.
  */
+#define MOE_W8A8_NO_WORKSPACE_T 24
 size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K);
 int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
                   const float* w_scale, int T, int N, int K, int type, void* out, int64_t ldo,
