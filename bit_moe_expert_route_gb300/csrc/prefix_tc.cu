@@ -11,8 +11,11 @@
 // K and V tiles come by TMA into one ring of slots in the order in which the
 // products use them (K0 K1 V0 K2 V1 ...); V is read as it lies (MN-major
 // operand, no transpose). Every query row of a KV head's sequences shares
-// these tiles: what bounds the kernel at head size 256 is the rate at which an
-// SM takes K and V in from L2 (64 KB for 64 keys, against 1312 cycles of MMAs).
+// these tiles. At head size 256 with 512 rows a tile of 64 keys takes 0.89 us
+// (about 1700 cycles), 1312 of them the MMAs' (16 of N = 64 at their least time
+// of 50, 4 of N = 256 at 128). Few rows and a long prefix are bound by HBM: 128
+// rows, 8 KV heads of 128, 131072 positions in 87 us, 6.1 TB/s. (Asking L2 for
+// tiles ahead of the ring made that 121 us.)
 //
 // The weights are rounded to bf16 once (2^-8 of each at most; with hundreds of
 // positions the roundings average out, to about the output's own): a second
@@ -87,12 +90,6 @@ MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
   return d;
 }
 
-constexpr int kAhead = 6;  // tiles from which L2 is asked before the ring loads them
-MOE_DEVINL void prefetch_tile(const void* desc, int32_t c0, int32_t c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(desc)), "r"(c0), "r"(c1)
-               : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ TcArgs args) {
   using C = TcCfg<D>;
@@ -159,21 +156,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         if (++slot == NS) slot = 0, phase ^= 1;
         return true;
       };
-      // The ring holds two and a half tiles, less than HBM's latency: tiles are
-      // asked into L2 ahead of it, each by one of the row tiles' CTAs that read it.
-      auto prefetch = [&](int i) {
-        if (i < n && i % tiles == tile) {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            prefetch_tile(&args.tm_k, h * D + c * 64, k0 + i * KT);
-            prefetch_tile(&args.tm_v, h * D + c * 64, k0 + i * KT);
-          }
-        }
-      };
-      for (int i = 0; i < kAhead; ++i) prefetch(i);
       alive = load(&args.tm_k, k0);
       for (int i = 0; i < n && alive; ++i) {
-        prefetch(i + kAhead);
         if (i + 1 < n) alive = load(&args.tm_k, k0 + (i + 1) * KT);
         if (alive) alive = load(&args.tm_v, k0 + i * KT);
       }
