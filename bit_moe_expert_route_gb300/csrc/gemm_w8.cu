@@ -185,15 +185,18 @@ __global__ void __launch_bounds__(256) widen_kernel(const GemmW8Params p) {
 constexpr int kTileN = 128;               // weight rows a tile (the MMA's M)
 constexpr int kKB = 128;                  // codes a k-block
 constexpr int kQStage = kTileN * kKB;     // packed codes of a stage: 16 KB
-constexpr int kConvGroups = 4;             // four warps each; group i converts k-blocks i, i + 4, ...
 constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 4 + 4 * kConvGroups;
-constexpr int kManyThreads = 32 * (kEpiWarp0 + kEpiWarps);  // by role, below
 
 template <int BN>
 struct CfgW8 {
+  // Converter groups of four warps; group i converts k-blocks i, i + kGroups, ...
+  // At 256 tokens two keep up with the MMAs, and the threads saved leave the
+  // epilogue registers for 64 columns at a time.
+  static constexpr int kGroups = BN == 256 ? 2 : 4;
+  static constexpr int kEpiWarp0 = 4 + 4 * kGroups;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);  // by role, below
   static constexpr int kSQ = 4;                  // packed-code stages
-  static constexpr int kSA = kConvGroups;        // f16 weight stages in tensor memory, 64 columns each
+  static constexpr int kSA = 4;                  // f16 weight stages in tensor memory, 64 columns each
   // Token stages of kBK codes. 256 tokens leave room for 160 KB of them beside
   // the packed codes: five stages of half a k-block.
   static constexpr int kBK = BN == 256 ? 64 : 128;
@@ -221,7 +224,7 @@ struct CfgW8 {
   // A group waits for its k-block's stage while earlier k-blocks may still be
   // loading: with fewer stages than groups it would wait on a barrier that is
   // two phases behind, whose parity looks like the phase it wants.
-  static_assert(kSQ >= kConvGroups, "every converter group needs a stage of its own");
+  static_assert(kSQ % kGroups == 0 && kSA % kGroups == 0, "every converter group needs stages of its own");
 };
 
 struct W8Args {
@@ -244,10 +247,11 @@ MOE_DEVINL void warp_arrive(uint64_t* bar) {
 }
 
 // Roles: warp 0 streams the packed weights, warp 1 issues the MMAs, warp 2
-// streams the tokens' operand, warps 4-19 convert, warps 20-27 write out.
+// streams the tokens' operand (with two issuers warp 3 is the other), then the
+// converters' warps and the epilogue's.
 // Tiles of 128 weight rows by BN tokens, weights fastest, one CTA an SM.
 template <int BN, bool F32>
-__global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_constant__ W8Args args) {
+__global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const __grid_constant__ W8Args args) {
   using C = CfgW8<BN>;
   const GemmW8Params& g = args.g;
   extern __shared__ uint8_t smem_raw[];
@@ -400,15 +404,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
       mbar_wait(drain, 0, abort_flag, g.status, 67);
     }
-  } else if (warp >= 4 && warp < kEpiWarp0) {
-    // thread = one weight row of every kConvGroups-th k-block: a k-block takes
+  } else if (warp >= 4 && warp < C::kEpiWarp0) {
+    // thread = one weight row of every kGroups-th k-block: a k-block takes
     // its group about 1000 cycles from wait to signal, most of it latency, so
     // several are under way at once
     const int m = (warp & 3) * 32 + lane, group = (warp - 4) >> 2;
-    const uint32_t a_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kACol + group * (kKB / 2);
+    const uint32_t a_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kACol;
     const int64_t mine = blockIdx.x < units ? ((units - 1 - blockIdx.x) / gridDim.x + 1) * KB : 0;  // this CTA's k-blocks
-    for (int64_t it = group; it < mine; it += kConvGroups) {
-      const int sq = (int)(it % C::kSQ);
+    for (int64_t it = group; it < mine; it += C::kGroups) {
+      const int sq = (int)(it % C::kSQ), sa = (int)(it % C::kSA);
       if (!warp_wait(&q_full[sq], (uint32_t)(it / C::kSQ) & 1, abort_flag, g.status, 68)) break;
       uint4 q[8];
 #pragma unroll
@@ -431,19 +435,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
             r[8 * c + 2 * i + 1] = v.y;
           }
         }
-        tmem_st_32x32b_x16(a_tmem + h * 16, r);
+        tmem_st_32x32b_x16(a_tmem + sa * (kKB / 2) + h * 16, r);
       }
       warp_arrive(&q_empty[sq]);  // (its codes were consumed)
       tc_wait_st();
       tc_fence_before();
-      warp_arrive(&a_full[group]);
+      warp_arrive(&a_full[sa]);
     }
-  } else if (warp >= kEpiWarp0) {
+  } else if (warp >= C::kEpiWarp0) {
     // lanes of quarter warp % 4 = 32 weight rows; the two groups of four warps take half the tokens each
-    const int quarter = warp & 3, group = (warp - kEpiWarp0) >> 2;
-    constexpr int kCols = BN / 2, kChunk = C::kIssuers == 2 ? 16 : 32;
+    const int quarter = warp & 3, group = (warp - C::kEpiWarp0) >> 2;
+    constexpr int kCols = BN / 2, kChunk = C::kIssuers == 2 ? 16 : BN == 256 ? 64 : 32;
     using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    float4* scales = reinterpret_cast<float4*>(smem + C::kOffScale + (warp - kEpiWarp0) * 128);
+    float4* scales = reinterpret_cast<float4*>(smem + C::kOffScale + (warp - C::kEpiWarp0) * 128);
     uint32_t tile = 0;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
       const uint32_t buf = tile % C::kAcc;
@@ -469,40 +473,45 @@ __global__ void __launch_bounds__(kManyThreads, 1) gemm_w8_kernel(const __grid_c
             for (int i = 0; i < kChunk; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(v2[i]));
           }
         } else {
-          tmem_ld_32x32b_x32(taddr + c0, v);
+#pragma unroll
+          for (int i = 0; i < kChunk; i += 32) tmem_ld_32x32b_x32(taddr + c0 + i, reinterpret_cast<uint32_t(&)[32]>(v[i]));
           tc_wait_ld();
         }
         if (c0 + kChunk == kCols) {  // the accumulator is in registers: the next tile may start
           tc_fence_before();
           warp_arrive(&acc_empty[buf]);
         }
-        const int t = t0 + c0, live = g.T - t;
-        __syncwarp();
-        reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
-        __syncwarp();
-        Out* dst = static_cast<Out*>(g.out) + (int64_t)t * g.ldo + n;
-        auto put = [&](uint32_t acc, float as) {
-          const float y = __uint_as_float(acc) * as * ws;
-          if constexpr (F32)
-            *dst = y;
-          else
-            *dst = __float2bfloat16_rn(y);
-          dst += g.ldo;
-        };
-        if (n < g.N) {  // one row of 32 outputs a store
-          if (live >= kChunk) {
+        constexpr int kPut = kChunk < 32 ? kChunk : 32;  // tokens whose scales are at hand
 #pragma unroll
-            for (int i = 0; i < kChunk / 4; ++i) {
-              const float4 as = scales[i];
-              put(v[4 * i], as.x);
-              put(v[4 * i + 1], as.y);
-              put(v[4 * i + 2], as.z);
-              put(v[4 * i + 3], as.w);
+        for (int i0 = 0; i0 < kChunk; i0 += kPut) {
+          const int t = t0 + c0 + i0, live = g.T - t;
+          __syncwarp();
+          reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
+          __syncwarp();
+          Out* dst = static_cast<Out*>(g.out) + (int64_t)t * g.ldo + n;
+          auto put = [&](uint32_t acc, float as) {
+            const float y = __uint_as_float(acc) * as * ws;
+            if constexpr (F32)
+              *dst = y;
+            else
+              *dst = __float2bfloat16_rn(y);
+            dst += g.ldo;
+          };
+          if (n < g.N) {  // one row of 32 outputs a store
+            if (live >= kPut) {
+#pragma unroll
+              for (int i = 0; i < kPut / 4; ++i) {
+                const float4 as = scales[i];
+                put(v[i0 + 4 * i], as.x);
+                put(v[i0 + 4 * i + 1], as.y);
+                put(v[i0 + 4 * i + 2], as.z);
+                put(v[i0 + 4 * i + 3], as.w);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kPut; ++i)
+                if (i < live) put(v[i0 + i], reinterpret_cast<const float*>(scales)[i]);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i)
-              if (i < live) put(v[i], reinterpret_cast<const float*>(scales)[i]);
           }
         }
       }
@@ -553,7 +562,7 @@ cudaError_t many_launch_t(const GemmW8Params& p, int sms, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   const int64_t units = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.T + BN - 1) / BN);
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, units));
-  cfg.blockDim = dim3(kManyThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   return cudaLaunchKernelEx(&cfg, gemm_w8_kernel<BN, F32>, args);
 }
