@@ -16,16 +16,15 @@
 // multiply-add: about four instructions an element with its ex2.
 //
 // Top k (k <= 32): a warp holds its best 32 in order, one a lane, and inserts
-// what reaches the block's threshold (a lower bound of the row's k-th best: the
-// best k-th place of any warp). The threshold starts from the thread maxima of
-// the block's first pass, so that only a few elements a pass ever reach the
-// insertion. Ties go to the lower index: entries are 64-bit keys (value in
+// what reaches the block's threshold, a lower bound of the row's k-th best. It starts from the thread
+// maxima of the block's first pass, so that only a few elements a pass ever
+// reach the insertion. Ties go to the lower index: entries are 64-bit keys (value in
 // order, then the index reversed), and an element equal to the threshold is
 // still inserted.
 //
-// Many rows: one block a row. Few rows: a cluster of 2, 4 or 8 blocks shares a
-// row and the first block merges their states from distributed shared memory,
-// so one launch suffices at every size.
+// Many rows: one block a row (short rows: one warp). Few rows: a cluster of 2, 4
+// or 8 blocks shares a row and the first block merges their states from
+// distributed shared memory, so one launch suffices at every size.
 #include <cmath>
 
 #include "common.cuh"
@@ -229,7 +228,7 @@ struct LpShared {
   uint64_t row_list[32];  // the block's results, read by the cluster's first block
   Sums row_sums;
   uint4 scratch[kLpWarps][kUnroll];  // a lane's vectors, looked at by its warp
-  uint32_t threshold;     // rank that an element has to reach
+  uint32_t kth[kLpWarps], qth[kLpWarps];  // the ranks of each warp's k-th and q-th best so far
 };
 
 // The best 32 of n lists in shared memory (n a power of two <= 8) into
@@ -257,23 +256,39 @@ MOE_DEVINL float remote_f32(uint32_t a) {
   return v;
 }
 
-template <bool F32, bool TOP>
+// Sums of the first n lanes, joined in every lane (n a power of two).
+MOE_DEVINL void join_lanes(Sums& s, int n) {
+  for (int off = n / 2; off > 0; off >>= 1) {
+    Sums o;
+    o.ref = __shfl_xor_sync(0xffffffffu, s.ref, off);
+    o.S = __shfl_xor_sync(0xffffffffu, s.S, off);
+    o.U = __shfl_xor_sync(0xffffffffu, s.U, off);
+    o.top = __shfl_xor_sync(0xffffffffu, s.top, off);
+    merge(s, o);
+  }
+}
+
+// W warps a row: 8 (a block's, or a cluster's of such blocks), or 1 (eight rows
+// a block, with no barrier).
+template <bool F32, bool TOP, int W>
 __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobParams p) {
-  constexpr int E = kVecElems<F32>;
+  constexpr int E = kVecElems<F32>, T = 32 * W;
   __shared__ LpShared sh;
   uint32_t rank, ranks;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const int64_t row = blockIdx.x / ranks;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = W == 1 ? 0 : warp, tid = wr * 32 + lane;  // in the row
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * kLpWarps + warp : blockIdx.x / ranks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (W == 1 && row >= p.N) return;
   const char* base = static_cast<const char*>(p.logits) + row * p.ld * (F32 ? 4 : 2);
   const int lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) / (F32 ? 4 : 2));
   // the row's vectors, the first one starting `lead` elements before it, in
   // contiguous parts for the cluster's blocks
   const int nvec = (lead + p.V + E - 1) / E, part = (nvec + (int)ranks - 1) / (int)ranks;
   const int v0 = (int)rank * part, v1 = min(nvec, v0 + part);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" :::);
   Sums s;
   s.ref = kLowest;
   s.S = 0.f;
@@ -282,17 +297,27 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
   uint64_t mine = 0;  // this lane's entry of the warp's list, 0 = none
   uint32_t bar = 0;   // the rank that an element has to reach, and its value
   float bar_z = -INFINITY;
+  // Two bounds of the row's k-th best from below, which need no list but a
+  // warp's own and may be read while others raise theirs: any warp's k-th best
+  // (near for small k), and, with n warps' q-th best places, q n >= k, the least
+  // of those (near for large k). n counts warps whose lanes all have elements.
+  const int full = W == 1 ? 1 : min(W, max(1, (v1 - v0) / 32)), q = TOP ? (p.k + full - 1) / full : 1;
+  auto shared_bar = [&]() {
+    const int w = lane & (W - 1);
+    const uint32_t kth = *reinterpret_cast<volatile uint32_t*>(&sh.kth[w]), qth = *reinterpret_cast<volatile uint32_t*>(&sh.qth[w]);
+    return max(__reduce_max_sync(0xffffffffu, kth), __reduce_min_sync(0xffffffffu, w < full ? qth : 0xFFFFFFFFu));
+  };
   // vectors [in0, in1) lie inside the row: a pass of only those is plain loads
   const int in0 = lead ? 1 : 0, in1 = (lead + p.V) / E;
   const uint4* vecs = reinterpret_cast<const uint4*>(base - lead * (F32 ? 4 : 2));
   auto load = [&](int v, uint4 (&w)[kUnroll]) {
-    if (v >= in0 && v + kUnroll * kLpThreads <= min(v1, in1)) {
+    if (v >= in0 && v + kUnroll * T <= min(v1, in1)) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) w[i] = __ldg(vecs + v + tid + i * kLpThreads);
+      for (int i = 0; i < kUnroll; ++i) w[i] = __ldg(vecs + v + tid + i * T);
     } else {
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        const int vi = v + i * kLpThreads + tid;
+        const int vi = v + i * T + tid;
         w[i] = vi < v1 ? load_vec<F32>(base, (int64_t)vi * E - lead, p.V) : none_vec<F32>();
       }
     }
@@ -300,9 +325,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
   uint4 w[kUnroll];
   load(v0, w);
 #pragma unroll 1
-  for (int v = v0; v < v1; v += kUnroll * kLpThreads) {
+  for (int v = v0; v < v1; v += kUnroll * T) {
     uint4 next[kUnroll];
-    load(v + kUnroll * kLpThreads, next);  // in flight while these are summed
+    load(v + kUnroll * T, next);  // in flight while these are summed
     const float m = largest<F32, kUnroll>(w);
     if (v == v0) {
       s.ref = fminf(fmaxf(m, kLowest), -kLowest);  // (NaN: the lowest)
@@ -310,18 +335,22 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         // the k-th largest of the threads' maxima bounds the k-th largest element
         // from below. A thread without elements counts as nothing (rank 0).
         const uint32_t sorted = sort32(v + tid < v1 ? rank_of(m) : 0u, lane);
-        sh.list[warp][lane] = ((uint64_t)sorted << 32);
-        merge_lists(sh.list, kLpWarps, warp, lane);
-        bar = (uint32_t)(sh.list[0][p.k - 1] >> 32);
-        if (tid == 0) sh.threshold = bar;
-        __syncthreads();
+        if constexpr (W == 1) {
+          bar = __shfl_sync(0xffffffffu, sorted, p.k - 1);
+        } else {
+          sh.list[warp][lane] = ((uint64_t)sorted << 32);
+          merge_lists(sh.list, kLpWarps, warp, lane);
+          bar = (uint32_t)(sh.list[0][p.k - 1] >> 32);
+          if (lane == 0) sh.kth[warp] = sh.qth[warp] = bar;
+          __syncthreads();
+        }
         bar_z = bar > 1 ? key_value(bar) : -INFINITY;
       }
     }
     add_vecs<F32>(s, w, m);
     // (a NaN hides the other elements: those are looked at)
     if (TOP && __any_sync(0xffffffffu, !(m < bar_z))) {
-      bar = max(bar, *reinterpret_cast<volatile uint32_t*>(&sh.threshold));
+      if (W > 1) bar = max(bar, shared_bar());
       unsigned hit = __ballot_sync(0xffffffffu, m != m || rank_of(m) >= bar);
       while (hit) {  // one lane's vectors at a time, through shared memory: an element a lane
         const int src = __ffs(hit) - 1;
@@ -331,7 +360,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
           for (int i = 0; i < kUnroll; ++i) sh.scratch[warp][i] = w[i];
         }
         __syncwarp();
-        const int vi = v + (lane / E) * kLpThreads + warp * 32 + src;
+        const int vi = v + (lane / E) * T + wr * 32 + src;
         const int64_t index = (int64_t)vi * E - lead + lane % E;
         uint64_t key = 0;
         if (lane < kUnroll * E && vi < v1 && index >= 0 && index < p.V) {
@@ -349,70 +378,64 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
           else if (lane > at) mine = up;
         }
       }
-      // the warp's k-th best may raise the block's threshold
-      const uint32_t kth = (uint32_t)(__shfl_sync(0xffffffffu, mine, p.k - 1) >> 32);
-      if (kth > bar) {
-        bar = kth;
-        if (lane == 0) atomicMax(&sh.threshold, kth);
+      // the warp's own places may raise the threshold
+      const uint32_t place = (uint32_t)(mine >> 32);
+      bar = max(bar, __shfl_sync(0xffffffffu, place, p.k - 1));
+      if constexpr (W > 1) {
+        if (lane == q - 1 && place > sh.qth[warp]) *reinterpret_cast<volatile uint32_t*>(&sh.qth[warp]) = place;
+        if (lane == p.k - 1 && place > sh.kth[warp]) *reinterpret_cast<volatile uint32_t*>(&sh.kth[warp]) = place;
       }
       bar_z = bar > 1 ? key_value(bar) : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) w[i] = next[i];
   }
-  // the block's sums and list
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Sums o;
-    o.ref = __shfl_xor_sync(0xffffffffu, s.ref, off);
-    o.S = __shfl_xor_sync(0xffffffffu, s.S, off);
-    o.U = __shfl_xor_sync(0xffffffffu, s.U, off);
-    o.top = __shfl_xor_sync(0xffffffffu, s.top, off);
-    merge(s, o);
-  }
-  if (lane == 0) sh.sums[warp] = s;
-  if (TOP) {
-    sh.list[warp][lane] = mine;  // (its last readers passed a barrier in the first pass)
-    merge_lists(sh.list, kLpWarps, warp, lane);
-  } else {
-    __syncthreads();
-  }
-  if (warp == 0) {
-    if (lane == 0) {
-      for (int w = 1; w < kLpWarps; ++w) merge(s, sh.sums[w]);
-      sh.row_sums = s;
+  join_lanes(s, 32);
+  uint64_t best = mine;  // lane i: the row's i-th
+  if constexpr (W > 1) {
+    // the block's sums and list, in warp 0
+    if (lane == 0) sh.sums[warp] = s;
+    if (TOP) {
+      sh.list[warp][lane] = mine;
+      merge_lists(sh.list, kLpWarps, warp, lane);
+    } else {
+      __syncthreads();
     }
-    if (TOP) sh.row_list[lane] = sh.list[0][lane];
-  }
-  if (ranks > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      if (TOP) {
-        if (warp < (int)ranks) {
-          uint64_t e;
-          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(e) : "r"(remote_addr(&sh.row_list[lane], warp)) : "memory");
-          sh.list[warp][lane] = e;
-        }
-        merge_lists(sh.list, (int)ranks, warp, lane);
-      }
-      if (tid == 0) {
-        for (uint32_t r = 1; r < ranks; ++r) {
-          const uint32_t a = remote_addr(&sh.row_sums, r);
-          Sums o;
-          o.ref = remote_f32(a);
-          o.S = remote_f32(a + 4);
-          o.U = remote_f32(a + 8);
-          o.top = remote_f32(a + 12);
-          merge(s, o);
-        }
-        sh.row_sums = s;
-      }
+    if (warp == 0) {
+      s = sh.sums[lane & (kLpWarps - 1)];
+      join_lanes(s, kLpWarps);
+      if (TOP) best = sh.list[0][lane];
     }
-    cluster_sync();  // the other blocks' shared memory stays until the first has read it
-    if (rank != 0) return;
+    if (ranks > 1) {
+      if (warp == 0) {
+        if (lane == 0) sh.row_sums = s;
+        if (TOP) sh.row_list[lane] = best;
+      }
+      cluster_sync();
+      if (rank == 0) {
+        if (TOP) {
+          if (warp < (int)ranks) {
+            uint64_t e;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(e) : "r"(remote_addr(&sh.row_list[lane], warp)) : "memory");
+            sh.list[warp][lane] = e;
+          }
+          merge_lists(sh.list, (int)ranks, warp, lane);
+        }
+        if (warp == 0) {
+          const uint32_t a = remote_addr(&sh.row_sums, lane & (ranks - 1));
+          s.ref = remote_f32(a);
+          s.S = remote_f32(a + 4);
+          s.U = remote_f32(a + 8);
+          s.top = remote_f32(a + 12);
+          join_lanes(s, (int)ranks);
+          if (TOP) best = sh.list[0][lane];
+        }
+      }
+      cluster_sync();  // the other blocks' shared memory stays until the first has read it
+      if (rank != 0) return;
+    }
+    if (warp != 0) return;
   }
-  __syncthreads();
-  s = sh.row_sums;
   const bool none = s.top == -INFINITY;   // nothing but -infinity
   const bool bad = !(s.top <= -kLowest);  // +infinity or NaN
   const float nan = __int_as_float(0x7fc00000);
@@ -422,7 +445,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
     if (bad) return nan;
     return none || z == -INFINITY ? -INFINITY : (z - s.ref) - logS;
   };
-  if (tid == 32 && p.logprob) {
+  if (lane == 0 && p.logprob) {
     const int id = p.ids[row];
     float lp = nan;
     if (id >= 0 && id < p.V)
@@ -430,18 +453,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
                      : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(base)[id]));
     p.logprob[row] = lp;
   }
-  if (tid == 64 && p.entropy) p.entropy[row] = bad ? nan : none ? 0.f : fmaxf(logS - s.U / s.S, 0.f);
-  if (TOP && tid < p.k) {
-    const uint64_t e = sh.list[0][tid];
-    p.top_ids[row * p.k + tid] = (int)~(uint32_t)e;
-    p.top_logprobs[row * p.k + tid] = log_p(key_value((uint32_t)(e >> 32)));
+  if (lane == 1 && p.entropy) p.entropy[row] = bad ? nan : none ? 0.f : fmaxf(logS - s.U / s.S, 0.f);
+  if (TOP && lane < p.k) {
+    p.top_ids[row * p.k + lane] = (int)~(uint32_t)best;
+    p.top_logprobs[row * p.k + lane] = log_p(key_value((uint32_t)(best >> 32)));
   }
 }
 
-template <bool F32, bool TOP>
+template <bool F32, bool TOP, int W>
 cudaError_t logprob_launch_t(const LogprobParams& p, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.N * cluster));
+  cfg.gridDim = dim3((unsigned)(W == 1 ? ((int64_t)p.N + kLpWarps - 1) / kLpWarps : (int64_t)p.N * cluster));
   cfg.blockDim = dim3(kLpThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -453,19 +475,26 @@ cudaError_t logprob_launch_t(const LogprobParams& p, int cluster, cudaStream_t s
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<F32, TOP>, p);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<F32, TOP, W>, p);
+}
+template <bool F32>
+cudaError_t logprob_launch_w(const LogprobParams& p, bool warp_rows, int cluster, cudaStream_t s) {
+  if (warp_rows) return p.k ? logprob_launch_t<F32, true, 1>(p, 1, s) : logprob_launch_t<F32, false, 1>(p, 1, s);
+  return p.k ? logprob_launch_t<F32, true, 8>(p, cluster, s) : logprob_launch_t<F32, false, 8>(p, cluster, s);
 }
 
 }  // namespace
 
 cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s) {
-  // More blocks a row while the grid leaves multiprocessors short of 4 blocks
-  // and each block keeps two passes over its threads' vectors.
-  const int64_t pass = (int64_t)kLpThreads * (p.f32 ? 4 : 8);
+  // Short rows: a warp each, of one pass over its lanes' vectors, or of up to
+  // eight where there are rows enough for every multiprocessor's warps.
+  const int64_t pass = (int64_t)32 * kUnroll * (p.f32 ? 4 : 8);
+  const bool warp_rows = p.V <= pass || (p.V <= 8 * pass && (int64_t)p.N >= (int64_t)sms * 16);
+  // Else a block each, or more while the grid leaves multiprocessors short of 4
+  // blocks and each block keeps two vectors a thread.
   int cluster = 1;
-  while (cluster < 8 && (int64_t)p.N * cluster * 2 <= (int64_t)sms * 4 && p.V >= cluster * 2 * 2 * pass) cluster *= 2;
-  if (p.f32) return p.k ? logprob_launch_t<true, true>(p, cluster, s) : logprob_launch_t<true, false>(p, cluster, s);
-  return p.k ? logprob_launch_t<false, true>(p, cluster, s) : logprob_launch_t<false, false>(p, cluster, s);
+  while (cluster < 8 && (int64_t)p.N * cluster * 2 <= (int64_t)sms * 4 && p.V >= cluster * 2 * 4 * pass) cluster *= 2;
+  return p.f32 ? logprob_launch_w<true>(p, warp_rows, cluster, s) : logprob_launch_w<false>(p, warp_rows, cluster, s);
 }
 
 }  // namespace moe

@@ -59,7 +59,8 @@ def inputs(N, V, dtype, seed, ld=None, offset=0):
 @pytest.mark.parametrize("N,V,k,ld,offset", [
     (1, 1, 1, None, 0), (1, 1, 0, None, 0), (3, 2, 2, None, 1), (2, 31, 31, 33, 3), (5, 100, 32, None, 0), (1, 5000, 20, None, 0),
     (1, 32000, 5, None, 0), (7, 40001, 32, None, 1), (2, 131072, 20, None, 0), (700, 3001, 8, 3007, 5), (33, 65537, 1, 65539, 7),
-    (1300, 513, 4, None, 0), (64, 20000, 0, None, 0)])
+    (1300, 513, 4, None, 0), (64, 20000, 0, None, 0), (9, 1024, 32, 1025, 1), (17, 1025, 32, 1025, 1), (2500, 4000, 20, 4001, 3),
+    (2433, 8192, 32, None, 0), (5, 300000, 32, 300001, 1)])
 def test_matches_64_bits(N, V, k, ld, offset, dtype):
     from bit_moe_expert_route_gb300 import ops
     z, ids = inputs(N, V, dtype, N + V, ld, offset)
