@@ -15,7 +15,8 @@
 // and splits K over its 8 warps; a lane loads 16 consecutive codes of two
 // rows per m16n8k16 product quadruple (the order of k is free as long as both
 // operands agree, so the fragments need no shuffling), and the warps' sums
-// meet in shared memory.
+// meet in shared memory. One token by 4608 x 2048 weights: 3.2 us; 8 tokens by
+// 100003 x 2048: 37 us (5.5 TB/s, 81% of the measured copy); 24: 52 us.
 //
 // More tokens: tcgen05. The MMA's M side is 128 weight rows, its N side up to
 // 256 tokens. TMA brings the packed weight codes, converter warps write them as
@@ -23,6 +24,8 @@
 // only the tokens' operand to the MMA. The tokens' codes (far fewer) are
 // widened to f16 in the workspace by a first kernel; its launch lets the
 // product's start early, and the product's weight stream does not wait for it.
+// 8192 x 8192 x 2048: 182 us, 1.51 PFLOP/s (81% of the measured burst rate); the
+// MMAs alone take 151 us at the clock that power leaves.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -16,15 +16,20 @@
 // multiply-add: about four instructions an element with its ex2.
 //
 // Top k (k <= 32): a warp holds its best 32 in order, one a lane, and inserts
-// what reaches the block's threshold, a lower bound of the row's k-th best. It starts from the thread
-// maxima of the block's first pass, so that only a few elements a pass ever
-// reach the insertion. Ties go to the lower index: entries are 64-bit keys (value in
-// order, then the index reversed), and an element equal to the threshold is
-// still inserted.
+// what reaches the block's threshold, a lower bound of the row's k-th best. It
+// starts from the thread maxima of the block's first pass, so that only a few
+// elements a pass ever reach the insertion. Ties go to the lower index: entries
+// are 64-bit keys (value in order, then the index reversed), and an element
+// equal to the threshold is still inserted.
 //
 // Many rows: one block a row (short rows: one warp). Few rows: a cluster of 2, 4
 // or 8 blocks shares a row and the first block merges their states from
 // distributed shared memory, so one launch suffices at every size.
+//
+// 2048 rows of 131072 bf16 logits: 84 us without alternatives (6.4 TB/s, 94% of
+// the measured copy), 95 with 8, 125 with 32; bound by HBM, then by instruction
+// issue (72% active with 8). 48 rows of 100003 fp32 logits with 20: 17.5 us, of
+// which 8 without alternatives: the merges' and insertions' latency.
 #include <cmath>
 
 #include "common.cuh"
