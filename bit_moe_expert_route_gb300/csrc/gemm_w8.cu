@@ -324,8 +324,10 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
           tma_load_2d(smem + C::kOffQ + s * kQStage, &args.tm_w, kb * kKB, row, &q_full[s], policy);
         }
       }
-      for (uint32_t j = it > (uint32_t)C::kSQ ? it - C::kSQ : 0; j < it; ++j)  // every load lands before the CTA ends
-        mbar_wait(&q_full[j % C::kSQ], (j / C::kSQ) & 1, abort_flag, g.status, 62);
+      // every load lands before the CTA ends, also when another role gave up
+      volatile int drained = 0;
+      for (uint32_t j = it > (uint32_t)C::kSQ ? it - C::kSQ : 0; j < it; ++j)
+        mbar_wait(&q_full[j % C::kSQ], (j / C::kSQ) & 1, &drained, g.status, 62);
     }
   } else if (warp == 2) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -350,8 +352,9 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
                         &b_full[s], policy);
         }
       }
+      volatile int drained = 0;
       for (uint32_t j = it > (uint32_t)C::kSB ? it - C::kSB : 0; j < it; ++j)
-        mbar_wait(&b_full[j % C::kSB], (j / C::kSB) & 1, abort_flag, g.status, 62);
+        mbar_wait(&b_full[j % C::kSB], (j / C::kSB) & 1, &drained, g.status, 62);
     }
   } else if (warp == 1 || (C::kIssuers == 2 && warp == 3)) {
     if (lane == 0) {
@@ -404,8 +407,9 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
         tc_commit(&acc_full[buf]);
         if (++buf == C::kAcc) buf = 0, pacc ^= 1;
       }
+      volatile int drained = 0;
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
-      mbar_wait(drain, 0, abort_flag, g.status, 67);
+      mbar_wait(drain, 0, &drained, g.status, 67);
     }
   } else if (warp >= 4 && warp < C::kEpiWarp0) {
     // thread = one weight row of every kGroups-th k-block: a k-block takes

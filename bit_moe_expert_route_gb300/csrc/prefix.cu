@@ -231,6 +231,9 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
   }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (l[r] != l[r] && m[r] == -INFINITY) m[r] = 0.f;  // nothing but NaN: not a state without positions
   cp_async_wait<0>();
   const int64_t state = (int64_t)it.slot * p.B * p.Hq;
   // the key groups' states of a row tile meet in shared memory

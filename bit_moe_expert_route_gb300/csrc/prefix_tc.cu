@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         if (i + 1 < n) alive = load(&args.tm_k, k0 + (i + 1) * KT);
         if (alive) alive = load(&args.tm_v, k0 + i * KT);
       }
-      // every load lands before the CTA ends
+      // every load lands before the CTA ends, also when another role gave up
+      volatile int drained = 0;
       for (int j = loads > NS ? loads - NS : 0; j < loads; ++j)
-        mbar_wait(&full[j % NS], (j / NS) & 1, abort_flag, p.status, 82);
+        mbar_wait(&full[j % NS], (j / NS) & 1, &drained, p.status, 82);
     }
   } else if (warp == 1 || warp == 2) {
     // Warp 1 issues the scores' products, warp 2 the outputs': what one does
@@ -212,8 +213,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
           advance(i + 2 < n ? 2 : 1);  // the last V follows the one before it
         }
       }
+      volatile int drained = 0;
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
-      mbar_wait(drain, 0, abort_flag, p.status, 87);
+      mbar_wait(drain, 0, &drained, p.status, 87);
     }
   } else if (warp >= 4) {
     const int quarter = warp & 3, r = quarter * 32 + lane;  // this thread's row of the tile
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       tc_fence_after();
       const bool mine = row0 + r < R;
       const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);
+      if (l != l && m == -INFINITY) m = 0.f;  // nothing but NaN: not a state without positions
       if (mine) p.part_ml[at] = make_float2(m, l);
       // through shared memory (the ring is free: every product is complete), so
       // that a row goes out as one copy; rows 16 bytes further apart than they

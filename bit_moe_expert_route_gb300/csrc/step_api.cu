@@ -87,7 +87,7 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
 static_assert(moe::kW8FewTokens == MOE_W8A8_NO_WORKSPACE_T, "the header's promise");
 
 size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K) {
-  if (T < 0 || N < 1 || K < 16 || K > 65536 || K % 16 != 0) return 0;
+  if (T < 0 || N < 1 || K < 16 || K > 65536 || K % 16 != 0 || (int64_t)T * K >= (int64_t)1 << 40) return 0;
   // the status word, then the tokens' codes as f16
   return 256 + (T > moe::kW8FewTokens ? ((size_t)T * K * 2 + 255) / 256 * 256 : 0);
 }

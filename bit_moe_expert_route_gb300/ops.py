@@ -319,6 +319,15 @@ def decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: f
     return out
 
 
+def _keep(stream, *tensors):
+    """Tensors made here are the current stream's; where the caller names another, their memory
+    stays theirs until that stream is past them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 Q8_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
 _FLOAT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -395,6 +404,7 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
     rc = lib().moe_add_rmsnorm_q8(px, _ld(x), pr, pw, T, d, eps, code, po, q.data_ptr(),
                                   scale.data_ptr(), pv, _stream(stream))
     _check("moe_add_rmsnorm_q8", rc)
+    _keep(stream, q, scale, vals, residual_out)
     return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
 
 
@@ -435,6 +445,7 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     rc = lib().moe_gemm_w8a8(pa, _ld(a), ps, pw, pt, T, N, K, _FLOAT_TYPES[dtype], po, _ld(out),
                              pws, nbytes, _stream(stream))
     _check("moe_gemm_w8a8", rc)
+    _keep(stream, out, ws)
     return out
 
 
@@ -473,6 +484,7 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po, ws.data_ptr(), ws.numel(),
         _stream(stream))
     _check("moe_prefix_attention", rc)
+    _keep(stream, out, ws)
     return out
 
 
@@ -509,6 +521,7 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
     rc = lib().moe_token_logprobs(pz, _FLOAT_TYPES[logits.dtype], _ld(logits), pi, N, V, top_k, pl,
                                   entropy.data_ptr(), pt, pp, _stream(stream))
     _check("moe_token_logprobs", rc)
+    _keep(stream, logprob, entropy, top_ids, top_lp)
     return TokenLogprobs(logprob, entropy, top_ids, top_lp)
 
 

@@ -67,7 +67,7 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
  *            (no initialisation needed), holds the status word; may be NULL
  *            for up to MOE_W8A8_NO_WORKSPACE_T tokens
  * a and w 16-byte aligned; T >= 0 (0 launches nothing), N >= 1, K a multiple of
- * 16, 16 <= K <= 65536. The integer sum is exact while its partial sums stay
+ * 16, 16 <= K <= 65536, T * K < 2^40. The integer sum is exact while its partial sums stay
  * below 2^24 in magnitude (always for K <= 1024), else it carries fp32
  * rounding; the scales multiply it in fp32 and the result is rounded once. One
  * launch for few tokens or little work, else two.

@@ -81,6 +81,30 @@ def test_strided_output_and_other_stream(T):
     s.synchronize()
     assert torch.equal(wide[:, 5:306], exact(a, sa, w, sw).float().to(torch.bfloat16))
     assert torch.all(wide[:, :5] == 7) and torch.all(wide[:, 306:] == 7)
+    torch.cuda.synchronize()
+    got = ops.gemm_w8a8(a, sa, w, sw, stream=s)  # made on the current stream, used on another
+    s.synchronize()
+    assert torch.equal(got, wide[:, 5:306])
+
+
+@gpu
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_captured_in_a_graph(T):
+    from bit_moe_expert_route_gb300 import ops
+    a, sa, w, sw = inputs(T, 4000, 256, T)
+    want = ops.gemm_w8a8(a, sa, w, sw)
+    out = torch.empty_like(want)
+    ws = torch.empty(ops.lib().moe_gemm_w8a8_workspace_bytes(T, 4000, 256), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.gemm_w8a8(a, sa, w, sw, out=out, ws=ws)
+        ops.gemm_w8a8(a, sa, w, sw, out=out, ws=ws)
+    a.copy_(torch.flip(a, [0]))
+    sa.copy_(torch.flip(sa, [0]))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, torch.flip(want, [0]))
 
 
 @gpu

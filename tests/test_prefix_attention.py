@@ -99,6 +99,25 @@ def test_rows_without_positions_are_zero():
 
 
 @gpu
+@pytest.mark.parametrize("B,d", [(3, 64), (3, 256), (30, 64), (30, 128), (30, 256)])
+def test_bad_queries_and_infinite_keys(B, d):
+    """A query row with a NaN gives NaN in that row alone; a key that scores -infinity for
+    some rows has no weight in them."""
+    from bit_moe_expert_route_gb300 import ops
+    q, kp, vp, ks, vs, ln = inputs(B, 400, 20, 8, 2, d, d, [20] * B)
+    q[1, 5, 3] = float("nan")
+    got = ops.prefix_attention(q, kp, vp, ks, vs, ln)
+    bad = torch.zeros(B, 8, dtype=torch.bool, device="cuda")
+    bad[1, 5] = True
+    assert torch.isnan(got[bad]).all() and torch.isfinite(got[~bad]).all()
+    q[1, 5, 3] = 1.0
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    kp[77, 0, 0] = float("-inf")  # every score of this key is -infinity
+    o, mag = expected(q, kp, vp, ks, vs, ln)
+    check(ops.prefix_attention(q, kp, vp, ks, vs, ln), o, mag)
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 256])
 def test_strided_caches_and_scale(d):
     """K and V interleaved in one buffer; a cache with room for more sequences' positions."""
