@@ -297,15 +297,18 @@ struct PrefixParams {
   int B, P, S, Hq, Hkv, d;
   float scale_log2;          // scale * log2 e
   // the plan
+  int joined;                // blocks of a cluster (one launch, no workspace), or 0
   int tc;                    // the prefix goes to prefix_tc_launch, 128 rows a block
   int row_warps, prefix_slice, prefix_splits, prefix_blocks, suffix_slice, suffix_splits;
-  int32_t* status;
+  int32_t* status;           // or null (joined)
   float* part_o;             // [prefix_splits + suffix_splits][B Hq][d]
   float2* part_ml;           // [prefix_splits + suffix_splits][B Hq]: reference (log2), sum
   uint16_t* out;             // bf16 [B][Hq][d]
 };
 bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d);
-// Fills the plan from the sizes (slices of whole key tiles).
+// Blocks of a cluster where one launch of clusters takes all, else 0.
+int prefix_joined_blocks(int B, int P, int S, int Hkv, int d);
+// Fills the rest of the plan from the sizes (slices of whole key tiles).
 void prefix_plan(PrefixParams& p, int sms);
 // The prefix's partial states from tcgen05 products.
 cudaError_t prefix_tc_launch(const PrefixParams& p, cudaStream_t s);

@@ -247,6 +247,7 @@ MOE_DEVINL void merge_lists(uint64_t (*list)[32], int n, int warp, int lane) {
 }
 
 MOE_DEVINL void cluster_sync() {
+  __syncwarp();  // (the barrier wants warps undivided)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of `q` in the shared memory of the cluster's block r.

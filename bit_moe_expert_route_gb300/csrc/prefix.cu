@@ -19,7 +19,7 @@
 // these products wait for memory anyway. The running maximum moves only when a score passes it by 2^8, which fp32 and
 // bf16 hold without loss, so the output is rarely rescaled. (With more than 32
 // rows a KV head the prefix goes to prefix_tc.cu; the sequences' own positions
-// stay here.)
+// stay here. Little work takes one launch of clusters, below.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,6 +31,7 @@ namespace {
 constexpr int kPfThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr float kLazyLog2 = 8.f;
+constexpr int kJoinedBlocks = 304, kJoinedTiles = 4, kJoinedWork = 2048;
 constexpr int kPrefixTcMin = 256;  // positions from which the tensor-memory kernel takes a prefix
 
 MOE_DEVINL float ex2(float x) {
@@ -85,7 +86,7 @@ struct PfCfg {
   static constexpr int kSmem = kSlots * kTile + kMaxRows * D * 2;
   static constexpr int kBlocks = D == 256 ? 2 : D == 128 ? 3 : 4;  // an SM's
   static_assert(kBlocks * (kSmem + 1024) <= 233472, "shared memory exceeded");
-  static_assert(64 * D * 4 + 64 * 8 <= kSlots * kTile, "the warps' states do not fit the ring");
+  static_assert(64 * D * 4 + (64 + 16) * 8 <= kSlots * kTile, "the warps' states do not fit the ring");
 };
 
 // One block's work: `rows` query rows (row r: sequence b0 + r / G, head
@@ -95,9 +96,22 @@ struct PfItem {
   const uint16_t *K, *V;
   int64_t ld;
   int k0, k1, slot;
+  // JOINED: keys from n0 on are K2's, V2's from their first
+  int n0;
+  const uint16_t *K2, *V2;
+  int64_t ld2;
 };
 
-template <int D, int WM>
+// Where a JOINED block leaves its state: the rows' outputs at the start of
+// shared memory, their (reference, sum) here.
+template <int D>
+MOE_DEVINL float2* joined_ml(uint8_t* smem) {
+  return reinterpret_cast<float2*>(smem + 64 * D * 4 + 64 * 8);
+}
+
+// JOINED: the keys are one sequence's, the prefix's and then its own, and the
+// state stays in shared memory; else it goes to the partial states.
+template <int D, int WM, bool JOINED>
 MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
   using C = PfCfg<D>;
   constexpr int WK = 4 / WM, KS = kTileKeys / WK, NT = KS / 8;
@@ -118,7 +132,7 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
   const int lr = tid / kChunks, lc = tid % kChunks;
   const uint32_t dst[2] = {smem_u32(smem) + tile_off<D>(lr, lc), smem_u32(smem) + tile_off<D>(lr + kStep, lc) - kStep * (D * 2)};
   int fill = 0;  // the next slot to fill
-  auto load_tile = [&](const uint16_t* base, int key) {
+  auto load_tile = [&](const uint16_t* base, const uint16_t* base2, int key) {
     if (key < it.k1) {
       const uint32_t at = fill * C::kTile;
       int64_t src = (int64_t)(key + lr) * it.ld + lc * 8;
@@ -126,15 +140,20 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
 #pragma unroll 8
       for (int j = 0; j < kTileKeys / kStep; ++j) {
         const bool in = j * kStep < left;  // keys past the end as zeros: their weight is 0 too
-        cp_async_16(dst[j & 1] + at + j * kStep * (D * 2), base + (in ? src : 0), in ? 16u : 0u);
+        const uint16_t* from = base + src;
+        if constexpr (JOINED) {
+          const int own = key + lr + j * kStep - it.n0;
+          if (own >= 0) from = base2 + own * it.ld2 + lc * 8;
+        }
+        cp_async_16(dst[j & 1] + at + j * kStep * (D * 2), in ? from : p.q, in ? 16u : 0u);
         src += kStep * it.ld;
       }
     }
     cp_async_commit();
     fill = fill + 1 == C::kSlots ? 0 : fill + 1;
   };
-  load_tile(it.K, it.k0);
-  load_tile(it.V, it.k0);
+  load_tile(it.K, it.K2, it.k0);
+  load_tile(it.V, it.V2, it.k0);
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < D / 8; ++j)
@@ -152,7 +171,7 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
 #pragma unroll 1
   for (int key = it.k0; key < it.k1; key += kTileKeys) {
     const uint8_t* ks = next_slot();
-    load_tile(it.K, key + kTileKeys);
+    load_tile(it.K, it.K2, key + kTileKeys);
     float s[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -209,7 +228,7 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
         l[i >> 1] += s[j][i];
       }
     const uint8_t* vs = next_slot();
-    load_tile(it.V, key + kTileKeys);
+    load_tile(it.V, it.V2, key + kTileKeys);
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
       uint32_t hi[4], lo[4];
@@ -268,9 +287,14 @@ MOE_DEVINL void attend(const PrefixParams& p, const PfItem& it, uint8_t* smem) {
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const int64_t at = state + query_row(it.row0 + row);
-    *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = acc;
-    if (c == 0) p.part_ml[at] = make_float2(M, L);
+    if constexpr (JOINED) {  // over warp 0's, which no other thread reads there
+      *reinterpret_cast<float4*>(so + row * D + c * 4) = acc;
+      if (c == 0) joined_ml<D>(smem)[row] = make_float2(M, L);
+    } else {
+      const int64_t at = state + query_row(it.row0 + row);
+      *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = acc;
+      if (c == 0) p.part_ml[at] = make_float2(M, L);
+    }
   }
 }
 
@@ -305,7 +329,7 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_kernel(c
     it.k0 = min(p.P, split * p.prefix_slice);
     it.k1 = min(p.P, it.k0 + p.prefix_slice);
     it.slot = split;
-    attend<D, WM>(p, it, pf_smem);
+    attend<D, WM, false>(p, it, pf_smem);
   } else {
     i -= prefix_blocks;
     it.h = i % p.Hkv;
@@ -325,10 +349,116 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_kernel(c
       for (int r = threadIdx.x; r < G; r += kPfThreads)
         p.part_ml[(int64_t)it.slot * p.B * p.Hq + (int64_t)b * p.Hq + it.h * G + r] = make_float2(-INFINITY, 0.f);
     } else {
-      attend<D, 1>(p, it, pf_smem);
+      attend<D, 1, false>(p, it, pf_smem);
     }
   }
   if (beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+MOE_DEVINL void cluster_sync() {
+  __syncwarp();  // (the barrier wants warps undivided)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `q` in the shared memory of the cluster's block r.
+MOE_DEVINL uint32_t remote_addr(const void* q, uint32_t r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
+  return a;
+}
+
+// Little work: a cluster takes one sequence and KV head, its blocks slices of the
+// prefix and the sequence's own positions joined, and merges their states from
+// distributed shared memory: one launch and no workspace, where launches and
+// allocations are most of the time. The prefix is then read once a sequence
+// (from L2 but for the first).
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_joined_kernel(const PrefixParams p) {
+  extern __shared__ __align__(128) uint8_t pf_smem[];
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = 0;
+  const int c0 = blockIdx.x / ranks, h = c0 % p.Hkv, b = c0 / p.Hkv, G = p.Hq / p.Hkv;
+  const int len = p.S > 0 ? max(0, min(p.lens[b], p.S)) : 0, n = p.P + len;
+  const int slice = ((n + kTileKeys - 1) / kTileKeys + (int)ranks - 1) / (int)ranks * kTileKeys;
+  PfItem it;
+  it.h = h;
+  it.row0 = 0;
+  it.rows = G;
+  it.b0 = b;
+  it.K = p.kp + (int64_t)h * D;
+  it.V = p.vp + (int64_t)h * D;
+  it.ld = p.ld_prefix;
+  it.n0 = p.P;
+  it.K2 = p.ks + (int64_t)b * p.seq_suffix + (int64_t)h * D;
+  it.V2 = p.vs + (int64_t)b * p.seq_suffix + (int64_t)h * D;
+  it.ld2 = p.ld_suffix;
+  it.k0 = min(n, (int)rank * slice);
+  it.k1 = min(n, it.k0 + slice);
+  it.slot = 0;
+  float2* ml = joined_ml<D>(pf_smem);
+  if (it.k0 < it.k1)
+    attend<D, 1, true>(p, it, pf_smem);
+  else if (threadIdx.x < 16)
+    ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+  cluster_sync();
+  for (int i = rank * kPfThreads + threadIdx.x; i < G * (D / 4); i += ranks * kPfThreads) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    float2 s[8];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      s[r] = make_float2(-INFINITY, 0.f);
+      if (r < (int)ranks)
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(s[r].x), "=f"(s[r].y) : "r"(remote_addr(ml + row, r)) : "memory");
+      M = fmaxf(M, s[r].x);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (s[r].x == -INFINITY) continue;  // (no state: its outputs were not written)
+      float4 v;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(remote_addr(pf_smem + row * (D * 4) + c * 16, r))
+                   : "memory");
+      const float f = ex2(s[r].x - M);
+      L = fmaf(f, s[r].y, L);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // no position at all: zeros
+    const int64_t at = ((int64_t)b * p.Hq + h * G + row) * D + c * 4;
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+  cluster_sync();  // a block's shared memory stays until the others have read it
+}
+
+template <int D>
+cudaError_t prefix_joined_launch(const PrefixParams& p, cudaStream_t s) {
+  using C = PfCfg<D>;
+  static const cudaError_t smem_set =
+      cudaFuncSetAttribute(prefix_joined_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (smem_set != cudaSuccess) return smem_set;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.joined;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.joined));
+  cfg.blockDim = dim3(kPfThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, prefix_joined_kernel<D>, p);
 }
 
 // One query row a block: merges its partial states. First the weights of the
@@ -448,6 +578,20 @@ bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d) {
          Hkv >= 1 && Hkv <= 1024 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 16;
 }
 
+int prefix_joined_blocks(int B, int P, int S, int Hkv, int d) {
+  const int64_t kt = ((int64_t)P + S + kTileKeys - 1) / kTileKeys;
+  int cluster = 1;
+  while (cluster < 8 && cluster < kt) cluster *= 2;
+  // One wave of blocks, two an SM, few tiles a block, and few enough in all that
+  // reading the prefix once a sequence costs less than the launch and the
+  // allocation saved (about 8 us of a call; 4 sequences over 2000 positions, 2 KV
+  // heads of 256, 11 us, 19 over 1983 25).
+  return (int64_t)B * Hkv * cluster <= kJoinedBlocks && kt <= kJoinedTiles * cluster &&
+                 (int64_t)B * Hkv * kt * (d / 64) <= kJoinedWork
+             ? cluster
+             : 0;
+}
+
 void prefix_plan(PrefixParams& p, int sms) {
   const int R = p.B * (p.Hq / p.Hkv);
   const int per_sm = p.d == 64 ? 4 : 2;  // blocks an SM over which a prefix is cut
@@ -482,6 +626,10 @@ void prefix_plan(PrefixParams& p, int sms) {
 }
 
 cudaError_t prefix_launch(const PrefixParams& p, cudaStream_t s) {
+  if (p.joined) {
+    if (p.d == 256) return prefix_joined_launch<256>(p, s);
+    return p.d == 128 ? prefix_joined_launch<128>(p, s) : prefix_joined_launch<64>(p, s);
+  }
   if (p.d == 256) return prefix_launch_d<256>(p, s);
   if (p.d == 128) return prefix_launch_d<128>(p, s);
   return prefix_launch_d<64>(p, s);

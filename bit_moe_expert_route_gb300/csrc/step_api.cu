@@ -162,6 +162,7 @@ size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, 
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.d = d;
+  if (moe::prefix_joined_blocks(B, P, S, n_kv_heads, d)) return 256;  // the status word, if one is wanted
   // the device's SM count decides the slices; the largest count has the most
   moe::prefix_plan(p, moe::kPrefixMaxSms);
   return prefix_carve(p, nullptr);
@@ -203,13 +204,18 @@ int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint
   p.d = d;
   p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf((float)d)) * 1.4426950408889634f;
   p.out = out;
-  if (!ws || !aligned(ws, 256) ||
-      ws_bytes < moe_prefix_attention_workspace_bytes(B, P, S, n_q_heads, n_kv_heads, d))
+  p.joined = moe::prefix_joined_blocks(B, P, S, n_kv_heads, d);
+  if (ws ? !aligned(ws, 256) || ws_bytes < moe_prefix_attention_workspace_bytes(B, P, S, n_q_heads, n_kv_heads, d)
+         : !p.joined)
     return MOE_ERR_WORKSPACE;
   const int sms = device_sms();
   if (sms < 0) return sms;
-  moe::prefix_plan(p, sms);
-  prefix_carve(p, ws);
+  if (p.joined) {
+    p.status = static_cast<int32_t*>(ws);
+  } else {
+    moe::prefix_plan(p, sms);
+    prefix_carve(p, ws);
+  }
   return cuda_status(moe::prefix_launch(p, static_cast<cudaStream_t>(stream)));
 }
 

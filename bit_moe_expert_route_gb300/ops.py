@@ -473,16 +473,16 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         po = out.data_ptr()
     else:
         po = _want(fn, "out", out, bf, (B, Hq, d))
-    if ws is None:
-        nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
-        if nbytes == 0:
-            raise MoeError("moe_prefix_attention_workspace_bytes", -3)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     width = Hkv * d  # the stride of an axis of one entry says nothing
-    rc = lib().moe_prefix_attention(
-        pq, pk, pv, ld[0] if P > 1 else width, pks, pvs, lds[0] if B > 1 else 0,
-        lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po, ws.data_ptr(), ws.numel(),
-        _stream(stream))
+    args = (pq, pk, pv, ld[0] if P > 1 else width, pks, pvs, lds[0] if B > 1 else 0,
+            lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po)
+    if ws is None:  # little work needs none
+        rc = lib().moe_prefix_attention(*args, None, 0, _stream(stream))
+        if rc == -4:
+            nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if ws is not None:
+        rc = lib().moe_prefix_attention(*args, ws.data_ptr(), ws.numel(), _stream(stream))
     _check("moe_prefix_attention", rc)
     _keep(stream, out, ws)
     return out

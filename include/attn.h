@@ -66,13 +66,17 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  *   out                 bf16 [B][n_q_heads][d]; zeros for a sequence without any
  *                       position (P == 0 and len[b] == 0)
  *   ws                  256-byte aligned, >= moe_prefix_attention_workspace_bytes
- *                       (no initialisation needed), holds the status word
+ *                       (no initialisation needed), holds the status word.
+ *                       May be NULL where little work takes one launch (then
+ *                       nothing in it can fail); MOE_ERR_WORKSPACE says that it
+ *                       may not, before anything is enqueued
  * All pointers but lens (4 bytes) 16-byte aligned, strides multiples of 8
  * elements. 0 <= B <= 65535 (0 launches nothing), P and S up to 2^28, d in {64,
  * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a
  * KV head. Scores and softmax in fp32; the softmax weights multiply the values as
  * two bf16 parts (with more than 32 query rows a KV head and a prefix of 256
- * positions or more: as one), with fp32 sums. Two or three launches: partial
+ * positions or more: as one), with fp32 sums. Up to three launches: with little
+ * work one, of clusters that merge their slices; else partial
  * states over slices of the prefix and of the sequences' own positions (with
  * more than 32 query rows a KV head the prefix has a launch of its own), then
  * their merge in a fixed order. Each is a programmatic dependent of the launch

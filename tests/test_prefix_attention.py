@@ -59,7 +59,10 @@ SHAPES = [(1, 1, 1, 2, 2, 64), (1, 0, 5, 16, 2, 256), (3, 64, 0, 16, 2, 128), (2
           (4, 4096, 64, 16, 1, 256),
           # more than 32 rows a KV head and at least 256 shared positions: the tensor-memory kernel
           (70, 512, 0, 3, 3, 64), (16, 513, 3, 16, 2, 128), (40, 1000, 30, 8, 2, 128), (13, 700, 10, 16, 1, 256), (20, 4099, 10, 12, 2, 256),
-          (65, 9000, 70, 2, 2, 128), (100, 30011, 9, 10, 1, 64), (64, 20000, 100, 16, 2, 256), (5, 256, 40, 16, 2, 128), (33, 257, 0, 2, 2, 64), (5, 700, 70, 16, 2, 256)]
+          (65, 9000, 70, 2, 2, 128), (100, 30011, 9, 10, 1, 64), (64, 20000, 100, 16, 2, 256), (5, 256, 40, 16, 2, 128), (33, 257, 0, 2, 2, 64), (5, 700, 70, 16, 2, 256),
+          # little work: one launch of clusters of 1 to 8 blocks, the prefix ending inside a tile or at its end
+          (1, 0, 1, 16, 1, 256), (7, 10, 50, 4, 4, 128), (4, 100, 28, 16, 1, 64), (3, 128, 64, 6, 2, 128), (2, 1900, 100, 16, 2, 64),
+          (9, 515, 1, 12, 4, 128), (19, 1983, 65, 2, 2, 256), (1, 2048, 0, 8, 8, 64)]
 
 
 @gpu
@@ -218,7 +221,7 @@ def test_refusals(L):
     for bad in ("q", "kp", "vpx", "ks", "vs", "out"):
         assert call(**{bad: p + 8}) == -2, bad
     assert call(lens=p + 2) == -2
-    for bad in (dict(ws=None), dict(ws=p + 64), dict(n=100)):
+    for bad in (dict(ws=None, P=5000), dict(ws=None, B=400), dict(ws=p + 64), dict(n=100), dict(P=5000, n=1000)):
         assert call(**bad) == -4, bad
     assert call(B=0, q=None) == 0
     assert L.moe_prefix_attention_workspace_bytes(2, 5, 10, 4, 2, 64) > 0
