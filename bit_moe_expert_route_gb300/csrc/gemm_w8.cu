@@ -580,23 +580,26 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
 
 }  // namespace
 
+// More than 24 tokens stay with the first kernel, 32 at a time, while its
+// blocks of 16 weight rows fill the machine at most twice (once where K is
+// short and a block has little to do): 64 tokens by 4608 x 2048 weights 7.9 us
+// against 12.2, 64 by 2048 x 2048 4.6 against 12.2.
+bool gemm_w8_few(int T, int N, int K) {
+  const int64_t blocks = ((int64_t)N + 15) / 16 * (((int64_t)T + 31) / 32);
+  return T <= kW8FewTokens || blocks <= (int64_t)kW8RuleSms * (K < 1024 ? 2 : 4);
+}
+
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
-  const int64_t blocks = (p.N + 15) / 16 * (int64_t)((p.T + 31) / 32);
-  const int nt = (p.T + 7) / 8;
-  const bool many_rows = p.N >= 32 * 4 * sms;  // several blocks an SM even with 32 or 64 rows each
-  // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
-  // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
-  // 32 rows at 16 and 24, against 62 and 56 in tensor memory, which is ahead
-  // from 25 (48 against 63 at 32).
-  if (many_rows && nt <= 3) {
-    if (nt == 1) return few_launch<4, 1>(p, s);
-    return nt == 2 ? few_launch<2, 2>(p, s) : few_launch<2, 3>(p, s);
-  }
-  // More than 32 tokens stay with the first kernel, 32 at a time, while its
-  // blocks of 16 weight rows fill the machine at most twice (once where K is
-  // short and a block has little to do): 64 tokens by 4608 x 2048 weights 7.9 us
-  // against 12.2, 64 by 2048 x 2048 4.6 against 12.2.
-  if (nt <= 3 || blocks <= (int64_t)sms * (p.K < 1024 ? 2 : 4)) {
+  if (gemm_w8_few(p.T, p.N, p.K)) {
+    const int nt = (p.T + 7) / 8;
+    // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
+    // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
+    // 32 rows at 16 and 24, against 62 and 56 in tensor memory, which is ahead
+    // from 25 (48 against 63 at 32).
+    if (p.N >= 32 * 4 * kW8RuleSms) {  // several blocks an SM even so
+      if (nt == 1) return few_launch<4, 1>(p, s);
+      return nt == 2 ? few_launch<2, 2>(p, s) : few_launch<2, 3>(p, s);
+    }
     if (nt == 1) return few_launch<1, 1>(p, s);
     if (nt == 2) return few_launch<1, 2>(p, s);
     return nt == 3 ? few_launch<1, 3>(p, s) : few_launch<1, 4>(p, s);

@@ -270,7 +270,10 @@ struct LogprobParams {
 cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integer product
-constexpr int kW8FewTokens = 24;  // up to here no scratch, and no wait that could fail
+constexpr int kW8FewTokens = 24;  // up to here no scratch at any size
+constexpr int kW8RuleSms = 152;   // for which its rules on sizes were measured
+// Whether the sizes go to the kernel without scratch or waits that could fail.
+bool gemm_w8_few(int T, int N, int K);
 struct GemmW8Params {
   const int8_t* a;           // [T], rows lda apart
   int64_t lda;
@@ -280,8 +283,8 @@ struct GemmW8Params {
   int T, N, K, f32;
   void* out;                 // bf16 or fp32, rows ldo apart
   int64_t ldo;
-  uint16_t* a16;             // scratch f16 [T][K] (T > kW8FewTokens)
-  int32_t* status;           // or null (T <= kW8FewTokens)
+  uint16_t* a16;             // scratch f16 [T][K] (not few)
+  int32_t* status;           // or null (few)
 };
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
 

@@ -89,7 +89,7 @@ static_assert(moe::kW8FewTokens == MOE_W8A8_NO_WORKSPACE_T, "the header's promis
 size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K) {
   if (T < 0 || N < 1 || K < 16 || K > 65536 || K % 16 != 0 || (int64_t)T * K >= (int64_t)1 << 40) return 0;
   // the status word, then the tokens' codes as f16
-  return 256 + (T > moe::kW8FewTokens ? ((size_t)T * K * 2 + 255) / 256 * 256 : 0);
+  return 256 + (moe::gemm_w8_few(T, N, K) ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256);
 }
 
 int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
@@ -103,7 +103,7 @@ int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
       !aligned(out, type == MOE_F32 ? 4 : 2))
     return MOE_ERR_ALIGN;
-  if (ws ? !aligned(ws, 256) || ws_bytes < need : T > moe::kW8FewTokens) return MOE_ERR_WORKSPACE;
+  if (ws ? !aligned(ws, 256) || ws_bytes < need : need > 256) return MOE_ERR_WORKSPACE;
   const int sms = device_sms();
   if (sms < 0) return sms;
   moe::GemmW8Params p;

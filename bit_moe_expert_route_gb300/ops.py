@@ -440,8 +440,9 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         nbytes = lib().moe_gemm_w8a8_workspace_bytes(T, N, K)
         if nbytes == 0:
             raise MoeError("moe_gemm_w8a8_workspace_bytes", -3)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        pws = ws.data_ptr()
+        if nbytes > 256:  # else the status word alone, of a call that cannot fail
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            pws = ws.data_ptr()
     rc = lib().moe_gemm_w8a8(pa, _ld(a), ps, pw, pt, T, N, K, _FLOAT_TYPES[dtype], po, _ld(out),
                              pws, nbytes, _stream(stream))
     _check("moe_gemm_w8a8", rc)

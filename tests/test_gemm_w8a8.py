@@ -141,10 +141,11 @@ def test_refusals(L):
         assert call(**{bad: None}) == -1, bad
     for bad in (dict(a=p + 8), dict(w=p + 4), dict(sa=p + 2), dict(sw=p + 1), dict(out=p + 1), dict(out=p + 2, type=1)):
         assert call(**bad) == -2, bad
-    for bad in (dict(ws=None, T=25), dict(ws=p + 16), dict(n=255), dict(T=33, n=256)):
+    for bad in (dict(ws=None, T=100, N=20000, ldo=20000), dict(ws=p + 16), dict(n=255), dict(T=100, N=20000, ldo=20000, n=256)):
         assert call(**bad) == -4, bad
     assert call(T=0, a=None) == 0
-    assert L.moe_gemm_w8a8_workspace_bytes(33, 8, 64) >= 256 + 33 * 64 * 2
+    assert L.moe_gemm_w8a8_workspace_bytes(100, 20000, 64) >= 256 + 100 * 64 * 2
+    assert L.moe_gemm_w8a8_workspace_bytes(24, 1 << 20, 64) == 256
     assert L.moe_gemm_w8a8_workspace_bytes(1, 8, 60) == 0
 
 
