@@ -309,7 +309,9 @@ struct PrefixParams {
   uint16_t* out;             // bf16 [B][Hq][d]
 };
 bool prefix_shape_supported(int B, int P, int S, int Hq, int Hkv, int d);
-// Blocks of a cluster where one launch of clusters takes all, else 0.
+// Blocks of a cluster where one launch of clusters takes all, else 0 (always 0
+// with more positions than kPrefixJoinedPositions).
+constexpr int kPrefixJoinedPositions = 2048;
 int prefix_joined_blocks(int B, int P, int S, int Hkv, int d);
 // Fills the rest of the plan from the sizes (slices of whole key tiles).
 void prefix_plan(PrefixParams& p, int sms);

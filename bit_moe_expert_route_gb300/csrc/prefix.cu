@@ -32,6 +32,7 @@ constexpr int kPfThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr float kLazyLog2 = 8.f;
 constexpr int kJoinedBlocks = 304, kJoinedTiles = 4, kJoinedWork = 2048;
+static_assert(kJoinedTiles * 8 * kTileKeys == kPrefixJoinedPositions, "eight blocks' tiles");
 constexpr int kPrefixTcMin = 256;  // positions from which the tensor-memory kernel takes a prefix
 
 MOE_DEVINL float ex2(float x) {

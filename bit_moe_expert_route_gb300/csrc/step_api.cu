@@ -152,6 +152,8 @@ int moe_token_logprobs(const void* logits, int type, int64_t ld, const int32_t* 
   return cuda_status(moe::logprob_launch(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
+static_assert(moe::kPrefixJoinedPositions == MOE_PREFIX_NO_WORKSPACE_POSITIONS, "the header's promise");
+
 size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, int n_kv_heads, int d) {
   if (!moe::prefix_shape_supported(B, P, S, n_q_heads, n_kv_heads, d)) return 0;
   moe::PrefixParams p;

@@ -450,6 +450,9 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     return out
 
 
+PREFIX_NO_WORKSPACE_POSITIONS = 2048
+
+
 def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
                      k_suffix: torch.Tensor | None = None, v_suffix: torch.Tensor | None = None,
                      lens: torch.Tensor | None = None, scale: float = 0.0,
@@ -477,12 +480,15 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     width = Hkv * d  # the stride of an axis of one entry says nothing
     args = (pq, pk, pv, ld[0] if P > 1 else width, pks, pvs, lds[0] if B > 1 else 0,
             lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po)
-    if ws is None:  # little work needs none
+    rc = -4
+    if ws is None and P + S <= PREFIX_NO_WORKSPACE_POSITIONS:  # little work needs none
         rc = lib().moe_prefix_attention(*args, None, 0, _stream(stream))
-        if rc == -4:
+    if rc == -4:
+        if ws is None:
             nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
+            if nbytes == 0:
+                raise MoeError("moe_prefix_attention_workspace_bytes", -3)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if ws is not None:
         rc = lib().moe_prefix_attention(*args, ws.data_ptr(), ws.numel(), _stream(stream))
     _check("moe_prefix_attention", rc)
     _keep(stream, out, ws)

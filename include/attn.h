@@ -82,6 +82,7 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  * their merge in a fixed order. Each is a programmatic dependent of the launch
  * before it on the stream.
  */
+#define MOE_PREFIX_NO_WORKSPACE_POSITIONS 2048 /* with P + S above it, a workspace is always needed */
 size_t moe_prefix_attention_workspace_bytes(int B, int P, int S, int n_q_heads, int n_kv_heads, int d);
 int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
                          int64_t ld_prefix, const uint16_t* k_suffix, const uint16_t* v_suffix,
