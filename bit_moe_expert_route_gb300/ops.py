@@ -467,8 +467,10 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     fn, bf, dev = "prefix_attention", torch.bfloat16, q.device
     pq = _want(fn, "q", q, bf, (B, Hq, d))
     pk, pv, ld = _want_cache(fn, "prefix", k_prefix, v_prefix, (P, Hkv, d))
-    S, pks, pvs, lds, seq, pl = 0, None, None, (0, 0), 0, None
+    S, pks, pvs, lds, pl = 0, None, None, (0, 0), None
     if k_suffix is not None:
+        if v_suffix is None or lens is None:
+            raise ValueError(f"{fn}: k_suffix without v_suffix or lens")
         S = k_suffix.shape[1]
         pks, pvs, lds = _want_cache(fn, "suffix", k_suffix, v_suffix, (B, S, Hkv, d))
         pl = _want(fn, "lens", lens, torch.int32, (B,))

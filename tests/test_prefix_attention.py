@@ -235,3 +235,15 @@ def test_binding_refuses_wrong_tensors():
         ops.prefix_attention(q, k, k)
     with pytest.raises(ValueError, match="float32"):
         ops.prefix_attention(q.float(), k, k)
+
+
+@gpu
+def test_binding_refuses_unlike_caches():
+    from bit_moe_expert_route_gb300 import ops
+    q, kp, vp, ks, vs, ln = inputs(2, 5, 3, 4, 2, 64, 0)
+    with pytest.raises(ValueError, match="strides"):
+        ops.prefix_attention(q, kp, torch.cat([vp, vp], dim=1)[:, :2])
+    with pytest.raises(ValueError, match="lens"):
+        ops.prefix_attention(q, kp, vp, ks, vs)
+    with pytest.raises(ValueError, match="k_suffix"):
+        ops.prefix_attention(q, kp, vp, ks[:, :, :1], vs, ln)
