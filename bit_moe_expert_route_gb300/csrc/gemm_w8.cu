@@ -309,7 +309,10 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
     // The weights were there before the widening kernel ran (it waited for
     // what came before it): only the f16 tokens are waited for, in warp 2.
     if (lane == 0) {
-      const uint64_t policy = l2_policy_evict_normal();
+      // With one tile of tokens the weights are read once and need not stay in L2:
+      // 64 tokens by 100003 x 2048 weights 47.6 us against 48.9, 64 by 16384 x 2048
+      // 12.1 against 13.0. With several, each of them reads the weights again.
+      const uint64_t policy = TT == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
       uint32_t it = 0;
       bool alive = true;
       for (int64_t u = blockIdx.x; u < units && alive; u += gridDim.x) {
@@ -594,8 +597,8 @@ cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
     const int nt = (p.T + 7) / 8;
     // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
     // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
-    // 32 rows at 16 and 24, against 62 and 56 in tensor memory, which is ahead
-    // from 25 (48 against 63 at 32).
+    // 32 rows at 16 and 24, against 62 and 56 in tensor memory (taken with the
+    // weights' loads at normal priority), which is ahead from 25 (47 against 63 at 32).
     if (p.N >= 32 * 4 * kW8RuleSms) {  // several blocks an SM even so
       if (nt == 1) return few_launch<4, 1>(p, s);
       return nt == 2 ? few_launch<2, 2>(p, s) : few_launch<2, 3>(p, s);
