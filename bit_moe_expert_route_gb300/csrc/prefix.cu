@@ -14,12 +14,12 @@
 // A block: 4 warps, WM of them over 16-row tiles and 4 / WM over the keys of
 // each 64-key tile, so that a few rows still use every warp. K and V tiles
 // come through a ring of cp.async slots; m16n8k16 products with fp32 sums. The
-// weights enter the second product as two bf16 parts: with one, a row of few
-// positions would carry its weights' rounding (2^-8 each) to the output, and
-// these products wait for memory anyway. The running maximum moves only when a score passes it by 2^8, which fp32 and
-// bf16 hold without loss, so the output is rarely rescaled. (With more than 32
-// rows a KV head the prefix goes to prefix_tc.cu; the sequences' own positions
-// stay here. Little work takes one launch of clusters, below.)
+// weights enter the second product as two bf16 parts: one would carry its
+// roundings (2^-8 of each weight) to the output, and these products wait for memory
+// anyway. The running maximum moves only when a score passes it by 2^8, which
+// fp32 and bf16 hold without loss, so the output is rarely rescaled. (With more
+// than 32 rows a KV head the prefix goes to prefix_tc.cu; the sequences' own
+// positions stay here. Little work takes one launch of clusters, below.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -63,7 +63,7 @@ MOE_DEVINL uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Two values as bf16, and what that leaves of them as bf16 too (2^-17 in all).
+// Two values as bf16, and what that leaves of them as bf16 too (2^-16 of each at most).
 MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(x, y);
   lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
@@ -598,8 +598,10 @@ void prefix_plan(PrefixParams& p, int sms) {
   const int per_sm = p.d == 64 ? 4 : 2;  // blocks an SM over which a prefix is cut
   const int64_t room = (int64_t)std::min(sms, kPrefixMaxSms) * per_sm;
   // More than 32 rows a KV head go to tensor memory, 128 rows a block, one block
-  // an SM (32768 positions, 2 KV heads of 256: 23.6 us at 72 rows, against 29 at
-  // 64 with the warps' products; 24.8 at 32). Else 16 or 32 rows a block.
+  // an SM, against the warps' products (16 or 32 rows a block): 32768 positions, 2 KV
+  // heads of 256, 40 rows 23.8 us against 34.1, heads of 128 13.9 against 23.1, of 64
+  // 12.3 against 13.5; 33 rows, 4 KV heads of 128, 4000 positions 10.8 against 12.1
+  // (300 positions 8.3 against 6.5: the longer chain of a short slice).
   p.tc = R > 32 && p.P >= kPrefixTcMin;
   p.row_warps = R <= 16 ? 1 : 2;
   const int tile_rows = p.tc ? 128 : 16 * p.row_warps, tiles = (R + tile_rows - 1) / tile_rows;

@@ -3,23 +3,27 @@
 //
 // A CTA takes one KV head, 128 query rows and one slice of the prefix. Per tile
 // of KT keys:  S = Q K^T (both in shared memory) into tensor memory; softmax
-// weights P = 2^(scale S - m) from there into tensor memory as bf16; O += P V
-// with P as the MMA's A operand and O kept in tensor memory through the slice.
-// One thread issues the scores' products, up to two tiles ahead of the weights,
-// another the outputs', so the tensor core works while the softmax warps do.
+// weights P = 2^(scale S - m) from there into the same columns of tensor memory
+// as bf16; O += P V with P as the MMA's A operand and O kept in tensor memory
+// through the slice. One thread issues the scores' products, another the
+// outputs', three tiles behind at most, so the tensor core works while the softmax
+// warps do (with two tiles' columns 64 sequences over 32768 positions, 2 KV heads
+// of 256, took 49.5 us, with three 44.6).
 //
 // K and V tiles come by TMA into one ring of slots in the order in which the
 // products use them (K0 K1 V0 K2 V1 ...); V is read as it lies (MN-major
 // operand, no transpose). Every query row of a KV head's sequences shares
-// these tiles. At head size 256 with 512 rows a tile of 64 keys takes 0.89 us
-// (about 1700 cycles), 1312 of them the MMAs' (16 of N = 64 at their least time
-// of 50, 4 of N = 256 at 128). Few rows and a long prefix are bound by HBM: 128
-// rows, 8 KV heads of 128, 131072 positions in 87 us, 6.1 TB/s. (Asking L2 for
-// tiles ahead of the ring made that 121 us.)
+// these tiles. At head size 256 with 512 rows a tile of 64 keys takes 1.05 us
+// (about 2000 cycles), 1824 of them the MMAs' (16 of N = 64 at their least time
+// of 50, 8 of N = 256 at 128). Few rows and a long prefix are bound by HBM: 128
+// rows, 8 KV heads of 128, 131072 positions in 91 us, 5.9 TB/s. (Asking L2 for
+// tiles ahead of the ring made it a third more.)
 //
-// The weights are rounded to bf16 once (2^-8 of each at most; with hundreds of
-// positions the roundings average out, to about the output's own): a second
-// part would make the outputs' products, half of all, twice as many.
+// The weights enter the second product as two bf16 parts, as in prefix.cu: one
+// part alone carries its roundings to the output, as much again as the output's
+// own (2.3e-3 of the 2-norm in all, against 1.7e-3), and its weights do not sum to
+// l. That costs 64 sequences over 32768 positions, 2 KV heads of 256, 39.3 -> 44.6
+// us, 8 KV heads of 128 (4 query heads each) 36.3 -> 48.1.
 //
 // The reference m moves only when a score passes it by 2^8; then the warp waits
 // for the products before and rescales its rows of O in tensor memory.
@@ -50,14 +54,15 @@ struct TcCfg {
   static constexpr int kSlot = KT * D * 2;          // K or V of a tile
   static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
   static constexpr int kQ = kTcRows * D * 2;
+  static constexpr int kBufs = 3;                   // tiles between their scores and their outputs
   static constexpr int kOffSlots = kQ;
   static constexpr int kOffBar = kOffSlots + kSlots * kSlot;
-  static constexpr int kBars = 2 * kSlots + 1 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kSlots + 1 + 3 * kBufs + 1;
   static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
-  // tensor memory: O, two score buffers, two weight buffers (two bf16 a column)
+  // tensor memory: O, then the score buffers; a tile's weights take the columns of
+  // its scores (two bf16 a column: the first parts, then the second)
   static constexpr int kColS = D;
-  static constexpr int kColP = D + 2 * KT;
-  static_assert(kColP + KT <= 512, "tensor memory exceeded");
+  static_assert(kColS + kBufs * KT <= 512, "tensor memory exceeded");
   static_assert(kSmem <= 232448, "shared memory exceeded");
   static_assert(kTcRows * (D * 4 + 16) <= kSlots * kSlot, "the output's rows do not fit the ring");
 };
@@ -66,6 +71,14 @@ struct TcArgs {
   CUtensorMap tm_k, tm_v;  // [P][Hkv d], box 64 x KT
   PrefixParams p;
 };
+
+// Two values as bf16, and what that leaves of them as bf16 too (2^-16 of each at most).
+MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
 
 // A wait by a whole warp; its lanes are together again after it.
 MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
@@ -93,17 +106,17 @@ MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ TcArgs args) {
   using C = TcCfg<D>;
-  constexpr int KT = C::KT, NS = C::kSlots;
+  constexpr int KT = C::KT, NS = C::kSlots, NB = C::kBufs;
   const PrefixParams& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] a slot's tile has landed
   uint64_t* empty = full + NS;                                      // [NS] its products are done
   uint64_t* q_full = empty + NS;                                    // [1]
-  uint64_t* s_full = q_full + 1;                                    // [2] scores are complete
-  uint64_t* p_full = s_full + 2;                                    // [2] weights are written
-  uint64_t* pv_done = p_full + 2;                                   // [2] their product is complete
-  uint64_t* drain = pv_done + 2;                                    // [1]
+  uint64_t* s_full = q_full + 1;                                    // [NB] scores are complete
+  uint64_t* p_full = s_full + NB;                                   // [NB] weights are written, over the scores
+  uint64_t* pv_done = p_full + NB;                                  // [NB] their product is complete: the columns are free
+  uint64_t* drain = pv_done + NB;                                   // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       mbar_init(&empty[i], 1);
     }
     mbar_init(q_full, 4);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
@@ -171,17 +184,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     // between two tiles (waits, commits) runs beside the other's MMAs.
     if (lane == 0) {
       const uint32_t slots = smem_u32(smem + C::kOffSlots);
-      int slot = 0, phase = 0;
+      int slot = 0, phase = 0, buf = 0, turn = 0;
       auto advance = [&](int by) {
         if ((slot += by) >= NS) slot -= NS, phase ^= 1;
+        if (++buf == NB) buf = 0, turn ^= 1;
       };
       if (warp == 1) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(kTcRows, KT);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(smem));
         bool alive = mbar_wait(q_full, 0, abort_flag, p.status, 84);
         for (int i = 0; i < n && alive; ++i) {
-          // the scores two tiles before have been read once their weights are written
-          if ((i >= 2 && !mbar_wait(&p_full[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, 91)) ||
+          // the columns hold the weights of NB tiles before until their product is complete
+          if ((i >= NB && !mbar_wait(&pv_done[buf], turn ^ 1, abort_flag, p.status, 91)) ||
               !mbar_wait(&full[slot], phase, abort_flag, p.status, 83))
             break;
           tc_fence_after();
@@ -190,26 +204,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
           for (int c = 0; c < D / 64; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(tmem + C::kColS + (i & 1) * KT, q_desc + ((c * (kTcRows * 128) + kk * 32) >> 4),
+              tc_mma_bf16(tmem + C::kColS + buf * KT, q_desc + ((c * (kTcRows * 128) + kk * 32) >> 4),
                           k_desc + ((c * (KT * 128) + kk * 32) >> 4), idesc_s, (c | kk) != 0);
           tc_commit(&empty[slot]);
-          tc_commit(&s_full[i & 1]);
+          tc_commit(&s_full[buf]);
           advance(i == 0 ? 1 : 2);  // K0 K1 V0 K2 V1 ...
         }
       } else {
         constexpr uint32_t idesc_o = idesc_bf16_f32(kTcRows, D) | (1u << 16);  // B (V) is MN-major
-        advance(n > 1 ? 2 : 1);
+        slot = n > 1 ? 2 : 1;
         for (int i = 0; i < n; ++i) {
           if (!mbar_wait(&full[slot], phase, abort_flag, p.status, 86) ||
-              !mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 85))
+              !mbar_wait(&p_full[buf], turn, abort_flag, p.status, 85))
             break;
           tc_fence_after();
           const uint64_t v_desc = smem_desc_mn(slots + slot * C::kSlot, KT * 128);
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk)
-            tc_mma_ts(tmem, tmem + C::kColP + (i & 1) * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o, (i | kk) != 0);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              tc_mma_ts(tmem, tmem + C::kColS + buf * KT + part * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o,
+                        (i | kk | part) != 0);
           tc_commit(&empty[slot]);
-          tc_commit(&pv_done[i & 1]);
+          tc_commit(&pv_done[buf]);
           advance(i + 2 < n ? 2 : 1);  // the last V follows the one before it
         }
       }
@@ -237,12 +254,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float m = -INFINITY, l = 0.f;
     bool alive = true;
+    int buf = 0, turn = 0, last = 0, last_turn = 0;  // of this tile and of the one before
     for (int i = 0; i < n; ++i) {
-      if (!(alive = warp_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, 88))) break;
+      if (!(alive = warp_wait(&s_full[buf], turn, abort_flag, p.status, 88))) break;
       tc_fence_after();
       uint32_t s[KT / 32][32];
 #pragma unroll
-      for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(tmem + lanes + C::kColS + (i & 1) * KT + c * 32, s[c]);
+      for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(tmem + lanes + C::kColS + buf * KT + c * 32, s[c]);
       tc_wait_ld();
       const int left = k1 - (k0 + i * KT);  // keys of this tile inside the slice
       if (left < KT) {
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         m = nm;
         if (i > 0) {
           // O is whole once the product before is complete
-          if (!(alive = warp_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.status, 89))) break;
+          if (!(alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 89))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -277,32 +295,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
           }
         }
       }
-      // the weights two tiles before have been multiplied: their columns are free
-      if (i >= 2 && !(alive = warp_wait(&pv_done[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, 92))) break;
-      tc_fence_after();
       const float ref = m == -INFINITY ? 0.f : m;
       const float2 sc = make_float2(p.scale_log2, p.scale_log2), nr = make_float2(-ref, -ref);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < KT / 32; ++c) {
-        uint32_t w[16];
+        uint32_t hi[16], lo[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), sc, nr);
           const float2 e = make_float2(ex2(x.x), ex2(x.y));
           sum = __fadd2_rn(sum, e);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          split_bf16(e.x, e.y, hi[j], lo[j]);
         }
-        tmem_st_32x32b_x16(tmem + lanes + C::kColP + (i & 1) * (KT / 2) + c * 16, w);
+        const uint32_t col = tmem + lanes + C::kColS + buf * KT + c * 16;
+        tmem_st_32x32b_x16(col, hi);
+        tmem_st_32x32b_x16(col + KT / 2, lo);
       }
       l += sum.x + sum.y;
       tc_wait_st();
       tc_fence_before();
-      warp_arrive(&p_full[i & 1]);
+      warp_arrive(&p_full[buf]);
+      last = buf, last_turn = turn;
+      if (++buf == NB) buf = 0, turn ^= 1;
     }
     // the slice's state: every product is complete with the last one
-    if (alive && warp_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.status, 90)) {
+    if (alive && warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 90)) {
       tc_fence_after();
       const bool mine = row0 + r < R;
       const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);

@@ -74,8 +74,7 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  * elements. 0 <= B <= 65535 (0 launches nothing), P and S up to 2^28, d in {64,
  * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a
  * KV head. Scores and softmax in fp32; the softmax weights multiply the values as
- * two bf16 parts (with more than 32 query rows a KV head and a prefix of 256
- * positions or more: as one), with fp32 sums. Up to three launches: with little
+ * two bf16 parts (2^-16 of each weight), with fp32 sums. Up to three launches: with little
  * work one, of clusters that merge their slices; else partial
  * states over slices of the prefix and of the sequences' own positions (with
  * more than 32 query rows a KV head the prefix has a launch of its own), then
