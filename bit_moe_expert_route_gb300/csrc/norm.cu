@@ -9,7 +9,10 @@
 // codes follow from values that stayed in registers. u is a product of two
 // bf16 values, exact in fp32; u * (top / a) in fp32 is within 3 * 2^-24 of the
 // exact quotient (relative), so only a quotient that near a rounding border is
-// compared with it exactly: every code is the correctly rounded one.
+// compared with it exactly: every code is the correctly rounded one. (Products of a
+// row whose a is below 2^-80 may fall below fp32's normal range, and top / a may
+// pass it: such a row finds its a again with exponents apart, and its quotients from
+// products lifted by a's exponent.)
 //
 // Bound by HBM: 7 bytes an element (x, residual in; residual, q out), 9 with
 // the bf16 values: 32768 rows of 2048 in 94 us with the values, 6.4 TB/s (95% of
@@ -67,28 +70,76 @@ MOE_DEVINL bool near_border_e4m3(float t) {
   return fabsf(t) >= 0x1p-6f ? cut : sub;
 }
 
+// Rows whose a is below this are done with exponents apart.
+constexpr float kTiny = 0x1p-80f;
+
+// |f w| as a whole number that rises with it: its exponent, then the 15 bits after
+// the leading one (a product of two bf16 values has 16 bits). 0 for 0.
+MOE_DEVINL uint32_t product_key(float f, float w) {
+  int ef, ew, ep;
+  const float p = frexpf(fabsf(frexpf(f, &ef) * frexpf(w, &ew)), &ep);  // exact, in [1/2, 1)
+  return p > 0.f ? (uint32_t)(ef + ew + ep + 512) << 15 | ((uint32_t)(p * 65536.f) - 32768u) : 0u;
+}
+MOE_DEVINL int key_exponent(uint32_t key) { return (int)(key >> 15) - 512; }
+MOE_DEVINL float key_fraction(uint32_t key) { return (float)((key & 32767u) + 32768u) * 0x1p-16f; }
+// The products f w 2^-exponent of a vector.
+struct Products8 {
+  float u[8];
+};
+__device__ __noinline__ Products8 lifted(uint4 r, uint4 weight, int exponent) {
+  float f[8], w[8];
+  unpack8(r, f);
+  unpack8(weight, w);
+  Products8 c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    int ef, ew;
+    const float p = frexpf(f[e], &ef) * frexpf(w[e], &ew);
+    c.u[e] = ldexpf(p, ef + ew - exponent);
+  }
+  return c;
+}
+// The largest product_key of a vector.
+__device__ __noinline__ uint32_t largest_key(uint4 r, uint4 weight) {
+  float f[8], w[8];
+  unpack8(r, f);
+  unpack8(weight, w);
+  uint32_t key = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) key = max(key, product_key(f[e], w[e]));
+  return key;
+}
+
 // A vector with a quotient near a border: the quotients moved to the border's
 // right side (or onto it: a tie). u and a have 16 significant bits, so
 // top |u| and border * a (borders have 8 bits at most) are exact in fp32 and
 // their comparison is the exact quotient's with the border. Out of line, for
 // the instruction cache: it is rarely taken.
+// (exponent < 0: a tiny row, whose a and products are lifted by 2^-exponent. a = 0: no quotients.)
 struct Quotients8 {
   float t[8];
 };
 template <bool E4M3>
-__device__ __noinline__ Quotients8 settle(uint4 r, uint4 weight, float a, bool some) {
+__device__ __noinline__ Quotients8 settle(uint4 r, uint4 weight, float a, int exponent) {
   constexpr float kTop = E4M3 ? 448.f : 127.f;
   // far from fp32's ends, by an exact factor: neither product overflows or loses bits
-  const float lift = a < 1e-20f ? 0x1p64f : a > 1e20f ? 0x1p-64f : 1.f, al = a * lift;
-  float f[8], w[8];
-  unpack8(r, f);
-  unpack8(weight, w);
-  Quotients8 c;
+  const float lift = exponent < 0 ? 1.f : a < 1e-20f ? 0x1p64f : a > 1e20f ? 0x1p-64f : 1.f, al = a * lift;
+  Products8 c;
+  if (exponent < 0) {  // (a lifted product that is rounded, below 2^-126, is far below any code's border)
+    c = lifted(r, weight, exponent);
+  } else {
+    float f[8], w[8];
+    unpack8(r, f);
+    unpack8(weight, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c.u[e] = f[e] * w[e] * lift;
+  }
+  Quotients8 q;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float u = f[e] * w[e] * lift;
-    float t = some ? u * (kTop / al) : 0.f;
-    if (some && (E4M3 ? near_border_e4m3(t) : near_border_int8(t))) {
+    const float u = c.u[e];
+    float t = a > 0.f ? u * (kTop / al) : 0.f;
+    if (a > 0.f && (E4M3 ? near_border_e4m3(t) : near_border_int8(t))) {
       const float b = fabsf(t);
       float border, below, above;  // the border and values that round to either side of it
       if (!E4M3 || b < 0x1p-6f) {
@@ -105,9 +156,20 @@ __device__ __noinline__ Quotients8 settle(uint4 r, uint4 weight, float a, bool s
       const float exact = kTop * fabsf(u), at = border * al;
       t = copysignf(exact < at ? below : exact > at ? above : border, t);
     }
-    c.t[e] = t;
+    q.t[e] = t;
   }
-  return c;
+  return q;
+}
+
+// A barrier of row `sub`'s G threads, G > 32: at most four rows a block. (A barrier
+// number that is not a constant would reserve all 16 for the block, and four blocks
+// would fill an SM: 32768 rows of 2048 118 us against 106.)
+static_assert(kNormThreads / 64 <= 4, "a constant for each row");
+MOE_DEVINL void row_barrier(int sub, int G) {
+  if (sub == 0) asm volatile("bar.sync 1, %0;" ::"r"(G) : "memory");
+  if (sub == 1) asm volatile("bar.sync 2, %0;" ::"r"(G) : "memory");
+  if (sub == 2) asm volatile("bar.sync 3, %0;" ::"r"(G) : "memory");
+  if (sub == 3) asm volatile("bar.sync 4, %0;" ::"r"(G) : "memory");
 }
 
 template <int NV, bool E4M3>
@@ -167,10 +229,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
     ss += __shfl_xor_sync(0xffffffffu, ss, off);
     a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
   }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, first = sub * (G / 32);
   if (G > 32) {  // the same for the whole block: every thread takes the barrier
     __shared__ float sh[2][32];
-    const int warp = threadIdx.x / 32, first = sub * (G / 32);
-    if ((threadIdx.x & 31) == 0) {
+    if (lane == 0) {
       sh[0][warp] = ss;
       sh[1][warp] = a;
     }
@@ -182,18 +244,39 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
       a = max_nan(a, sh[1][w]);
     }
   }
+  int exponent = 0;  // of a tiny row (< 0): its a is a 2^exponent from here on
+  if (a < kTiny) {  // (the same for the row's threads; rows past the end take it too)
+    uint32_t key = 0;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = lt + i * G;
+        if (v < nvec) key = max(key, largest_key(r[i], __ldg(reinterpret_cast<const uint4*>(p.weight) + v)));
+      }
+    }
+    key = __reduce_max_sync(0xffffffffu, key);
+    if (G > 32) {
+      __shared__ uint32_t sh_key[32];
+      if (lane == 0) sh_key[warp] = key;
+      row_barrier(sub, G);
+      for (int w = first; w < first + G / 32; ++w) key = max(key, sh_key[w]);
+    }
+    a = key ? key_fraction(key) : 0.f;
+    exponent = key_exponent(key);
+  }
   if (!live) return;
   constexpr float kTop = E4M3 ? 448.f : 127.f, kMax = 3.402823466e38f;
   const float nan = __int_as_float(0x7fc00000);
   // a NaN or an infinity in the row shows in the sum of squares, one in the
   // products (a weight's, or an overflow) in a
   const bool fine = ss <= kMax && a <= kMax;
-  const float scale = fine ? a / kTop / sqrtf(ss / (float)p.d + p.eps) : nan;
+  float scale = fine ? a / kTop / sqrtf(ss / (float)p.d + p.eps) : nan;
+  if (exponent < 0) scale = ldexpf(scale, exponent);
   if (lt == 0) p.scale[row] = scale;
   // Rows without a usable fp32 quotient (zeros, values that are not finite,
-  // and rows so small that top / a overflows) are settled apart, as NaNs.
-  const bool some = fine && a > 0.f;
-  const float inv = some && a > 1e-36f ? kTop / a : nan;
+  // and tiny rows) are settled apart, as NaNs.
+  if (!fine) a = 0.f;
+  const float inv = exponent == 0 && a > 0.f ? kTop / a : nan;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lt + i * G;
@@ -209,7 +292,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
         near |= E4M3 ? near_border_e4m3(t[e]) : near_border_int8(t[e]);
       }
       if (near) {
-        const Quotients8 c = settle<E4M3>(r[i], weight, a, some);
+        const Quotients8 c = settle<E4M3>(r[i], weight, a, exponent);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = c.t[e];
       }

@@ -36,8 +36,9 @@ enum moe_q8_format {
  *   u = r * weight                    a = max |u|,  rms = sqrt(mean(r^2) + eps)
  *   q = round(u * top / a),  scale = a / (top * rms),  top = 127 (int8) or 448 (e4m3)
  * so q * scale stands for r / rms * weight. Rounding is to nearest, ties to
- * even, of the exact quotient (u, a product of two bf16 values, is exact in
- * fp32; quotients next to a tie are compared with it exactly).
+ * even, of the exact quotient, at any size of u (a product of two bf16 values is
+ * exact in fp32, and rows of a < 2^-80 keep its exponent apart; quotients next to
+ * a tie are compared with it exactly).
  *   x            bf16 [T][d], rows ldx elements apart (ldx >= d, multiple of 8)
  *   residual     bf16 [T][d] or NULL
  *   weight       bf16 [d]
