@@ -150,6 +150,30 @@ def _stream(stream=None):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _tensors(x):
+    if isinstance(x, torch.Tensor):
+        return [x] if x.is_cuda else []
+    if isinstance(x, dict):
+        x = list(x.values())
+    return [t for y in x for t in _tensors(y)] if isinstance(x, (tuple, list)) else []
+
+
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` current: the tensors that it makes are that stream's, so no block
+    that another stream is still using is handed to it. The arguments' memory is kept until
+    `stream` is past them, the results' until the caller's stream is past what it has
+    enqueued with them when they go."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if stream != here:
+        for t in _tensors(args):
+            t.record_stream(stream)
+        for t in _tensors(out):
+            t.record_stream(here)
+    return out
+
+
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """Zero-filled device workspace (the decode call requires a zeroed one)."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -220,6 +244,8 @@ def pick_block_n(T, n_experts, top_k) -> int:
 def route(logits: torch.Tensor, top_k: int, block_n: int, with_shared: bool = True,
           bias: torch.Tensor | None = None, stream=None) -> dict:
     """moe_route on fp32 logits [T, E]; returns the routing arrays as device tensors."""
+    if stream is not None:
+        return _on(stream, route, logits, top_k, block_n, with_shared, bias)
     T, E = logits.shape
     dev = logits.device
     mt = max_tiles(T, E, top_k, block_n, with_shared)
@@ -241,7 +267,7 @@ def route(logits: torch.Tensor, top_k: int, block_n: int, with_shared: bool = Tr
         _p(logits), _p(bias), T, E, top_k, block_n, int(with_shared), _p(r["topk_ids"]),
         _p(r["topk_w"]), _p(r["counts"]), _p(r["offsets"]), _p(r["perm"]), _p(r["inv_perm"]),
         _p(r["row_token"]), _p(r["row_weight"]), _p(r["block_map"]), _p(r["num_tiles"]), mt,
-        _p(ws), ws.numel(), _stream(stream))
+        _p(ws), ws.numel(), _stream())
     _check("moe_route", rc)
     r["max_tiles"] = mt
     r["ws"] = ws
@@ -253,6 +279,10 @@ def grouped_gemm_w4a16(A, W, n_groups, N, block_map, num_tiles, max_tiles_, bloc
                        C=None, C_rows=None, operand=None, stream=None):
     """moe_grouped_gemm_w4a16. W / W_extra: list of (q, scale, bias) device tensors.
     operand: OPERAND_F16 / OPERAND_BF16; by default taken from A's dtype (float16 -> f16)."""
+    if stream is not None:
+        return _on(stream, grouped_gemm_w4a16, A, W, n_groups, N, block_map, num_tiles,
+                   max_tiles_, block_n, epilogue, row_index, n_rows, W_extra, row_scale, out_row,
+                   C, C_rows, operand)
     if operand is None:
         operand = OPERAND_F16 if A.dtype == torch.float16 else OPERAND_BF16
     A_rows, K = A.shape
@@ -273,7 +303,7 @@ def grouped_gemm_w4a16(A, W, n_groups, N, block_map, num_tiles, max_tiles_, bloc
         _p(A), A_rows, K, _p(row_index), n_rows, ctypes.cast(Ws, ctypes.c_void_p), n_groups, N,
         None if Wx is None else ctypes.cast(Wx, ctypes.c_void_p), _p(block_map), _p(num_tiles),
         max_tiles_, block_n, epilogue, operand, _p(row_scale), _p(out_row), _p(C), C.shape[0],
-        C.stride(0), _p(ws), ws.numel(), _stream(stream))
+        C.stride(0), _p(ws), ws.numel(), _stream())
     _check("moe_grouped_gemm_w4a16", rc)
     return C, ws
 
@@ -288,13 +318,15 @@ def gdn_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Ten
     beta fp32 [T, Hv]; state fp32 [Hv, dv, dk], advanced in place over the T tokens.
     state_early (MOE_GDN_STATE_EARLY): the previous launch on the stream does not write
     this state, so it is read before waiting for that launch. Returns out fp32 [T, Hv, dv]."""
+    if stream is not None:
+        return _on(stream, gdn_scan, q, k, v, alpha, beta, state, out, None, state_early)
     T, Hk, dk = k.shape
     Hv, dv = v.shape[1], v.shape[2]
     if out is None:
         out = torch.empty(T, Hv, dv, dtype=torch.float32, device=state.device)
     rc = lib().moe_gdn_scan_ex(_p(q), _p(k), _p(v), _p(alpha), _p(beta), T, Hk, Hv, dk, dv,
                                _p(state), _p(out), GDN_STATE_EARLY if state_early else 0,
-                               _stream(stream))
+                               _stream())
     _check("moe_gdn_scan_ex", rc)
     return out
 
@@ -304,6 +336,8 @@ def decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: f
                      stream=None) -> torch.Tensor:
     """moe_decode_attention (include/attn.h): q bf16 [Hq, d]; K, V bf16 [L, Hkv, d];
     scale <= 0 means 1/sqrt(d). Returns out fp32 [Hq, d]."""
+    if stream is not None:
+        return _on(stream, decode_attention, q, K, V, scale, out, ws)
     Hq, d = q.shape
     L, Hkv = K.shape[0], K.shape[1]
     nbytes = lib().moe_decode_attention_workspace_bytes(L, Hq, Hkv, d)
@@ -314,18 +348,9 @@ def decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: f
     if out is None:
         out = torch.empty(Hq, d, dtype=torch.float32, device=q.device)
     rc = lib().moe_decode_attention(_p(q), _p(K), _p(V), L, Hq, Hkv, d, float(scale), _p(out),
-                                    _p(ws), ws.numel(), _stream(stream))
+                                    _p(ws), ws.numel(), _stream())
     _check("moe_decode_attention", rc)
     return out
-
-
-def _keep(stream, *tensors):
-    """Tensors made here are the current stream's; where the caller names another, their memory
-    stays theirs until that stream is past them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
 
 
 Q8_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
@@ -380,6 +405,8 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
     """moe_add_rmsnorm_q8 (include/step.h): x bf16 [T, d] (rows may be strided), weight bf16
     [d], residual bf16 [T, d] or None. fmt "int8" or "e4m3". residual_out may be `residual`
     (updated in place); without a residual and a residual_out, `.residual` is x itself."""
+    if stream is not None:
+        return _on(stream, add_rmsnorm_q8, x, weight, residual, eps, fmt, values, residual_out)
     T, d = x.shape
     fn, bf, dev = "add_rmsnorm_q8", torch.bfloat16, x.device
     if fmt not in Q8_FORMATS:
@@ -402,9 +429,8 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
         vals = torch.empty(shape, dtype=bf, device=dev)
         pv = vals.data_ptr()
     rc = lib().moe_add_rmsnorm_q8(px, _ld(x), pr, pw, T, d, eps, code, po, q.data_ptr(),
-                                  scale.data_ptr(), pv, _stream(stream))
+                                  scale.data_ptr(), pv, _stream())
     _check("moe_add_rmsnorm_q8", rc)
-    _keep(stream, q, scale, vals, residual_out)
     return NormQ8(q, scale, x if residual_out is None else residual_out, vals)
 
 
@@ -417,6 +443,8 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     """moe_gemm_w8a8 (include/step.h): a int8 [T, K] (rows may be strided) with a_scale fp32
     [T], w int8 [N, K] with w_scale fp32 [N]. Returns out [T, N], bf16 or fp32 (`dtype`, or
     `out`'s own type; out's rows may be strided)."""
+    if stream is not None:
+        return _on(stream, gemm_w8a8, a, a_scale, w, w_scale, dtype, out, ws)
     T, K = a.shape
     N = w.shape[0]
     fn, dev, f32 = "gemm_w8a8", a.device, torch.float32
@@ -444,9 +472,8 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             pws = ws.data_ptr()
     rc = lib().moe_gemm_w8a8(pa, _ld(a), ps, pw, pt, T, N, K, _FLOAT_TYPES[dtype], po, _ld(out),
-                             pws, nbytes, _stream(stream))
+                             pws, nbytes, _stream())
     _check("moe_gemm_w8a8", rc)
-    _keep(stream, out, ws)
     return out
 
 
@@ -462,6 +489,9 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     [P, Hkv, d]; the sequences' own K, V bf16 [B, S, Hkv, d] (or None) of which lens int32 [B]
     positions count. Positions and sequences may be strided (K and V alike). scale <= 0 means
     1/sqrt(d). Returns out bf16 [B, Hq, d]."""
+    if stream is not None:
+        return _on(stream, prefix_attention, q, k_prefix, v_prefix, k_suffix, v_suffix, lens,
+                   scale, out, ws)
     B, Hq, d = q.shape
     P, Hkv = k_prefix.shape[:2]
     fn, bf, dev = "prefix_attention", torch.bfloat16, q.device
@@ -484,16 +514,15 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
             lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po)
     rc = -4
     if ws is None and P + S <= PREFIX_NO_WORKSPACE_POSITIONS:  # little work needs none
-        rc = lib().moe_prefix_attention(*args, None, 0, _stream(stream))
+        rc = lib().moe_prefix_attention(*args, None, 0, _stream())
     if rc == -4:
         if ws is None:
             nbytes = lib().moe_prefix_attention_workspace_bytes(B, P, S, Hq, Hkv, d)
             if nbytes == 0:
                 raise MoeError("moe_prefix_attention_workspace_bytes", -3)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        rc = lib().moe_prefix_attention(*args, ws.data_ptr(), ws.numel(), _stream(stream))
+        rc = lib().moe_prefix_attention(*args, ws.data_ptr(), ws.numel(), _stream())
     _check("moe_prefix_attention", rc)
-    _keep(stream, out, ws)
     return out
 
 
@@ -510,6 +539,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
     """moe_token_logprobs (include/step.h): logits bf16 or fp32 [N, V] (rows may be strided),
     ids int32 [N] or None. Returns the ids' log probabilities, each row's entropy (nats) and
     its top_k (at most 32) alternatives, largest first, ties to the lower id."""
+    if stream is not None:
+        return _on(stream, token_logprobs, logits, ids, top_k)
     N, V = logits.shape
     fn, dev = "token_logprobs", logits.device
     if logits.dtype not in _FLOAT_TYPES:
@@ -528,9 +559,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
     if top_k:
         pt, pp = top_ids.data_ptr(), top_lp.data_ptr()
     rc = lib().moe_token_logprobs(pz, _FLOAT_TYPES[logits.dtype], _ld(logits), pi, N, V, top_k, pl,
-                                  entropy.data_ptr(), pt, pp, _stream(stream))
+                                  entropy.data_ptr(), pt, pp, _stream())
     _check("moe_token_logprobs", rc)
-    _keep(stream, logprob, entropy, top_ids, top_lp)
     return TokenLogprobs(logprob, entropy, top_ids, top_lp)
 
 
@@ -563,12 +593,14 @@ class Forward:
             ctypes.byref(self.views)))
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        if stream is not None:
+            return _on(stream, self, x, out)
         if out is None:
             out = torch.empty(self.T, self.layer.shape.d_model, dtype=torch.bfloat16,
                               device=x.device)
         rc = lib().moe_forward_ex(_p(x), ctypes.byref(self.layer.weights),
                                   ctypes.byref(self.shape), self.block_n, self.flags, _p(out),
-                                  _p(self.ws), self.ws.numel(), _stream(stream))
+                                  _p(self.ws), self.ws.numel(), _stream())
         _check("moe_forward_ex", rc)
         return out
 
@@ -604,11 +636,13 @@ class DecodeBatch:
         return self.ws[off:off + nbytes].view(dtype).view(*shape)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        if stream is not None:
+            return _on(stream, self, x, out)
         if out is None:
             out = torch.empty(self.T, self.layer.shape.d_model, dtype=torch.bfloat16, device=x.device)
         rc = lib().moe_decode_batch_w4(_p(x), ctypes.byref(self.layer.weights),
                                        ctypes.byref(self.shape), _p(out), _p(self.ws),
-                                       self.ws.numel(), _stream(stream))
+                                       self.ws.numel(), _stream())
         _check("moe_decode_batch_w4", rc)
         return out
 
@@ -628,11 +662,13 @@ class Decode:
             _p(self.ws), self.ws.numel(), ctypes.byref(self.shape), ctypes.byref(self.views)))
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        if stream is not None:
+            return _on(stream, self, x, out)
         if out is None:
             out = torch.empty(self.layer.shape.d_model, dtype=torch.bfloat16, device=x.device)
         rc = lib().moe_decode_gemv_w4(_p(x), ctypes.byref(self.layer.weights),
                                       ctypes.byref(self.shape), _p(out), _p(self.ws),
-                                      self.ws.numel(), _stream(stream))
+                                      self.ws.numel(), _stream())
         _check("moe_decode_gemv_w4", rc)
         return out
 
