@@ -274,9 +274,8 @@ __global__ void __launch_bounds__(32 * kGdnWarps) gdn_scan_kernel(const GdnParam
 template <int DK, int R>
 cudaError_t gdn_launch_r(const GdnParams& p, int blocks, cudaStream_t s) {
   constexpr size_t kMax = 2 * sizeof(Chunk<DK, kGdnWarps * R>) + sizeof(ChunkF<DK>);
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(gdn_scan_kernel<DK, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMax);
-  if (attr != cudaSuccess) return attr;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(gdn_scan_kernel<DK, R>, (int)kMax); err != cudaSuccess) return err;
   // a one-chunk sequence (decode) needs one staging buffer: more blocks per SM
   const size_t smem = (p.T > kGdnChunk ? 2 : 1) * sizeof(Chunk<DK, kGdnWarps * R>) + sizeof(ChunkF<DK>);
   cudaLaunchConfig_t cfg = {};

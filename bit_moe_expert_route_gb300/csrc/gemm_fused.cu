@@ -28,7 +28,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -572,12 +571,8 @@ cudaError_t gemm_fused_launch(const FusedParams& p, cudaStream_t s) {
     kp.tm[3] = kp.tm[1];
     kp.tm[5] = kp.tm[4];
   }
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(gemm_fused_kernel, kSmem); err != cudaSuccess) return err;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -556,9 +556,8 @@ cudaError_t many_launch_t(const GemmW8Params& p, int sms, cudaStream_t s) {
   if (!encode_2d(&args.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, p.N, p.K, kKB, kTileN) ||
       !encode_2d(&args.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.a16, p.T, p.K, 64, BN))
     return cudaErrorInvalidValue;
-  static const cudaError_t smem_set =
-      cudaFuncSetAttribute(gemm_w8_kernel<BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (smem_set != cudaSuccess) return smem_set;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(gemm_w8_kernel<BN, F32>, C::kSmem); err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

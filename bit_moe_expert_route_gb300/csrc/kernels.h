@@ -1,6 +1,7 @@
 // Internal launch interfaces of the CUDA kernels (host side, C++).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -10,6 +11,28 @@
 #include "moe.h"
 
 namespace moe {
+
+// A kernel's opt-in to more than 48 KB of dynamic shared memory, which holds for one
+// device: asked for once on each device that the process uses. Only success is
+// remembered (a call after a failed one asks again). A static of the launch function.
+class SharedMemoryOptIn {
+ public:
+  template <class Kernel>
+  cudaError_t operator()(Kernel* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool known = dev >= 0 && dev < kMaxDev;
+    if (known && done_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && known) done_[dev].store(true, std::memory_order_relaxed);
+    return err;
+  }
+
+ private:
+  static constexpr int kMaxDev = 64;
+  std::atomic<bool> done_[kMaxDev] = {};
+};
 
 // ---------------------------------------------------------------- routing
 constexpr int kRouteTPB = 128;  // tokens per block of the top-k and scatter kernels

@@ -442,9 +442,8 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_joined_k
 template <int D>
 cudaError_t prefix_joined_launch(const PrefixParams& p, cudaStream_t s) {
   using C = PfCfg<D>;
-  static const cudaError_t smem_set =
-      cudaFuncSetAttribute(prefix_joined_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (smem_set != cudaSuccess) return smem_set;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(prefix_joined_kernel<D>, C::kSmem); err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -536,9 +535,8 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
 template <int D, int WM>
 cudaError_t prefix_launch_t(const PrefixParams& p, cudaStream_t s) {
   using C = PfCfg<D>;
-  static const cudaError_t smem_set =
-      cudaFuncSetAttribute(prefix_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (smem_set != cudaSuccess) return smem_set;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(prefix_kernel<D, WM>, C::kSmem); err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

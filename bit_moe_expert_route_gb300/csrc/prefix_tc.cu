@@ -373,9 +373,8 @@ cudaError_t prefix_tc_launch_t(const PrefixParams& p, cudaStream_t s) {
   memset(&args, 0, sizeof args);
   args.p = p;
   if (!encode_cache(&args.tm_k, p.kp, p, C::KT) || !encode_cache(&args.tm_v, p.vp, p, C::KT)) return cudaErrorInvalidValue;
-  static const cudaError_t smem_set =
-      cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (smem_set != cudaSuccess) return smem_set;
+  static SharedMemoryOptIn opt_in;
+  if (const cudaError_t err = opt_in(prefix_tc_kernel<D>, C::kSmem); err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
