@@ -49,6 +49,9 @@ MOE_DEVINL uint2 widen4(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// a / b rounded up; a may be any int.
+__host__ __device__ constexpr int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
+
 MOE_DEVINL void store_out(void* out, int f32, int64_t at, float v) {
   if (f32)
     static_cast<float*>(out)[at] = v;
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, M > 1 || NT <= 2 ? 3 : 2) gemm
 template <int M, int NT>
 cudaError_t few_launch(const GemmW8Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.N + 16 * M - 1) / (16 * M)), (unsigned)((p.T + 8 * NT - 1) / (8 * NT)));
+  cfg.gridDim = dim3((unsigned)ceil_div(p.N, 16 * M), (unsigned)ceil_div(p.T, 8 * NT));
   cfg.blockDim = dim3(32 * kFewWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int MT = (g.N + kTileN - 1) / kTileN, TT = (g.T + BN - 1) / BN, KB = (g.K + kKB - 1) / kKB;
+  const int MT = ceil_div(g.N, kTileN), TT = ceil_div(g.T, BN), KB = (g.K + kKB - 1) / kKB;
   const int64_t units = (int64_t)MT * TT;
 
   if (threadIdx.x == 0) {
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
       const uint32_t buf = tile % C::kAcc;
       const int64_t n = (u % MT) * kTileN + quarter * 32 + lane;
-      const int t0 = (int)(u / MT) * BN + group * kCols;
+      const int64_t t0 = u / MT * BN + group * kCols;  // (may pass 32 bits where the tile ends past the tokens)
       const float ws = n < g.N ? __ldg(g.w_scale + n) : 0.f;
       if (!warp_wait(&acc_full[buf], (tile / C::kAcc) & 1, abort_flag, g.status, 70)) break;
       tc_fence_after();
@@ -494,11 +497,12 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
         constexpr int kPut = kChunk < 32 ? kChunk : 32;  // tokens whose scales are at hand
 #pragma unroll
         for (int i0 = 0; i0 < kChunk; i0 += kPut) {
-          const int t = t0 + c0 + i0, live = g.T - t;
+          const int64_t t = t0 + c0 + i0;
+          const int live = (int)(g.T - t);
           __syncwarp();
           reinterpret_cast<float*>(scales)[lane] = lane < live ? __ldg(g.a_scale + t + lane) : 0.f;
           __syncwarp();
-          Out* dst = static_cast<Out*>(g.out) + (int64_t)t * g.ldo + n;
+          Out* dst = static_cast<Out*>(g.out) + t * g.ldo + n;
           auto put = [&](uint32_t acc, float as) {
             const float y = __uint_as_float(acc) * as * ws;
             if constexpr (F32)
@@ -569,7 +573,7 @@ cudaError_t many_launch_t(const GemmW8Params& p, int sms, cudaStream_t s) {
   cfg.blockDim = dim3(256);
   cudaError_t err = cudaLaunchKernelEx(&cfg, widen_kernel, p);
   if (err != cudaSuccess) return err;
-  const int64_t units = (int64_t)((p.N + kTileN - 1) / kTileN) * ((p.T + BN - 1) / BN);
+  const int64_t units = (int64_t)ceil_div(p.N, kTileN) * ceil_div(p.T, BN);
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, units));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
@@ -587,13 +591,13 @@ cudaError_t many_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
 // short and a block has little to do): 64 tokens by 4608 x 2048 weights 7.9 us
 // against 12.2, 64 by 2048 x 2048 4.6 against 12.2.
 bool gemm_w8_few(int T, int N, int K) {
-  const int64_t blocks = ((int64_t)N + 15) / 16 * (((int64_t)T + 31) / 32);
+  const int64_t blocks = (int64_t)ceil_div(N, 16) * ceil_div(T, 32);
   return T <= kW8FewTokens || blocks <= (int64_t)kW8RuleSms * (K < 1024 ? 2 : 4);
 }
 
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
   if (gemm_w8_few(p.T, p.N, p.K)) {
-    const int nt = (p.T + 7) / 8;
+    const int nt = ceil_div(p.T, 8);
     // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
     // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
     // 32 rows at 16 and 24, against 62 and 56 in tensor memory (taken with the
@@ -608,9 +612,9 @@ cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
   }
   // The token width whose waves cost least, by the measured time of a k-block
   // (about 0.48, 0.56 and 0.72 us at 64, 128 and 256 tokens) and a tile's ends.
-  const int64_t MT = (p.N + kTileN - 1) / kTileN, kb = (p.K + kKB - 1) / kKB;
+  const int64_t MT = ceil_div(p.N, kTileN), kb = (p.K + kKB - 1) / kKB;
   auto cost = [&](int bn, int64_t step, int64_t ends) {
-    return (MT * ((p.T + bn - 1) / bn) + sms - 1) / sms * (kb * step + ends);
+    return (MT * ceil_div(p.T, bn) + sms - 1) / sms * (kb * step + ends);
   };
   const int64_t c64 = cost(64, 48, 50), c128 = cost(128, 56, 80), c256 = cost(256, 72, 150);
   if (c256 <= c128 && c256 <= c64) return many_launch<256>(p, sms, s);

@@ -51,3 +51,34 @@ def test_a_failed_opt_in_is_not_kept(dev, call):
         L.fake_fail_attributes(1)
         assert call(L) != 0
         assert call(L) == 0
+
+
+MOST = 2**31 - 1  # tokens and output channels of the 8-bit product
+
+
+@pytest.mark.parametrize("T,N,K", [(MOST, 1, 16), (1, MOST, 16), (9, MOST, 16), (24, MOST - 10, 16), (40, MOST, 16),
+                                   (MOST - 100, 40000, 64), (300, MOST, 1024), (64, MOST - 126, 2048)])
+def test_the_products_largest_sizes(T, N, K):
+    """Grids cover every size that the interface takes: no sum next to 2^31 wraps."""
+    L = F.lib()
+    assert L.moe_gemm_w8a8_workspace_bytes(T, N, K) >= 256 and F.gemm(L, T, N, K) == 0
+    for name, grid, *_ in F.launches(L):
+        if name.startswith("gemm_w8_few"):
+            m, nt = (int(x) for x in name.split("<")[1][:-1].split(","))
+            assert grid[0] * 16 * m >= N and grid[1] * 8 * nt >= T
+        elif name == "widen_kernel":
+            assert grid[0] * 256 * 16 >= T * K
+        else:
+            assert grid[0] == 152
+
+
+def test_the_other_operators_largest_sizes():
+    L = F.lib()
+    P = F.P
+    for d in (8, 264, 2048, 16384):
+        assert L.moe_add_rmsnorm_q8(P, d, P, P, MOST, d, 1e-6, 0, P, P, P, P, None) == 0
+    for V in (2, 1000, 100000, 2**30 - 1):
+        assert L.moe_token_logprobs(P, 0, V, P, MOST, V, 2, P, P, P, P, None) == 0
+    for Pn, S, heads in ((2**28, 2**28, (1024, 1024, 64)), (0, 2**28, (16384, 1024, 64)), (2**28, 0, (16, 1, 256)), (0, 0, (16384, 1024, 256))):
+        for B in (1, 65535):
+            assert F.prefix(L, B, Pn, S, *heads) == 0, (B, Pn, S, heads)
