@@ -15,6 +15,7 @@
 namespace moe {
 
 constexpr int kStatusWords = 64;  // 256 bytes reserved at the start of each workspace
+constexpr int kTicketWord = 32;   // where a call's ticket is among them (64 bits)
 
 // ---------------------------------------------------------------- status
 // First fault wins: word 0 = moe_device_status, word 1 = where (kernel id),
@@ -299,6 +300,29 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 MOE_DEVINL uint32_t sw128_offset(uint32_t r, uint32_t chunk16) {
   return (r >> 3) * 1024u + (r & 7u) * 128u + ((chunk16 ^ (r & 7u)) << 4);
 }
+
+// ---------------------------------------------------------------- two launches back
+// griddepcontrol.wait makes what the launches before wrote visible to the grid that
+// executes it. A grid that starts beside its predecessor and does not wait for the
+// predecessor's end needs another chain to what the predecessor itself waited for: a
+// thread of the predecessor, past its wait, releases the call's ticket, and here a thread
+// acquires it (others follow through a barrier). Without the ticket after some polls:
+// the wait after all. Tickets differ from call to call, and a call's last kernel clears
+// the word, so that a graph that runs again does not find its earlier run's.
+MOE_DEVINL void release_ticket(uint64_t* word, uint64_t ticket) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(word), "l"(ticket) : "memory");
+}
+constexpr int kTicketPolls = 16;
+MOE_DEVINL void acquire_ticket(const uint64_t* word, uint64_t ticket) {
+  for (int i = 0; i < kTicketPolls; ++i) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
+    if (v == ticket) return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Orders the generic proxy's view of global memory before TMA loads by this thread.
+MOE_DEVINL void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // ---------------------------------------------------------------- misc math
 // Order-preserving map of a float onto uint32 (larger value, larger key);

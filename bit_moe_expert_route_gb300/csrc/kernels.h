@@ -308,6 +308,8 @@ struct GemmW8Params {
   int64_t ldo;
   uint16_t* a16;             // scratch f16 [T][K] (not few)
   int32_t* status;           // or null (few)
+  uint64_t* ticket_word;     // scratch (not few)
+  uint64_t ticket;           // the call's, not 0
 };
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s);
 
@@ -327,6 +329,8 @@ struct PrefixParams {
   int tc;                    // the prefix goes to prefix_tc_launch, 128 rows a block
   int row_warps, prefix_slice, prefix_splits, prefix_blocks, suffix_slice, suffix_splits;
   int32_t* status;           // or null (joined)
+  uint64_t* ticket_word;     // scratch (not joined)
+  uint64_t ticket;           // the call's, not 0
   float* part_o;             // [prefix_splits + suffix_splits][B Hq][d]
   float2* part_ml;           // [prefix_splits + suffix_splits][B Hq]: reference (log2), sum
   uint16_t* out;             // bf16 [B][Hq][d]

@@ -39,7 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 256;  // warp 0 TMA, warps 1 and 2 MMA, warps 4-7 softmax
+constexpr int kTcThreads = 256;  // warp 0 TMA, warps 1 and 2 MMA, warp 3 the ticket, warps 4-7 softmax
 constexpr float kLazyLog2 = 8.f;
 
 MOE_DEVINL float ex2(float x) {
@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
   asm volatile("griddepcontrol.launch_dependents;" :::);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-  if (warp == 0) {
+  if (warp == 3) {  // for the blocks that run beside this kernel (prefix.cu)
+    if (blockIdx.x == 0 && lane == 0) release_ticket(p.ticket_word, p.ticket);
+  } else if (warp == 0) {
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_last();  // the other row tiles read the same tiles
       int slot = 0, phase = 1, loads = 0;

@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer (include/step.h, and attention over
 // a shared prefix in include/attn.h): argument checks and launches.
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstring>
 
@@ -40,10 +41,24 @@ int device_sms() {
   return r;
 }
 
+// A number that no other call has: from the clock and a random place, then counted.
+uint64_t next_ticket() {
+  static std::atomic<uint64_t> next{
+      ((uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull) ^
+      (reinterpret_cast<uintptr_t>(&next_ticket) << 20)};
+  uint64_t t = 0;
+  while (t == 0) t = next.fetch_add(1, std::memory_order_relaxed);
+  return t;
+}
+uint64_t* ticket_word(void* ws) {
+  return ws ? reinterpret_cast<uint64_t*>(static_cast<int32_t*>(ws) + moe::kTicketWord) : nullptr;
+}
+
 // Lays the partial states out in the workspace; returns its bytes.
 size_t prefix_carve(moe::PrefixParams& p, void* ws) {
   const size_t states = (size_t)(p.prefix_splits + p.suffix_splits) * p.B * p.Hq;
   p.status = static_cast<int32_t*>(ws);
+  p.ticket_word = ticket_word(ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + 256);
   const size_t off = 256 + (states * sizeof(float2) + 255) / 256 * 256;
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off);
@@ -119,6 +134,8 @@ int moe_gemm_w8a8(const int8_t* a, int64_t lda, const float* a_scale, const int8
   p.out = out;
   p.ldo = ldo;
   p.status = static_cast<int32_t*>(ws);
+  p.ticket_word = ticket_word(ws);
+  p.ticket = next_ticket();
   p.a16 = ws ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + 256) : nullptr;
   return cuda_status(moe::gemm_w8_launch(p, sms, static_cast<cudaStream_t>(stream)));
 }
@@ -217,6 +234,7 @@ int moe_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint
   } else {
     moe::prefix_plan(p, sms);
     prefix_carve(p, ws);
+    p.ticket = next_ticket();
   }
   return cuda_status(moe::prefix_launch(p, static_cast<cudaStream_t>(stream)));
 }
