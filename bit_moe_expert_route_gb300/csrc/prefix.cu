@@ -478,7 +478,10 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.Hq;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket_word = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.ticket_word = 0;
+    if (p.prefix_splits + p.suffix_splits == 0) *p.status = 0;  // no launch before this one
+  }
   const int tid = threadIdx.x, c = tid % kCols, grp = tid / kCols, n = p.prefix_splits + p.suffix_splits;
   constexpr int kPer = (kMaxStates + 255) / 256;
   float2 ml[kPer];
