@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
     float4* scales = reinterpret_cast<float4*>(smem + C::kOffScale + (warp - C::kEpiWarp0) * 128);
     uint32_t tile = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // (the scales)
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++tile) {
+    int64_t u = blockIdx.x;
+    for (; u < units; u += gridDim.x, ++tile) {
       const uint32_t buf = tile % C::kAcc;
       const int64_t n = (u % MT) * kTileN + quarter * 32 + lane;
       const int64_t t0 = u / MT * BN + group * kCols;  // (may pass 32 bits where the tile ends past the tokens)
@@ -539,6 +540,14 @@ __global__ void __launch_bounds__(CfgW8<BN>::kThreads, 1) gemm_w8_kernel(const _
           }
         }
       }
+    }
+    // after a wait that ran out: what was not computed is NaN, beside the status
+#pragma unroll 1
+    for (; u < units; u += gridDim.x) {
+      const int64_t n = (u % MT) * kTileN + quarter * 32 + lane, t0 = u / MT * BN + group * kCols;
+#pragma unroll 1
+      for (int64_t t = t0; t < t0 + kCols && t < g.T; ++t)
+        if (n < g.N) store_out(g.out, F32, t * g.ldo + n, __int_as_float(0x7fc00000));
     }
   }
   __syncwarp();  // the single-lane roles join their warps

@@ -322,10 +322,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       if (++buf == NB) buf = 0, turn ^= 1;
     }
     // the slice's state: every product is complete with the last one
-    if (alive && warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 90)) {
+    const bool mine = row0 + r < R;
+    const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);
+    if (alive) alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 90);
+    if (!alive) {  // after a wait that ran out: a state that makes the row NaN, beside the status
+      if (mine) p.part_ml[at] = make_float2(0.f, __int_as_float(0x7fc00000));
+    } else {
       tc_fence_after();
-      const bool mine = row0 + r < R;
-      const int64_t at = (int64_t)split * p.B * p.Hq + (mine ? query_row(row0 + r) : 0);
       if (l != l && m == -INFINITY) m = 0.f;  // nothing but NaN: not a state without positions
       if (mine) p.part_ml[at] = make_float2(m, l);
       // through shared memory (the ring is free: every product is complete), so

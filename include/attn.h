@@ -69,7 +69,8 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  *                       (no initialisation needed), holds the status word.
  *                       May be NULL where little work takes one launch (then
  *                       nothing in it can fail); MOE_ERR_WORKSPACE says that it
- *                       may not, before anything is enqueued
+ *                       may not, before anything is enqueued. Where the status
+ *                       says MOE_DEV_TIMEOUT, the rows not computed are NaN
  * All pointers but lens (4 bytes) 16-byte aligned, strides multiples of 8
  * elements. 0 <= B <= 65535 (0 launches nothing), P and S up to 2^28, d in {64,
  * 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a

@@ -67,7 +67,8 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
  *   ws       256-byte aligned, >= moe_gemm_w8a8_workspace_bytes(T, N, K) bytes
  *            (no initialisation needed), holds the status word; may be NULL
  *            where that is 256 (then nothing in the call can fail), always so
- *            for up to MOE_W8A8_NO_WORKSPACE_T tokens
+ *            for up to MOE_W8A8_NO_WORKSPACE_T tokens. Where the status says
+ *            MOE_DEV_TIMEOUT, what was not computed is NaN
  * a and w 16-byte aligned; T >= 0 (0 launches nothing), N >= 1, K a multiple of
  * 16, 16 <= K <= 65536, T * K < 2^40. The integer sum is exact while its partial sums stay
  * below 2^24 in magnitude (always for K <= 1024), else it carries fp32
