@@ -171,16 +171,16 @@ cudaError_t few_launch(const GemmW8Params& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, gemm_w8_few_kernel<M, NT>, p);
 }
 // ---------------------------------------------------------------- many tokens
-// The tokens' codes as f16 rows of K, contiguous; clears the status word. The last
+// The tokens' codes as f16 rows of K, contiguous; clears the status word. The first
 // block releases the ticket with which the product's weight stream starts.
 __global__ void __launch_bounds__(256) widen_kernel(const GemmW8Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  if (blockIdx.x == gridDim.x - 1) {  // a block of its own: the others need not wait for the release
+  if (blockIdx.x == 0) {  // a block of its own: the others need not wait for the release
     if (threadIdx.x == 0) release_ticket(p.ticket_word, p.ticket);
     return;
   }
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.x - 1) * 256 + threadIdx.x;
   const int vecs = p.K / 16;
   if (i == 0) *p.status = 0;
   if (i >= (int64_t)p.T * vecs) return;
