@@ -382,9 +382,11 @@ def _want(fn, name, t, dtype, shape, rows=False):
 def _want_cache(fn, name, k, v, shape):
     """The addresses of a K and a V cache whose heads are contiguous, and their strides (which
     have to be the same)."""
-    bf, st = torch.bfloat16, k.stride()
+    bf, st, sv = torch.bfloat16, k.stride(), v.stride()
+    if st != sv and k.shape == v.shape:  # the stride of an axis of one entry says nothing
+        sv = tuple(a if n == 1 else b for n, a, b in zip(k.shape, st, sv))
     if (k.dtype is bf and v.dtype is bf and k.shape == shape and v.shape == shape and k.is_cuda
-            and v.is_cuda and (k.numel() == 0 or st == v.stride() and st[-1] == 1
+            and v.is_cuda and (k.numel() == 0 or st == sv and st[-1] == 1
                                and (st[-2] == shape[-1] or shape[-2] == 1))):
         return k.data_ptr(), v.data_ptr(), st
     for n, t in (("k_" + name, k), ("v_" + name, v)):
