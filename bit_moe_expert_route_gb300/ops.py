@@ -396,6 +396,13 @@ def _want_cache(fn, name, k, v, shape):
     raise ValueError(f"{fn}: k_{name} and v_{name} have different strides or scattered heads")
 
 
+def _want_ws(fn, ws):
+    """The address and bytes of the caller's workspace."""
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws is not contiguous memory on the GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _ld(t):
     """Elements from one row of a 2-D tensor to the next (its width where there is one row)."""
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -465,7 +472,7 @@ def gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         po = _want(fn, "out", out, dtype, (T, N), rows=True)
     pws, nbytes = None, 0
     if ws is not None:
-        pws, nbytes = ws.data_ptr(), ws.numel()
+        pws, nbytes = _want_ws(fn, ws)
     elif T > W8A8_NO_WORKSPACE_T:
         nbytes = lib().moe_gemm_w8a8_workspace_bytes(T, N, K)
         if nbytes == 0:
@@ -497,6 +504,8 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     B, Hq, d = q.shape
     P, Hkv = k_prefix.shape[:2]
     fn, bf, dev = "prefix_attention", torch.bfloat16, q.device
+    if k_suffix is None and v_suffix is not None:
+        raise ValueError(f"{fn}: v_suffix without k_suffix")
     pq = _want(fn, "q", q, bf, (B, Hq, d))
     pk, pv, ld = _want_cache(fn, "prefix", k_prefix, v_prefix, (P, Hkv, d))
     S, pks, pvs, lds, pl = 0, None, None, (0, 0), None
@@ -514,8 +523,10 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     width = Hkv * d  # the stride of an axis of one entry says nothing
     args = (pq, pk, pv, ld[0] if P > 1 else width, pks, pvs, lds[0] if B > 1 else 0,
             lds[1] if S > 1 else width, pl, B, P, S, Hq, Hkv, d, scale, po)
-    rc = -4
-    if ws is None and P + S <= PREFIX_NO_WORKSPACE_POSITIONS:  # little work needs none
+    rc, pws, nbytes = -4, None, 0
+    if ws is not None:
+        pws, nbytes = _want_ws(fn, ws)
+    elif P + S <= PREFIX_NO_WORKSPACE_POSITIONS:  # little work needs none
         rc = lib().moe_prefix_attention(*args, None, 0, _stream())
     if rc == -4:
         if ws is None:
@@ -523,7 +534,8 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
             if nbytes == 0:
                 raise MoeError("moe_prefix_attention_workspace_bytes", -3)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        rc = lib().moe_prefix_attention(*args, ws.data_ptr(), ws.numel(), _stream())
+            pws = ws.data_ptr()
+        rc = lib().moe_prefix_attention(*args, pws, nbytes, _stream())
     _check("moe_prefix_attention", rc)
     return out
 

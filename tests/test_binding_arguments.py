@@ -21,3 +21,30 @@ def test_strides_of_axes_of_one_entry_do_not_count():
         assert torch.equal(ops.prefix_attention(q, kp, odd(vp), ks, odd(vs), ln), want)
         assert torch.equal(ops.prefix_attention(q, odd(kp), vp, odd(ks), vs, ln), want)
         A.check(want, *A.expected(q, kp, vp, ks, vs, ln))
+
+
+def test_values_without_keys():
+    from bit_moe_expert_route_gb300 import ops
+    q, k = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="k_suffix"):
+        ops.prefix_attention(q, k, k, v_suffix=torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16))
+
+
+@gpu
+def test_workspaces_that_no_kernel_can_use():
+    """Host memory, and views with gaps, are refused before anything is enqueued; a workspace of
+    another type counts in bytes."""
+    import test_gemm_w8a8 as W
+    import test_prefix_attention as A
+    from bit_moe_expert_route_gb300 import ops
+    x, y = W.inputs(40, 20000, 64, 1), A.inputs(4, 3000, 20, 16, 2, 64, 1)
+    n = ops.lib().moe_gemm_w8a8_workspace_bytes(40, 20000, 64)
+    m = ops.lib().moe_prefix_attention_workspace_bytes(4, 3000, 20, 16, 2, 64)
+    for call, size in ((lambda ws: ops.gemm_w8a8(*x, ws=ws), n), (lambda ws: ops.prefix_attention(*y, ws=ws), m)):
+        for ws in (torch.empty(size, dtype=torch.uint8), torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError, match="ws"):
+                call(ws)
+        with pytest.raises(ops.MoeError):
+            call(torch.empty(size - 1, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(call(torch.empty(size // 4 + 1, dtype=torch.int32, device="cuda")),
+                           call(torch.empty(size, dtype=torch.uint8, device="cuda")))
