@@ -61,12 +61,17 @@ class Continuations:
         self.k_own = torch.zeros(batch, room, Hkv, d, dtype=torch.bfloat16, device="cuda")
         self.v_own = torch.zeros_like(self.k_own)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.steps = 0  # taken: the positions in use, on the host
         self.embedding = normal(vocab, D)
         self.rows = torch.arange(batch, device="cuda")
 
     def step(self, tokens: torch.Tensor, wanted: torch.Tensor, top_k: int = 5) -> dict:
         """One token of every continuation (int32 [batch]); scores the tokens that come next
-        (`wanted`). Returns every intermediate by name, the scores as "scores"."""
+        (`wanted`). Returns every intermediate by name, the scores as "scores". `room` steps at
+        most."""
+        if self.steps >= self.room:
+            raise ValueError(f"the continuations' caches hold {self.room} positions, all in use")
+        self.steps += 1
         B, (Hq, Hkv, d) = self.batch, self.heads
         x = self.embedding[tokens.long()]
         n1 = ops.add_rmsnorm_q8(x, self.norms[0])
