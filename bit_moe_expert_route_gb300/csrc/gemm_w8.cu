@@ -15,8 +15,8 @@
 // and splits K over its 8 warps; a lane loads 16 consecutive codes of two
 // rows per m16n8k16 product quadruple (the order of k is free as long as both
 // operands agree, so the fragments need no shuffling), and the warps' sums
-// meet in shared memory. One token by 4608 x 2048 weights: 3.2 us; 8 tokens by
-// 100003 x 2048: 37 us (5.5 TB/s, 81% of the measured copy); 24: 52 us.
+// meet in shared memory. One token by 4608 x 2048 weights: 3.4 us; 8 tokens by
+// 100003 x 2048: 35 us (5.9 TB/s, 87% of the measured copy); 24: 52 us.
 //
 // More tokens: tcgen05. The MMA's M side is 128 weight rows, its N side up to
 // 256 tokens. TMA brings the packed weight codes, converter warps write them as
@@ -619,12 +619,15 @@ bool gemm_w8_few(int T, int N, int K) {
 cudaError_t gemm_w8_launch(const GemmW8Params& p, int sms, cudaStream_t s) {
   if (gemm_w8_few(p.T, p.N, p.K)) {
     const int nt = ceil_div(p.T, 8);
-    // Rows a block: more reuse the tokens' fragments, fewer fill the machine.
-    // 100003 x 2048 weights: 37 us with 64 rows up to 8 tokens; 42 and 52 us with
-    // 32 rows at 16 and 24, against 62 and 56 in tensor memory (taken with the
-    // weights' loads at normal priority), which is ahead from 25 (47 against 63 at 32).
+    // Rows a block: more reuse the tokens' fragments, fewer fill the machine. With 32
+    // rows 100003 x 2048 weights take 34, 35, 42 and 52 us at 1, 8, 16 and 24 tokens
+    // (with 64 rows 35 and 37 at 1 and 8; 32768 x 8192 at 1 token 44 to 47 against 55). In
+    // tensor memory they take 60 us at 17 tokens, 55 at 24 and 49 at 25, from where
+    // it serves. It is ahead sooner by long rows (17 and 24 tokens by 32768 x 8192: 59
+    // us against 67 and 69; by 20480 x 4096 31 against 25), but wants a workspace,
+    // which the interface promises not to want up to 24 tokens.
     if (p.N >= 32 * 4 * kW8RuleSms) {  // several blocks an SM even so
-      if (nt == 1) return few_launch<4, 1>(p, s);
+      if (nt == 1) return few_launch<2, 1>(p, s);
       return nt == 2 ? few_launch<2, 2>(p, s) : few_launch<2, 3>(p, s);
     }
     if (nt == 1) return few_launch<1, 1>(p, s);

@@ -14,7 +14,7 @@ gpu = pytest.mark.gpu
 KS = [16, 64, 128, 144, 8192]  # less than a k-block, whole and ragged ones, sums past 2^24
 PRODUCTS = [(kernel, T, N, K) for kernel, T, N, ks in (
     ("gemm_w8_few_kernel<1, 1>", 5, 300, KS), ("gemm_w8_few_kernel<1, 2>", 16, 300, KS), ("gemm_w8_few_kernel<1, 3>", 24, 300, KS),
-    ("gemm_w8_few_kernel<1, 4>", 70, 300, KS), ("gemm_w8_few_kernel<4, 1>", 8, 20011, KS), ("gemm_w8_few_kernel<2, 2>", 13, 20011, KS),
+    ("gemm_w8_few_kernel<1, 4>", 70, 300, KS), ("gemm_w8_few_kernel<2, 1>", 8, 20011, KS), ("gemm_w8_few_kernel<2, 2>", 13, 20011, KS),
     ("gemm_w8_few_kernel<2, 3>", 24, 20011, KS), ("gemm_w8_kernel<64, false>", 40, 20011, KS), ("gemm_w8_kernel<64, false>", 64, 40000, KS),
     ("gemm_w8_kernel<128, false>", 100, 20011, KS), ("gemm_w8_kernel<128, false>", 300, 40000, KS[:4]),
     ("gemm_w8_kernel<256, false>", 4097, 20011, KS[:4]), ("gemm_w8_kernel<256, false>", 300, 40000, KS[4:])) for K in ks]
