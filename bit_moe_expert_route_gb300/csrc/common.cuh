@@ -103,8 +103,35 @@ MOE_DEVINL void mbar_arrive_warp(uint64_t* bar) {
   if ((threadIdx.x & 31) == __ffs(mask) - 1) mbar_arrive(bar);
 }
 
+// mbar_wait by a whole warp: every lane gets one answer, and the lanes are
+// together again after it. (A lane may see the phase complete a poll later than
+// another; tcgen05.ld and .st need the warp undivided, and an arrival on
+// behalf of the warp must happen once.)
+MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                          int32_t* status, int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
+}
+MOE_DEVINL void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+
 MOE_DEVINL void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- thread-block clusters
+MOE_DEVINL void cluster_sync() {
+  __syncwarp();  // (the barrier wants warps undivided)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The address of `q` in the shared memory of the cluster's block r.
+MOE_DEVINL uint32_t remote_addr(const void* q, uint32_t r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
+  return a;
 }
 
 // ---------------------------------------------------------------- TMA
@@ -334,6 +361,28 @@ MOE_DEVINL uint32_t order_key(float v) {
 }
 MOE_DEVINL float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+MOE_DEVINL float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The larger of two values, NaN where one is.
+MOE_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+MOE_DEVINL uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two values as bf16, and what that leaves of them as bf16 too (2^-16 of each at most).
+MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x, y);
+  lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 MOE_DEVINL float bf16_bits_to_f32(uint16_t b) { return __uint_as_float(((uint32_t)b) << 16); }

@@ -244,19 +244,6 @@ struct W8Args {
   GemmW8Params g;
 };
 
-// mbar_wait by a whole warp: every lane gets one answer, and the lanes are
-// together again after it. (A lane may see the phase complete a poll later than
-// another; tcgen05.ld and .st need the warp undivided, and an arrival on
-// behalf of the warp must happen once.)
-MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
-}
-MOE_DEVINL void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-  __syncwarp();
-}
-
 // Roles: warp 0 streams the packed weights, warp 1 issues the MMAs, warp 2
 // streams the tokens' operand (with two issuers warp 3 is the other), then the
 // converters' warps and the epilogue's.

@@ -294,7 +294,9 @@ cudaError_t logprob_launch(const LogprobParams& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integer product
 constexpr int kW8FewTokens = 24;  // up to here no scratch at any size
-constexpr int kW8RuleSms = 152;   // for which its rules on sizes were measured
+// The SM count for which its rules on sizes were measured. (Not the device's: the
+// workspace's size, asked for without a device, has to follow from the sizes alone.)
+constexpr int kW8RuleSms = 152;
 // Whether the sizes go to the kernel without scratch or waits that could fail.
 bool gemm_w8_few(int T, int N, int K);
 struct GemmW8Params {

@@ -44,16 +44,6 @@ constexpr float kLazy = 20.f;  // e^20: fp32 sums hold it easily
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 
-MOE_DEVINL float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-MOE_DEVINL float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // The order of a logit among the top alternatives: larger value, larger rank;
 // NaN below every number (rank 1), 0 = no element.
@@ -246,16 +236,6 @@ MOE_DEVINL void merge_lists(uint64_t (*list)[32], int n, int warp, int lane) {
   __syncthreads();
 }
 
-MOE_DEVINL void cluster_sync() {
-  __syncwarp();  // (the barrier wants warps undivided)
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of `q` in the shared memory of the cluster's block r.
-MOE_DEVINL uint32_t remote_addr(const void* q, uint32_t r) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
-  return a;
-}
 MOE_DEVINL float remote_f32(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");

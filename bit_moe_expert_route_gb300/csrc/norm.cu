@@ -37,18 +37,6 @@ MOE_DEVINL void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-MOE_DEVINL uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// The larger of two values, NaN where one is.
-MOE_DEVINL float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Adding this and taking it away rounds |t| < 2^22 to a whole number (its low
 // byte, in two's complement, ends in the sum's), or |t| < 2^13 to a multiple
 // of 2^-9 (the spacing of e4m3 below 2^-6).
@@ -203,8 +191,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
         float f[8], g[8];
         unpack8(r[i], f);
         unpack8(s[i], g);
-        r[i] = make_uint4(pack2(f[0] + g[0], f[1] + g[1]), pack2(f[2] + g[2], f[3] + g[3]),
-                          pack2(f[4] + g[4], f[5] + g[5]), pack2(f[6] + g[6], f[7] + g[7]));
+        r[i] = make_uint4(pack_bf16(f[0] + g[0], f[1] + g[1]), pack_bf16(f[2] + g[2], f[3] + g[3]),
+                          pack_bf16(f[4] + g[4], f[5] + g[5]), pack_bf16(f[6] + g[6], f[7] + g[7]));
       }
     }
 #pragma unroll
@@ -326,8 +314,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int G) {
           }
         }
         *reinterpret_cast<uint4*>(p.values + base + 8 * v) =
-            make_uint4(pack2(t[0] * scale, t[1] * scale), pack2(t[2] * scale, t[3] * scale),
-                       pack2(t[4] * scale, t[5] * scale), pack2(t[6] * scale, t[7] * scale));
+            make_uint4(pack_bf16(t[0] * scale, t[1] * scale), pack_bf16(t[2] * scale, t[3] * scale),
+                       pack_bf16(t[4] * scale, t[5] * scale), pack_bf16(t[6] * scale, t[7] * scale));
       }
     }
   }

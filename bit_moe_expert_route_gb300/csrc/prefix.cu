@@ -31,15 +31,12 @@ namespace {
 constexpr int kPfThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr float kLazyLog2 = 8.f;
+// (Two blocks on each of the 152 SMs for which the rule was measured; whether a call
+// needs a workspace has to follow from its sizes alone.)
 constexpr int kJoinedBlocks = 304, kJoinedTiles = 4, kJoinedWork = 2048;
 static_assert(kJoinedTiles * 8 * kTileKeys == kPrefixJoinedPositions, "eight blocks' tiles");
 constexpr int kPrefixTcMin = 256;  // positions from which the tensor-memory kernel takes a prefix
 
-MOE_DEVINL float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 MOE_DEVINL void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -57,16 +54,6 @@ MOE_DEVINL void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uin
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-MOE_DEVINL uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Two values as bf16, and what that leaves of them as bf16 too (2^-16 of each at most).
-MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(x, y);
-  lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of D bf16 a row: chunks
@@ -359,17 +346,6 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<D>::kBlocks) prefix_kernel(c
     }
   }
   if (beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-MOE_DEVINL void cluster_sync() {
-  __syncwarp();  // (the barrier wants warps undivided)
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of `q` in the shared memory of the cluster's block r.
-MOE_DEVINL uint32_t remote_addr(const void* q, uint32_t r) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
-  return a;
 }
 
 // Little work: a cluster takes one sequence and KV head, its blocks slices of the

@@ -42,12 +42,6 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 256;  // warp 0 TMA, warps 1 and 2 MMA, warp 3 the ticket, warps 4-7 softmax
 constexpr float kLazyLog2 = 8.f;
 
-MOE_DEVINL float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 template <int D>
 struct TcCfg {
   static constexpr int KT = D == 256 ? 64 : 128;    // keys a tile
@@ -71,24 +65,6 @@ struct TcArgs {
   CUtensorMap tm_k, tm_v;  // [P][Hkv d], box 64 x KT
   PrefixParams p;
 };
-
-// Two values as bf16, and what that leaves of them as bf16 too (2^-16 of each at most).
-MOE_DEVINL void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-
-// A wait by a whole warp; its lanes are together again after it.
-MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, where));
-}
-MOE_DEVINL void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-  __syncwarp();
-}
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of N
 // a 128-byte row, one row a key; blocks of 64 N `block` bytes apart, groups of
