@@ -64,7 +64,9 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  *   lens                int32 [B] device, 0 .. S (others are clamped); NULL when S == 0
  *   scale               multiplies every score; <= 0 means 1 / sqrt(d)
  *   out                 bf16 [B][n_q_heads][d]; zeros for a sequence without any
- *                       position (P == 0 and len[b] == 0)
+ *                       position (P == 0 and len[b] == 0), and for a row whose
+ *                       every score is -infinity; NaN for a row with a score that
+ *                       is NaN or +infinity
  *   ws                  256-byte aligned, >= moe_prefix_attention_workspace_bytes
  *                       (no initialisation needed), holds the status word.
  *                       May be NULL where little work takes one launch (then

@@ -70,10 +70,11 @@ int moe_add_rmsnorm_q8(const uint16_t* x, int64_t ldx, const uint16_t* residual,
  *            for up to MOE_W8A8_NO_WORKSPACE_T tokens. Where the status says
  *            MOE_DEV_TIMEOUT, what was not computed is NaN
  * a and w 16-byte aligned; T >= 0 (0 launches nothing), N >= 1, K a multiple of
- * 16, 16 <= K <= 65536, T * K < 2^40. The integer sum is exact while its partial sums stay
- * below 2^24 in magnitude (always for K <= 1024), else it carries fp32
- * rounding; the scales multiply it in fp32 and the result is rounded once. One
- * launch for few tokens or little work, else two.
+ * 16, 16 <= K <= 65536, T * K < 2^40. The integer sum is exact while its
+ * partial sums stay below 2^24 in magnitude (always for K <= 1024); a larger one is
+ * held in fp32, and each step of 16 codes may cost it 2^-23 of itself (the tensor
+ * cores may truncate). The scales multiply it in fp32 and the result is rounded
+ * once. One launch for few tokens or little work, else two.
  */
 #define MOE_W8A8_NO_WORKSPACE_T 24
 size_t moe_gemm_w8a8_workspace_bytes(int T, int N, int K);
