@@ -24,7 +24,7 @@
 // only the tokens' operand to the MMA. The tokens' codes (far fewer) are
 // widened to f16 in the workspace by a first kernel; its launch lets the
 // product's start early, and the product's weight stream does not wait for it.
-// 8192 x 8192 x 2048: 182 us, 1.51 PFLOP/s (81% of the measured burst rate); the
+// 8192 x 8192 x 2048: 183 us, 1.50 PFLOP/s (77% of the measured burst rate); the
 // MMAs alone take 151 us at the clock that power leaves.
 #include <cuda.h>
 #include <cudaTypedefs.h>

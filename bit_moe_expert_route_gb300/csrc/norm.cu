@@ -15,7 +15,7 @@
 // products lifted by a's exponent.)
 //
 // Bound by HBM: 7 bytes an element (x, residual in; residual, q out), 9 with
-// the bf16 values: 32768 rows of 2048 in 94 us with the values, 6.4 TB/s (95% of
+// the bf16 values: 32768 rows of 2048 in 93 us with the values, 6.5 TB/s (95% of
 // the measured copy). A row belongs to G threads of NV 16-byte vectors each,
 // whole warps, joined by one barrier.
 #include <cuda_fp8.h>

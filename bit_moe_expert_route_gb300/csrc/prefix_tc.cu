@@ -13,8 +13,8 @@
 // K and V tiles come by TMA into one ring of slots in the order in which the
 // products use them (K0 K1 V0 K2 V1 ...); V is read as it lies (MN-major
 // operand, no transpose). Every query row of a KV head's sequences shares
-// these tiles. At head size 256 with 512 rows a tile of 64 keys takes 1.05 us
-// (about 2000 cycles), 1824 of them the MMAs' (16 of N = 64 at their least time
+// these tiles. At head size 256 with 512 rows a tile of 64 keys takes 1.1 us
+// (about 2050 cycles), 1824 of them the MMAs' (16 of N = 64 at their least time
 // of 50, 8 of N = 256 at 128). Few rows and a long prefix are bound by HBM: 128
 // rows, 8 KV heads of 128, 131072 positions in 91 us, 5.9 TB/s. (Asking L2 for
 // tiles ahead of the ring made it a third more.)
