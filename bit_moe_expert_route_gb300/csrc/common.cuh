@@ -149,6 +149,16 @@ MOE_DEVINL void tma_load_2d(void* smem_dst, const void* desc, int32_t c0, int32_
       : "memory");
 }
 
+// The same of a 4-D tensor.
+MOE_DEVINL void tma_load_4d(void* smem_dst, const void* desc, int32_t c0, int32_t c1, int32_t c2, int32_t c3, uint64_t* bar,
+                            uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(cache_hint)
+      : "memory");
+}
+
 // L2 cache-policy handles for TMA loads.
 MOE_DEVINL uint64_t l2_policy_evict_first() {
   uint64_t p;
@@ -303,6 +313,19 @@ MOE_DEVINL uint64_t smem_desc_sw128(uint32_t saddr) {
   d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;  // stride byte offset
   d |= (uint64_t)1u << 46;                        // descriptor version (tcgen05)
   d |= (uint64_t)2u << 61;                        // swizzle mode: 128 B
+  return d;
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of N
+// a 128-byte row, one row a key; blocks of 64 N `block` bytes apart, groups of
+// 8 keys 1024 bytes apart.
+MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
   return d;
 }
 

@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "cache.h"
 #include "moe.h"
 
 namespace moe {
@@ -347,5 +348,52 @@ void prefix_plan(PrefixParams& p, int sms);
 // The prefix's partial states from tcgen05 products.
 cudaError_t prefix_tc_launch(const PrefixParams& p, cudaStream_t s);
 cudaError_t prefix_launch(const PrefixParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------- head norms, rotation, appending to a paged cache
+struct RopeParams {
+  struct Part {              // queries and keys, or keys and values
+    const uint16_t* src;     // tokens ld apart
+    int64_t ld;
+    int heads;
+    const uint16_t* weight;  // or null
+    uint16_t* dst;           // tokens ld_dst apart, or the pages
+    int64_t ld_dst;
+    int turn;
+  } part[2];
+  int T, d;
+  float eps;
+  const float* freqs;
+  const int32_t* positions;  // or null (paged: the position in the cache)
+  int64_t ld_positions;
+  int pairs, n_axes, cyclic, adjacent;
+  int sections[MOE_ROPE_MAX_AXES];
+  // appending (starts not null)
+  const int32_t *starts, *lens, *rows, *table;
+  int64_t ld_table, page_stride, position_stride, head_stride;
+  int B, n_rows, width, n_pages, page_log2;
+  int split;                 // warps a token (set by the launch)
+};
+cudaError_t rope_launch(const RopeParams& p, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- attention of new tokens over a paged cache
+constexpr int kTreeMaxSms = 160;  // bounds the partial states
+constexpr int kTreeRows = 128;    // query rows a tile
+struct TreeParams {
+  const uint16_t* q;         // tokens ldq apart
+  int64_t ldq;
+  const uint16_t *k_pages, *v_pages;
+  int64_t page_stride, position_stride, head_stride, ld_table;
+  const int32_t *table, *starts, *lens;
+  const int64_t* tree;       // or null
+  int N, B, Hq, Hkv, d, width, n_pages, page_log2;
+  float scale_log2;          // scale * log2 e
+  int ctas, rows;            // blocks; rows of a partial state
+  int32_t* status;
+  int64_t* begin;            // [B + 1] scratch: a sequence's first tile of all
+  float2* part_ml;           // [2 ctas][rows]: reference (log2), sum
+  float* part_o;             // [2 ctas][rows][d]
+  uint16_t* out;             // [N][Hq][d]
+};
+cudaError_t tree_launch(const TreeParams& p, cudaStream_t s);
 
 }  // namespace moe

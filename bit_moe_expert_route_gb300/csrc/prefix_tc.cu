@@ -66,19 +66,6 @@ struct TcArgs {
   PrefixParams p;
 };
 
-// Descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of N
-// a 128-byte row, one row a key; blocks of 64 N `block` bytes apart, groups of
-// 8 keys 1024 bytes apart.
-MOE_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ TcArgs args) {
   using C = TcCfg<D>;

@@ -123,6 +123,14 @@ def lib():
         L.moe_prefix_attention_workspace_bytes.argtypes = [i32] * 6
         L.moe_prefix_attention.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, vp] + [i32] * 6 + [
             ctypes.c_float, vp, vp, sz, vp]
+        L.moe_qk_norm_rope.argtypes = [vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float,
+                                       vp, vp, i64, vp, i64, vp]
+        L.moe_append_paged.argtypes = [vp, i64, vp, i64, vp, i32, i32, vp, vp, vp, vp,
+                                       ctypes.c_float, vp, vp]
+        L.moe_tree_attention_workspace_bytes.restype = sz
+        L.moe_tree_attention_workspace_bytes.argtypes = [i32, i32, vp]
+        L.moe_tree_attention.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp,
+                                         sz, vp]
         L.moe_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int32)]
         L.moe_debug_decode_fault.argtypes = [ctypes.c_uint64, i32]
         _lib = L
@@ -576,6 +584,228 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
                                   entropy.data_ptr(), pt, pp, _stream())
     _check("moe_token_logprobs", rc)
     return TokenLogprobs(logprob, entropy, top_ids, top_lp)
+
+
+# ------------------------------------------------------------------ the paged cache
+class Rope(NamedTuple):
+    """A rotation of heads by position (moe_rope, include/cache.h): freqs fp32 [pairs] on the GPU,
+    radians a position; sections: pairs of each axis of the positions (None: one axis), in blocks or
+    cyclic; adjacent: pairs are elements (2i, 2i + 1), else (i, i + pairs)."""
+    freqs: torch.Tensor
+    sections: tuple | None = None
+    cyclic: bool = False
+    adjacent: bool = False
+
+
+class PagedCache(NamedTuple):
+    """Keys and values in pages (moe_paged, include/cache.h): k_pages, v_pages bf16 [n_pages, page,
+    Hkv, d] with the same strides (views of other orders too), table int32 [B, width]: position p of
+    sequence b is place p % page of page table[b, p // page]."""
+    k_pages: torch.Tensor
+    v_pages: torch.Tensor
+    table: torch.Tensor
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64),
+                ("pairs", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("cyclic", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
+
+
+class _PagedArgs(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "position_stride", "head_stride")] + [
+        ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page", "width", "n_sequences", "n_kv_heads", "d")]
+
+
+def rope_freqs(rotary: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Frequencies theta^(-2i / rotary), i < rotary / 2, as Rope takes them (rounded to fp32 once)."""
+    i = torch.arange(0, rotary, 2, dtype=torch.float64)
+    return (float(theta) ** (-i / rotary)).to(torch.float32).to(device)
+
+
+def tree_masks(parents) -> tuple[torch.Tensor, torch.Tensor]:
+    """Masks and depths of a tree of drafted tokens: parents[i] is the index (below i) of the token
+    that token i follows, or -1 where that is the last one before the draft. Returns int64 [n], a bit
+    for each token on the path to i and i itself (tree_attention's `tree`), and int32 [n], how many
+    drafted tokens come before i on it (a token's position is the cached ones' number plus that), on
+    the CPU."""
+    bits, depths = [], []
+    for i, j in enumerate(parents):
+        if not -1 <= j < i or i >= 64:
+            raise ValueError(f"tree_masks: parents[{i}] is {j}, an earlier token or -1 (and 64 tokens) is wanted")
+        bits.append((1 << i) | (bits[j] if j >= 0 else 0))
+        depths.append(depths[j] + 1 if j >= 0 else 0)
+    signed = [m - (1 << 64) if m >> 63 else m for m in bits]
+    return torch.tensor(signed, dtype=torch.int64), torch.tensor(depths, dtype=torch.int32)
+
+
+def _here(fn, *named):
+    """Refuses tensors that are not on the current device, whose stream the call goes to."""
+    dev = torch._C._cuda_getDevice()
+    for name, t in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, cuda:{dev} is the current device")
+
+
+def _want_heads(fn, name, t, shape):
+    """The address of bf16 [tokens, heads, d] whose heads are contiguous, and its tokens' stride."""
+    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, "
+                         f"torch.bfloat16 {tuple(shape)} on the GPU is wanted")
+    (T, H, d), st = shape, t.stride()
+    if t.numel() and (st[2] != 1 or (H > 1 and st[1] != d)):
+        raise ValueError(f"{fn}: {name} has scattered heads")
+    return t.data_ptr(), st[0] if T > 1 else H * d  # the stride of an axis of one entry says nothing
+
+
+def _rope_args(fn, rope, positions, T):
+    """moe_rope of a rotation for T tokens (None: none)."""
+    if rope is None:
+        if positions is not None:
+            raise ValueError(f"{fn}: positions without rope")
+        return None
+    pairs = rope.freqs.numel()
+    sections = (pairs,) if rope.sections is None else tuple(rope.sections)
+    A = len(sections)
+    if not 1 <= A <= 4:
+        raise ValueError(f"{fn}: {A} sections, 1 to 4 are wanted")
+    pf, pp, ld = _want(fn, "rope.freqs", rope.freqs, torch.float32, (pairs,)), None, 0
+    if positions is not None:
+        if positions.dim() == 1 and A == 1:
+            positions = positions[None]
+        pp = _want(fn, "positions", positions, torch.int32, (A, T), rows=True) if T else None
+        ld = positions.stride(0) if A > 1 else 0
+        _here(fn, ("positions", positions))
+    _here(fn, ("rope.freqs", rope.freqs))
+    return ctypes.byref(_RopeArgs(pf, pp, ld, pairs, A, (ctypes.c_int32 * 4)(*sections), rope.cyclic, rope.adjacent))
+
+
+def _paged_args(fn, cache, Hkv, d):
+    """moe_paged of a cache with heads of the sizes that the call's other tensors have."""
+    k, v, table = cache
+    if k.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"{fn}: k_pages {tuple(k.shape)} and table {tuple(table.shape)}: "
+                         "[n_pages, page, Hkv, d] and [B, width] are wanted")
+    n, page = k.shape[:2]
+    shape, bf = (n, page, Hkv, d), torch.bfloat16
+    for name, t in (("k_pages", k), ("v_pages", v)):
+        if t.dtype != bf or t.shape != shape or not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, "
+                             f"{bf} {tuple(shape)} on the GPU is wanted")
+    st, sv = k.stride(), v.stride()
+    if any(a != b and e > 1 for e, a, b in zip(shape, st, sv)) or st[3] != 1:
+        raise ValueError(f"{fn}: k_pages and v_pages have different strides or scattered elements")
+    B, width = table.shape
+    pt = _want(fn, "table", table, torch.int32, (B, width), rows=True)
+    _here(fn, ("k_pages", k), ("v_pages", v), ("table", table))
+    return _PagedArgs(k.data_ptr(), v.data_ptr(), *st[:3], pt, _ld(table), n, page, width, B, Hkv, d), B
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: Rope | None = None,
+                 positions: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """moe_qk_norm_rope (include/cache.h): q bf16 [T, Hq, d] and k bf16 [T, Hkv, d] (tokens may be
+    strided), each head normed where its weight (bf16 [d]) is given and turned by positions
+    (int32 [T], or [axes, T]). Returns (q, k), new or q_out, k_out (which may be q and k themselves);
+    k may be None."""
+    if stream is not None:
+        return _on(stream, qk_norm_rope, q, k, rope, positions, q_weight, k_weight, eps, q_out, k_out)
+    fn, bf = "qk_norm_rope", torch.bfloat16
+    T, Hq, d = q.shape
+    if rope is not None and positions is None:
+        raise ValueError(f"{fn}: rope without positions")
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError(f"{fn}: k_weight or k_out without k")
+    pq, ldq = _want_heads(fn, "q", q, (T, Hq, d))
+    pk = pko = pwq = pwk = None
+    Hkv = ldk = ldko = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        pk, ldk = _want_heads(fn, "k", k, (T, Hkv, d))
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, d), dtype=bf, device=q.device)
+        pko, ldko = _want_heads(fn, "k_out", k_out, (T, Hkv, d))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=bf, device=q.device)
+    pqo, ldqo = _want_heads(fn, "q_out", q_out, (T, Hq, d))
+    if q_weight is not None:
+        pwq = _want(fn, "q_weight", q_weight, bf, (d,))
+    if k_weight is not None:
+        pwk = _want(fn, "k_weight", k_weight, bf, (d,))
+    turn = _rope_args(fn, rope, positions, T)
+    _here(fn, ("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out), ("k_out", k_out))
+    rc = lib().moe_qk_norm_rope(pq, ldq, pk, ldk, T, Hq, Hkv, d, pwq, pwk, eps, turn, pqo, ldqo, pko, ldko,
+                                _stream())
+    _check("moe_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def append_paged(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, starts: torch.Tensor,
+                 lens: torch.Tensor, rope: Rope | None = None, positions: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 rows: torch.Tensor | None = None, stream=None) -> None:
+    """moe_append_paged (include/cache.h): writes new tokens' k, v bf16 [N, Hkv, d] (tokens may be
+    strided) to the cache's pages, sequence b's (starts[b] .. starts[b + 1] - 1; starts int32 [B + 1])
+    from position lens[b] on (int32 [B], not changed). Keys are normed (k_weight bf16 [d]) and turned on
+    the way where asked, by positions (int32 [N] or [axes, N]) or, without, by their place in the cache.
+    rows int32 [N]: token t's k and v are k[rows[t]], v[rows[t]]."""
+    if stream is not None:
+        return _on(stream, append_paged, k, v, cache, starts, lens, rope, positions, k_weight, eps, rows)
+    fn, i32 = "append_paged", torch.int32
+    M, Hkv, d = k.shape
+    N = M if rows is None else rows.shape[0]
+    pk, ldk = _want_heads(fn, "k", k, (M, Hkv, d))
+    pv, ldv = _want_heads(fn, "v", v, (M, Hkv, d))
+    paged, B = _paged_args(fn, cache, Hkv, d)
+    ps = _want(fn, "starts", starts, i32, (B + 1,))
+    pl = _want(fn, "lens", lens, i32, (B,))
+    pw = None if k_weight is None else _want(fn, "k_weight", k_weight, torch.bfloat16, (d,))
+    pr = None if rows is None else _want(fn, "rows", rows, i32, (N,))
+    turn = _rope_args(fn, rope, positions, N)
+    _here(fn, ("k", k), ("v", v), ("starts", starts), ("lens", lens), ("k_weight", k_weight), ("rows", rows))
+    rc = lib().moe_append_paged(pk, ldk, pv, ldv, pr, M, N, ps, pl, ctypes.byref(paged), pw, eps, turn,
+                                _stream())
+    _check("moe_append_paged", rc)
+
+
+def tree_attention(q: torch.Tensor, cache: PagedCache, starts: torch.Tensor, lens: torch.Tensor,
+                   tree: torch.Tensor | None = None, scale: float = 0.0,
+                   out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """moe_tree_attention (include/cache.h): q bf16 [N, Hq, d] (tokens may be strided) of sequences'
+    new tokens (starts int32 [B + 1], at most 64 each), whose keys and values are in the cache already
+    from position lens[b] on. A token attends to what was there before, and to the new tokens j of its
+    sequence for which bit j of its word of tree (int64 [N]) is set; without, to those up to itself.
+    scale <= 0 means 1/sqrt(d). Returns out bf16 [N, Hq, d]; tokens of no sequence are left as they were."""
+    if stream is not None:
+        return _on(stream, tree_attention, q, cache, starts, lens, tree, scale, out, ws)
+    fn, bf, i32 = "tree_attention", torch.bfloat16, torch.int32
+    N, Hq, d = q.shape
+    Hkv = cache.k_pages.shape[2] if cache.k_pages.dim() == 4 else 0
+    pq, ldq = _want_heads(fn, "q", q, (N, Hq, d))
+    paged, B = _paged_args(fn, cache, Hkv, d)
+    ps = _want(fn, "starts", starts, i32, (B + 1,))
+    pl = _want(fn, "lens", lens, i32, (B,))
+    pt = None if tree is None else _want(fn, "tree", tree, torch.int64, (N,))
+    if out is None:
+        out = torch.empty((N, Hq, d), dtype=bf, device=q.device)
+        po = out.data_ptr()
+    else:
+        po = _want(fn, "out", out, bf, (N, Hq, d))
+    ref = ctypes.byref(paged)
+    if ws is None:
+        nbytes = lib().moe_tree_attention_workspace_bytes(N, Hq, ref)
+        if nbytes == 0:
+            raise MoeError("moe_tree_attention_workspace_bytes", -3)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    pws, nbytes = _want_ws(fn, ws)
+    _here(fn, ("q", q), ("starts", starts), ("lens", lens), ("tree", tree), ("out", out), ("ws", ws))
+    rc = lib().moe_tree_attention(pq, ldq, N, Hq, ps, pl, pt, ref, scale, po, pws, nbytes, _stream())
+    _check("moe_tree_attention", rc)
+    return out
 
 
 FWD_DETERMINISTIC = 1
