@@ -81,11 +81,11 @@ constexpr int64_t kMaxPositions = (int64_t)1 << 28;
 size_t tree_carve(moe::TreeParams& p, void* ws, int ctas) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   p.rows = std::min(moe::kTreeRows, std::min(p.N, MOE_TREE_MAX_NEW) * (p.Hq / p.Hkv));
-  const size_t states = (size_t)2 * ctas * p.rows;
+  const size_t parts = (size_t)ctas * moe::kTreeParts, states = parts * p.rows;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  const size_t begin = 256, ml = begin + up((size_t)(p.B + 1) * 8), o = ml + up(states * sizeof(float2));
+  const size_t notes = 256, ml = notes + up(parts * sizeof(moe::TreePart)), o = ml + up(states * sizeof(float2));
   p.status = reinterpret_cast<int32_t*>(at);
-  p.begin = reinterpret_cast<int64_t*>(at + begin);
+  p.parts = reinterpret_cast<moe::TreePart*>(at + notes);
   p.part_ml = reinterpret_cast<float2*>(at + ml);
   p.part_o = reinterpret_cast<float*>(at + o);
   return o + states * p.d * sizeof(float);

@@ -371,13 +371,22 @@ struct RopeParams {
   const int32_t *starts, *lens, *rows, *table;
   int64_t ld_table, page_stride, position_stride, head_stride;
   int B, n_rows, width, n_pages, page_log2;
-  int split;                 // warps a token (set by the launch)
+  // set by the launch
+  float inv_d;
+  int split;                 // warps a token
+  int tokens, token_blocks;  // a block's tokens; or blocks a token
 };
 cudaError_t rope_launch(const RopeParams& p, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- attention of new tokens over a paged cache
 constexpr int kTreeMaxSms = 160;  // bounds the partial states
 constexpr int kTreeRows = 128;    // query rows a tile
+constexpr int kTreeParts = 3;     // items of which a CTA can have a part
+// A part's note: whose it is. what: KV head << 16 | row tile << 12 | (rows - 1) << 4 | whether it is the item's first.
+struct alignas(16) TreePart {
+  int64_t item;              // a number that no other item has; -1: no part
+  int32_t tok0, what;
+};
 struct TreeParams {
   const uint16_t* q;         // tokens ldq apart
   int64_t ldq;
@@ -389,9 +398,9 @@ struct TreeParams {
   float scale_log2;          // scale * log2 e
   int ctas, rows;            // blocks; rows of a partial state
   int32_t* status;
-  int64_t* begin;            // [B + 1] scratch: a sequence's first tile of all
-  float2* part_ml;           // [2 ctas][rows]: reference (log2), sum
-  float* part_o;             // [2 ctas][rows][d]
+  TreePart* parts;           // [ctas][kTreeParts] scratch
+  float2* part_ml;           // [ctas][kTreeParts][rows]: reference (log2), sum
+  float* part_o;             // [ctas][kTreeParts][rows][d]
   uint16_t* out;             // [N][Hq][d]
 };
 cudaError_t tree_launch(const TreeParams& p, cudaStream_t s);

@@ -13,11 +13,17 @@
 // tile) items, one behind another, go in equal runs to one persistent CTA an SM. Lengths
 // are known on the device only, so every CTA sums the sequences' tiles and finds its own
 // run. What a CTA has of an item is a segment. A whole item's output is written at once;
-// a part's state (m, l, o) goes to the workspace (at most two a CTA: of the item that its
-// run begins in and of the one that it ends in) and a second kernel merges the parts.
+// a part's state (m, l, o) goes to the workspace with a note of whose it is, and a second
+// kernel merges the parts.
+//
+// Row tiles of one KV head read the same keys. Where there are several, long items are cut into
+// chunks of about a run, and a chunk's row tiles stand next to one another: the CTAs that have
+// them go over the same keys at the same time, and HBM is read once. (4 sequences of 64
+// tokens over up to 50001 positions, 4 row tiles: 188 us with an item's tiles in one piece.)
 //
 // A segment: S = Q K^T into tensor memory, weights P = 2^(scale S - m) over the scores as
-// two bf16 parts, O += P V with P as the MMA's A operand from tensor memory. One thread
+// two bf16 parts (of 32 keys each, one behind the other, where their scores were), O += P V
+// with P as the MMA's A operand from tensor memory. One thread
 // issues the scores' products, another the outputs', three tiles behind at most. K and V
 // tiles come by TMA, a box a page (or a tile, where pages are longer), through one ring of
 // slots in the order K0 K1 V0 K2 V1 ... that runs on through the segments, so that the next
@@ -92,29 +98,32 @@ MOE_DEVINL int64_t tiles_of(const TreeParams& p, const Sequence& s) {
   return s.bad || s.n == 0 ? 0 : (int64_t)p.Hkv * row_tiles(p, s) * key_tiles<KT>(s);
 }
 
-// CTA `cta`'s run begins here. With fewer tiles than CTAs the first `tiles` have one each,
-// so that no CTA between two that hold parts of an item is without one.
+// CTA `cta`'s run begins here. With fewer tiles than CTAs the first `tiles` have one each.
 MOE_DEVINL int64_t run_begin(int64_t tiles, int cta, int ctas) {
   return tiles <= ctas ? min((int64_t)cta, tiles) : tiles * cta / ctas;
 }
 
-// A CTA's run of tiles, segment by segment.
+// A CTA's run of tiles, segment by segment. A sequence's tiles in order: KV head, chunk of
+// keys, row tile, key.
 template <int KT>
 struct Walk {
   int64_t cur, end, base, count;  // of all tiles: the next, the run's end, this sequence's first; how many it has
-  int b;
+  int b, run;                     // (run: tiles of the longest one)
   Sequence s;
-  int kt, rt;
-  // the segment
+  int kt, rt, chunks;
+  // the segment: keys k0 .. k1 - 1 (in tiles) of row tile row0 / 128
   int h, row0, rows, k0, k1;
-  MOE_DEVINL void start(const TreeParams& p, int64_t cur_, int64_t end_, int b_, int64_t base_) {
-    cur = cur_, end = end_, b = b_, base = base_;
+  MOE_DEVINL void start(const TreeParams& p, const int64_t* found) {
+    cur = found[0], end = found[1], b = (int)found[2], base = found[3], run = (int)found[4];
     if (cur < end) load(p);
   }
   MOE_DEVINL void load(const TreeParams& p) {
     s = sequence_of(p, b);
     kt = key_tiles<KT>(s), rt = row_tiles(p, s), count = tiles_of<KT>(p, s);
+    // chunks of 3/4 to 3/2 of a run
+    chunks = rt > 1 ? max(1, (int)((2 * (int64_t)kt + run) / (2 * (int64_t)run))) : 1;
   }
+  MOE_DEVINL int bound(int chunk) const { return chunks == 1 ? (chunk ? kt : 0) : (int)((int64_t)kt * chunk / chunks); }
   MOE_DEVINL bool next(const TreeParams& p) {
     if (cur >= end) return false;
     while (cur >= base + count) {
@@ -123,18 +132,28 @@ struct Walk {
       ++b;
       load(p);
     }
-    const int64_t off = cur - base;
-    const int64_t item = off / kt;
-    k0 = (int)(off - item * kt);
-    k1 = (int)min((int64_t)kt, k0 + (end - cur));
+    const int64_t head = (int64_t)kt * rt, off = cur - base;
+    h = (int)(off / head);
+    const int64_t in = off - h * head;
+    int chunk = 0;
+    if (chunks > 1) {
+      chunk = (int)(in / rt * chunks / kt);
+      while (chunk + 1 < chunks && (int64_t)bound(chunk + 1) * rt <= in) ++chunk;
+      while (chunk > 0 && (int64_t)bound(chunk) * rt > in) --chunk;
+    }
+    const int from = bound(chunk), to = bound(chunk + 1);
+    const int64_t at = in - (int64_t)from * rt;
+    const int row = (int)(at / (to - from));
+    k0 = from + (int)(at - (int64_t)row * (to - from));
+    k1 = (int)min((int64_t)to, k0 + (end - cur));
     cur += k1 - k0;
-    h = (int)(item / rt);
-    row0 = (int)(item % rt) * kTreeRows;
+    row0 = row * kTreeRows;
     rows = min(kTreeRows, s.n * (p.Hq / p.Hkv) - row0);
     return true;
   }
-  // Where a part's state goes: slot 0 of the CTA for the item that its run begins in.
   MOE_DEVINL bool whole() const { return k0 == 0 && k1 == kt; }
+  // The segment's item, as no other's.
+  MOE_DEVINL int64_t item() const { return base + ((int64_t)h * rt + row0 / kTreeRows) * kt; }
 };
 
 // Which of the 32 positions from the rel-th new token on (rel < 0: cached ones before) a
@@ -162,8 +181,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   uint64_t* p_full = s_full + NB;                                   // [NB] weights are written, over the scores
   uint64_t* pv_done = p_full + NB;                                  // [NB] their product is complete: the columns are free
   uint64_t* drain = pv_done + NB;                                   // [1]
-  int64_t* found = reinterpret_cast<int64_t*>(drain + 1);           // the run: first tile, end, sequence, its first tile
-  int64_t* sums = found + 4;                                        // [8] a warp's tiles
+  int64_t* found = reinterpret_cast<int64_t*>(drain + 1);           // the run: first tile, end, sequence, its first tile, the longest's tiles
+  int64_t* sums = found + 5;                                        // [8] a warp's tiles
   int* bad_tile = reinterpret_cast<int*>(sums + 8);                 // [kBadRing] 1 + tile of the run with a bad page
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad_tile + kBadRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -185,7 +204,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     }
     mbar_init(drain, 2);
     for (int i = 0; i < kBadRing; ++i) bad_tile[i] = 0;
-    found[0] = found[1] = found[2] = found[3] = 0;
+    found[0] = found[1] = 0;
     *abort_flag = 0;
     *v_bad = 0;
     fence_mbar_init();
@@ -206,49 +225,71 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 
   // The run: the sum of all sequences' tiles, then where its share of it begins.
   {
-    int64_t total = 0;
-    for (int round = 0; round < 2; ++round) {
-      int64_t before = 0;
-      const int64_t from = run_begin(total, blockIdx.x, p.ctas), to = run_begin(total, blockIdx.x + 1, p.ctas);
-      if (round == 1 && from == to) break;
-      for (int b0 = 0; b0 < p.B; b0 += kTrThreads) {
-        const int b = b0 + threadIdx.x;
-        const int64_t mine = b < p.B ? tiles_of<KT>(p, sequence_of(p, b)) : 0;
-        int64_t upto = mine;  // of the warp's lanes up to this one
-#pragma unroll
-        for (int off = 1; off < 32; off *= 2) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-          if (lane >= off) upto += v;
-        }
-        if (lane == 31) sums[warp] = upto;
-        __syncthreads();
-        int64_t first = before + upto - mine;
-        for (int w = 0; w < kTrThreads / 32; ++w) {
-          if (w < warp) first += sums[w];
-          before += sums[w];
-        }
-        if (round == 0) {
-          if (blockIdx.x == 0 && b < p.B) p.begin[b] = first;
-        } else if (first <= from && from < first + mine) {
-          found[0] = from, found[1] = to, found[2] = b, found[3] = first;
-        }
-        __syncthreads();
+    int64_t total = 0, first = 0, mine = 0;  // of all; before this thread's last sequence; that one's
+    int bad = 0;
+    auto add = [&](int b0) {  // of the sequences b0 .. b0 + 255
+      const int b = b0 + threadIdx.x;
+      mine = 0;
+      if (b < p.B) {
+        const Sequence s = sequence_of(p, b);
+        mine = tiles_of<KT>(p, s);
+        bad |= s.bad;
       }
-      if (round == 0) {
-        total = before;
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.begin[p.B] = total;
+      int64_t upto = mine;  // of the warp's lanes up to this one
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      first = total + upto - mine;
+#pragma unroll
+      for (int w = 0; w < kTrThreads / 32; ++w) {
+        if (w < warp) first += sums[w];
+        total += sums[w];
+      }
+      if (p.B > kTrThreads) __syncthreads();
+    };
+    for (int b0 = 0; b0 < p.B; b0 += kTrThreads) add(b0);
+    const int64_t all = total, from = run_begin(all, blockIdx.x, p.ctas), to = run_begin(all, blockIdx.x + 1, p.ctas);
+    auto note = [&](int b) {
+      if (first <= from && from < first + mine) {
+        found[0] = from, found[1] = to, found[2] = b, found[3] = first;
+        found[4] = (all + p.ctas - 1) / p.ctas;
+      }
+    };
+    if (p.B <= kTrThreads) {
+      if (from < to) note(threadIdx.x);
+    } else if (from < to) {
+      total = 0;
+      for (int b0 = 0; b0 < p.B; b0 += kTrThreads) {
+        add(b0);
+        note(b0 + threadIdx.x);
+      }
+    }
+    if (__syncthreads_or(bad)) {  // sequences that cannot be right: NaN, by all CTAs
+      for (int b = 0; b < p.B; ++b) {
+        const Sequence s = sequence_of(p, b);
+        if (!s.bad) continue;
+        const int64_t words = (int64_t)s.n * p.Hq * (D / 8);
+        uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)s.tok0 * p.Hq * D);
+        for (int64_t i = (int64_t)blockIdx.x * kTrThreads + threadIdx.x; i < words; i += (int64_t)p.ctas * kTrThreads)
+          out[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
       }
     }
   }
   Walk<KT> walk;
-  walk.start(p, found[0], found[1], (int)found[2], found[3]);
+  walk.start(p, found);
   const int total = (int)(found[1] - found[0]);  // tiles of the run
+  TreePart* const parts = p.parts + (int64_t)blockIdx.x * kTreeParts;
 
-  if (total == 0) {
-    // (nothing to do: fewer tiles than CTAs)
+  if (total == 0) {  // fewer tiles than CTAs
+    if (threadIdx.x < kTreeParts) parts[threadIdx.x].item = -1;
   } else if (warp == 0) {
     fence_proxy_async_global();  // the pages are written by ordinary stores of earlier launches
-    const uint64_t policy = l2_policy_evict_first();
+    // keys that one CTA alone reads leave L2 first
+    const uint64_t policy = p.rows < kTreeRows ? l2_policy_evict_first() : l2_policy_evict_normal();
     const int pieces_log2 = (KT == 64 ? 6 : 7) - args.box_log2, pieces = 1 << pieces_log2;
     // a lane's box of each tile: 64 columns, one page's (or the tile's) positions
     const int piece = lane & (pieces - 1), col = lane >> pieces_log2;
@@ -358,7 +399,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             for (int kk = 0; kk < KT / 16; ++kk)
 #pragma unroll
               for (int part = 0; part < 2; ++part)
-                tc_mma_ts(tmem, tmem + C::kColS + buf * KT + part * (KT / 2) + kk * 8, v_desc + ((kk * 2048) >> 4), idesc_o,
+                tc_mma_ts(tmem, tmem + C::kColS + buf * KT + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, v_desc + ((kk * 2048) >> 4), idesc_o,
                           ((key - walk.k0) | kk | part) != 0);
             tc_commit(&empty[slot]);
             tc_commit(&pv_done[buf]);
@@ -374,72 +415,78 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const int quarter = warp & 3, r = quarter * 32 + lane, tid = threadIdx.x - 128;  // r: this thread's row of the tile
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     bool alive = true;
-    int buf = 0, turn = 0, last = 0, last_turn = 0, it = 0, seg = 0, tails = 0;  // of this tile and of the one before
-    for (; walk.next(p); ++seg) {
-      const int row0 = walk.row0, rows = walk.rows, L = walk.s.L, n = walk.s.n;
-      auto query_row = [&](int row, int& token) {  // of the call's
-        const int i = (row0 + row) / G;
-        token = walk.s.tok0 + i;
-        return walk.h * G + (row0 + row) - i * G;
-      };
-      int token;
+    int buf = 0, turn = 0, last = 0, last_turn = 0, it = 0, seg = 0, tails = 0, n_parts = 0;  // of this tile and of the one before
+    const uint32_t per_group = (65535 + G) / G;  // x / G = x per_group >> 16 for x < 4096
+    // The queries of the segment at hand into the swizzled K-major operand, as zeros past the end up to
+    // whole warps (which choose together when to rescale: what another call left there may not decide
+    // that; warps without rows hold what was there).
+    auto fetch_queries = [&]() {
+      constexpr int kChunks = D / 8;
+      const uint16_t* q = p.q + walk.s.tok0 * p.ldq + (int64_t)walk.h * G * D;
+#pragma unroll 4
+      for (int j = tid; j < (walk.rows + 31) / 32 * 32 * kChunks; j += 128) {
+        const int row = j / kChunks, c = j % kChunks;
+        const bool in = row < walk.rows;
+        const int x = walk.row0 + (in ? row : 0), i = (int)(x * per_group >> 16);
+        cp_async_16(smem_u32(smem + (c / 8) * (kTreeRows * 128) + sw128_offset(row, c % 8)),
+                    q + i * p.ldq + (x - i * G) * D + c * 8, in ? 16u : 0u);
+      }
+      cp_async_commit();
+    };
+    auto queries_ready = [&]() {
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      warp_arrive(q_full);
+    };
+    bool more = walk.next(p);
+    if (more) {
+      fetch_queries();
+      queries_ready();
+    }
+    for (; more; ++seg) {
+      const Walk<KT> now = walk;
+      const int rows = now.rows, L = now.s.L, n = now.s.n;
       const bool mine = r < rows, warp_rows = quarter * 32 < rows;
-      const int head = query_row(mine ? r : 0, token);
-      const int i_new = token - walk.s.tok0;
-      uint64_t bits = (2ull << i_new) - 1;
+      const int x = now.row0 + (mine ? r : 0), i_new = (int)(x * per_group >> 16);
+      const int token = now.s.tok0 + i_new, head = now.h * G + x - i_new * G;
+      uint64_t bits = p.tree ? (uint64_t)p.tree[token] : (2ull << i_new) - 1;
+      if (n < 64) bits &= (1ull << n) - 1;
       float m = -INFINITY, l = 0.f;
       bool poison = false;
-      if (alive) {
-        // The queries into the swizzled K-major operand, as zeros past the end up to whole warps (which
-        // choose together when to rescale: what another call left there may not decide that; warps without rows hold
-        // what was there). (The products that read the queries before are complete: their scores were.)
-        constexpr int kChunks = D / 8;
-        for (int j = tid; j < (rows + 31) / 32 * 32 * kChunks; j += 128) {
-          const int row = j / kChunks, c = j % kChunks;
-          const bool in = row < rows;
-          int t;
-          const int qh = query_row(in ? row : 0, t);
-          cp_async_16(smem_u32(smem + (c / 8) * (kTreeRows * 128) + sw128_offset(row, c % 8)),
-                      p.q + t * p.ldq + (int64_t)qh * D + c * 8, in ? 16u : 0u);
-        }
-        cp_async_commit();
-        if (p.tree) bits = (uint64_t)p.tree[token];
-        if (n < 64) bits &= (1ull << n) - 1;
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        warp_arrive(q_full);
-      }
-      for (int key = walk.k0; key < walk.k1 && alive; ++key, ++it) {
+      for (int key = now.k0; key < now.k1 && alive; ++key, ++it) {
         if (!(alive = warp_wait(&s_full[buf], turn, abort_flag, p.status, 108))) break;
         tc_fence_after();
         if (bad_tile[it % kBadRing] == it + 1) poison = true;
         const int64_t rel = (int64_t)key * KT - L;  // of the tile's first position to the first new token
         const bool tail = rel + KT > 0;
         if (warp_rows) {
-          uint32_t s[KT / 32][32];
-#pragma unroll
-          for (int c = 0; c < KT / 32; ++c) tmem_ld_32x32b_x32(tmem + lanes + C::kColS + buf * KT + c * 32, s[c]);
-          tc_wait_ld();
-          if (tail) {
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-              const uint32_t in = attended(rel + c * 32, bits);
+          // Twice over the scores in tensor memory, in pieces: the largest, then the weights, over
+          // the scores of their piece. (All of a tile's scores in registers are one long piece of code,
+          // which a call of few tiles spends its time fetching.)
+          const uint32_t cols = tmem + lanes + C::kColS + buf * KT;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 32) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(cols + c, s);
+            tc_wait_ld();
+            if (tail) {
+              const uint32_t in = attended(rel + c, bits);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!(in >> j & 1)) s[c][j] = 0xFF800000u;
+                if (!(in >> j & 1)) s[j] = 0xFF800000u;
+              tmem_st_32x32b_x32(cols + c, s);
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < KT / 32; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[c][j]));
+          if (tail) tc_wait_st();
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
             const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.f : ex2(m - nm);  // (m -infinity: 0)
             l *= f;
             m = nm;
-            if (key > walk.k0) {
+            if (key > now.k0) {
               // O is whole once the product before is complete
               if (!(alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 109))) break;
               tc_fence_after();
@@ -455,31 +502,30 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float2 sc = make_float2(p.scale_log2, p.scale_log2);
-          const float2 nr = make_float2(-ref, -ref);
-          if (__any_sync(0xffffffffu, fabsf(ref) >= 65536.f)) {
-            // what the fused product leaves of a large reference's rounding would pass 2^-8: scale apart, rounded
-            // as the reference was
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[c][j] = __float_as_uint(__fmul_rn(__uint_as_float(s[c][j]), p.scale_log2));
-            sc = make_float2(1.f, 1.f);
-          }
+          // What the fused product leaves of a large reference's rounding would pass 2^-8: then scale apart,
+          // rounded as the reference was.
+          const bool apart = __any_sync(0xffffffffu, fabsf(ref) >= 65536.f);
+          const float sc1 = apart ? 1.f : p.scale_log2;
+          const float2 sc = make_float2(sc1, sc1), nr = make_float2(-ref, -ref);
           float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 32) {
+            uint32_t s[32], hi[16], lo[16];
+            tmem_ld_32x32b_x32(cols + c, s);
+            tc_wait_ld();
+            if (apart) {
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
-            uint32_t hi[16], lo[16];
+              for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__fmul_rn(__uint_as_float(s[j]), p.scale_log2));
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), sc, nr);
-              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sc, nr);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
               sum = __fadd2_rn(sum, e);
               split_bf16(e.x, e.y, hi[j], lo[j]);
             }
-            const uint32_t dst = tmem + lanes + C::kColS + buf * KT + c * 16;
-            tmem_st_32x32b_x16(dst, hi);
-            tmem_st_32x32b_x16(dst + KT / 2, lo);
+            tmem_st_32x32b_x16(cols + c, hi);
+            tmem_st_32x32b_x16(cols + c + 16, lo);
           }
           l += sum.x + sum.y;
           tc_wait_st();
@@ -519,10 +565,20 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         last = buf, last_turn = turn;
         if (++buf == NB) buf = 0, turn ^= 1;
       }
+      // The next segment's queries: the products that read these are complete (their scores were), and
+      // the next scores' run while this segment's outputs are read.
+      more = walk.next(p);
+      if (alive && more) fetch_queries();
       // the segment's outputs: every product is complete with the last one
       if (alive) alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 110);
-      const bool whole = walk.whole();
-      const int64_t state = ((int64_t)blockIdx.x * 2 + (seg > 0)) * p.rows + r;
+      if (alive && more) queries_ready();
+      const bool whole = now.whole();
+      int part = 0;
+      if (!whole) {
+        part = min(n_parts++, kTreeParts - 1);  // (never more: a chunk has 3/4 of a run at least)
+        if (tid == 0) parts[part] = TreePart{now.item(), now.s.tok0, now.h << 16 | now.row0 / kTreeRows << 12 | (rows - 1) << 4 | (now.k0 == 0)};
+      }
+      const int64_t state = ((int64_t)blockIdx.x * kTreeParts + part) * p.rows + r;
       if (l != l && m == -INFINITY) m = 0.f;  // nothing but NaN: not a state without positions
       if (!alive || poison) {  // after a wait that ran out, or a bad page: NaN
         m = 0.f;
@@ -548,13 +604,13 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             for (int j = 0; j < 32; ++j) o[j] = 0u;
           }
           if (odd && mine && !poison) {
-            const int64_t from = max((int64_t)walk.k0 * KT, (int64_t)L), to = min((int64_t)walk.k1 * KT, (int64_t)L + n);
+            const int64_t from = max((int64_t)now.k0 * KT, (int64_t)L), to = min((int64_t)now.k1 * KT, (int64_t)L + n);
 #pragma unroll 1
             for (int64_t at = from; at < to; ++at) {
               if (!(bits >> (at - L) & 1)) continue;
-              const int64_t id = p.table[walk.b * p.ld_table + (at >> p.page_log2)];
+              const int64_t id = p.table[now.b * p.ld_table + (at >> p.page_log2)];
               const uint16_t* v = p.v_pages + id * p.page_stride + (at & ((1 << p.page_log2) - 1)) * p.position_stride +
-                                  walk.h * p.head_stride + c;
+                                  now.h * p.head_stride + c;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float x = bf16_bits_to_f32(v[j]);
@@ -584,6 +640,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       }
       tc_fence_before();
     }
+    cp_async_wait<0>();  // (after a wait that ran out: queries on their way)
+    if (tid == 0)
+      for (int i = n_parts; i < kTreeParts; ++i) parts[i].item = -1;
   }
   __syncwarp();  // the single-lane roles join their warps
   tc_fence_before();
@@ -592,94 +651,141 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// One query row a block: merges its item's parts, those of the CTAs whose runs hold its
-// tiles. (An item of one CTA alone has its output already.)
+// Merges items' parts. Every block reads all notes; eight rows of an item at a time, a warp a
+// row. (Grids over all rows would mostly find nothing to do: 60 sequences of 59 tokens, 48000
+// rows in 480 items that no run cuts, 206 us instead of 33.)
+constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
-  constexpr int KT = TrCfg<D>::KT, kCols = D / 4, kGroups = 256 / kCols;
-  __shared__ float4 acc_s[kGroups][kCols];
-  __shared__ float w_s[kTreeMaxSms], red[2][8];
-  __shared__ int seq_s;
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeParams p) {
+  constexpr int kC = D < 128 ? 1 : D / 128;  // float4 a lane (D = 64: half the lanes)
+  constexpr int kAll = kTreeMaxSms * kTreeParts, kThreads = 32 * kMergeWarps, kPer = (kAll + kThreads - 1) / kThreads;
+  __shared__ int list[kAll];
+  __shared__ float weight[kMergeWarps][kAll];
+  __shared__ int counts[kMergeWarps];
+  __shared__ TreePart chosen;
+  __shared__ int chosen_unit;  // of the item
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  const int tid = threadIdx.x;
-  const int token = blockIdx.x / p.Hq, head = blockIdx.x % p.Hq, G = p.Hq / p.Hkv;
-  // the token's sequence: the last that begins at it or before (none: as it was)
-  if (tid == 0) seq_s = -1;
-  __syncthreads();
-  for (int b = tid; b < p.B; b += 256) {
-    if (p.starts[b] <= token && token < p.starts[b + 1]) seq_s = b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, all = p.ctas * kTreeParts;
+  // this thread's notes, and the units of all
+  TreePart mine[kPer];
+  int units = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    mine[k].item = -1;
+    if (tid * kPer + k < all) mine[k] = p.parts[tid * kPer + k];
   }
-  __syncthreads();
-  const int b = seq_s;
-  if (b < 0) return;
-  const Sequence s = sequence_of(p, b);
-  const int c = tid % kCols, grp = tid / kCols;
-  uint16_t* out = p.out + (int64_t)blockIdx.x * D + c * 4;
-  if (s.bad) {
-    if (grp == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
-    return;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (mine[k].item >= 0 && (mine[k].what & 1)) units += ((mine[k].what >> 4 & 255) + kMergeWarps) / kMergeWarps;
+  int upto = units;
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += v;
   }
-  const int row = (token - s.tok0) * G + head % G, kt = key_tiles<KT>(s), rt = row_tiles(p, s);
-  const int64_t total = p.begin[p.B];
-  const int64_t t0 = p.begin[b] + ((int64_t)(head / G) * rt + row / kTreeRows) * kt, t1 = t0 + kt;  // the item's tiles
-  // the CTAs that hold t0 and t1 - 1: the last whose run begins at it or before
-  auto cta_of = [&](int64_t t) {
-    int i = total <= p.ctas ? (int)t : (int)(t * p.ctas / total);
-    while (i + 1 < p.ctas && run_begin(total, i + 1, p.ctas) <= t) ++i;
-    while (i > 0 && run_begin(total, i, p.ctas) > t) --i;
-    return i;
-  };
-  const int c0 = cta_of(t0), n = cta_of(t1 - 1) - c0 + 1;
-  if (n == 1) return;
-  // slot 0 of a CTA is the part of the item that its run begins in
-  auto state_of = [&](int i) {
-    const int cta = c0 + i, slot = run_begin(total, cta, p.ctas) >= t0 ? 0 : 1;
-    return ((int64_t)cta * 2 + slot) * p.rows + row % kTreeRows;
-  };
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < n) ml = p.part_ml[state_of(tid)];
-  float M = ml.x;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  if (lane == 31) counts[warp] = upto;
   __syncthreads();
+  int n_units = 0, before = upto - units;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w]);
-  const float f0 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-  if (tid < n) w_s[tid] = f0;
-  float sum = f0 * ml.y;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if ((tid & 31) == 0) red[1][tid >> 5] = sum;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) L += red[1][w];
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp; i < n; i += kGroups) {
-    const float f = w_s[i];
-    if (f == 0.f) continue;
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + state_of(i) * D + c * 4);
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (w < warp) before += counts[w];
+    n_units += counts[w];
   }
-  acc_s[grp][c] = acc;
-  __syncthreads();
-  if (grp == 0) {
+  const int G = p.Hq / p.Hkv;
+  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
+    __syncthreads();  // (the unit before is done with what is shared)
+    if (before <= unit && unit < before + units) {
+      int u = before;
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 v = acc_s[k][c];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+      for (int k = 0; k < kPer; ++k) {
+        if (mine[k].item < 0 || !(mine[k].what & 1)) continue;
+        const int n = ((mine[k].what >> 4 & 255) + kMergeWarps) / kMergeWarps;
+        if (u <= unit && unit < u + n) {
+          chosen = mine[k];
+          chosen_unit = unit - u;
+        }
+        u += n;
+      }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing attended to: zeros
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    __syncthreads();
+    const TreePart first = chosen;
+    const int rows = (first.what >> 4 & 255) + 1, r = chosen_unit * kMergeWarps + warp;
+    // the item's parts, in the order of their places
+    int is = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) is += mine[k].item == first.item;
+    int at = is;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += v;
+    }
+    if (lane == 31) counts[warp] = at;
+    __syncthreads();
+    int n = 0;
+    at -= is;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      if (w < warp) at += counts[w];
+      n += counts[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (mine[k].item == first.item) list[at++] = tid * kPer + k;
+    __syncthreads();
+    if (r >= rows) continue;
+    float M = -INFINITY, sum = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = p.part_ml[(int64_t)list[i] * p.rows + r];
+      M = fmaxf(M, ml.x);
+      weight[warp][i] = ml.x;
+      sum = i == lane ? ml.y : sum;  // (the lane's first; others are read again)
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float mass = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float x = weight[warp][i], f = x == -INFINITY ? 0.f : ex2(x - M);
+      weight[warp][i] = f;
+      mass = fmaf(f, i == lane ? sum : p.part_ml[(int64_t)list[i] * p.rows + r].y, mass);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, off);
+    __syncwarp();
+    float4 acc[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane * 4 < D) {
+      const float* o = p.part_o + (int64_t)r * D + lane * 4;
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 v[8][kC];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // (a part in which the row attends to nothing has zeros)
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            v[i][c] = *reinterpret_cast<const float4*>(o + (int64_t)list[min(i0 + i, n - 1)] * p.rows * D + c * 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i0 + i >= n) break;
+          const float f = weight[warp][i0 + i];
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            acc[c].x = fmaf(f, v[i][c].x, acc[c].x);
+            acc[c].y = fmaf(f, v[i][c].y, acc[c].y);
+            acc[c].z = fmaf(f, v[i][c].z, acc[c].z);
+            acc[c].w = fmaf(f, v[i][c].w, acc[c].w);
+          }
+        }
+      }
+      const float inv = mass == 0.f ? 0.f : 1.f / mass;  // nothing attended to: zeros
+      const int x = (first.what >> 12 & 15) * kTreeRows + r;
+      uint16_t* out = p.out + ((int64_t)(first.tok0 + x / G) * p.Hq + (first.what >> 16) * G + x % G) * D + lane * 4;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        *reinterpret_cast<uint2*>(out + c * 128) =
+            make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
+    }
   }
 }
 
@@ -722,8 +828,8 @@ cudaError_t tree_launch_t(const TreeParams& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (const cudaError_t err = cudaLaunchKernelEx(&cfg, tree_kernel<D>, args); err != cudaSuccess) return err;
-  cfg.gridDim = dim3((unsigned)((int64_t)p.N * p.Hq));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)std::min(4 * p.ctas, p.ctas * ((p.rows + kMergeWarps - 1) / kMergeWarps)));
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
 }

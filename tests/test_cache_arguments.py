@@ -111,7 +111,7 @@ def test_attention(L):
         c = dict(d=d, hs=d, os=2 * d, ps=32 * d)
         assert tree(L, c=cache(**c), ldq=16 * d) == 0
         (k, grid, *_), (m, merge, *_) = F.launches(L)
-        assert k == f"tree_kernel<{d}>" and m == f"tree_merge_kernel<{d}>" and grid[0] == 152 and merge[0] == 160
+        assert k == f"tree_kernel<{d}>" and m == f"tree_merge_kernel<{d}>" and grid[0] == 152 and merge[0] == 608
         need = L.moe_tree_attention_workspace_bytes(10, 16, cache(**c))
         assert need >= 2 * 152 * 80 * (d + 2) * 4 and tree(L, c=cache(**c), ldq=16 * d, n=need - 1) == WS
         for order in (dict(os=d, hs=16 * d, ps=32 * d), dict(os=4 * d, hs=d, ps=64 * d)):

@@ -177,47 +177,89 @@ def begin(total, cta, ctas):
     return min(cta, total) if total <= ctas else total * cta // ctas
 
 
-def segments_of(items, cta, ctas):
-    """[(item, k0, k1)] of a CTA's run; items: tiles of each."""
-    total = sum(items)
-    at, end, out, base = begin(total, cta, ctas), begin(total, cta + 1, ctas), [], 0
-    for i, n in enumerate(items):
-        if at < end and at < base + n:
-            k0, k1 = at - base, min(n, at - base + end - at)
-            out.append((i, k0, k1))
+class Seq:
+    """A sequence's tiles as the kernel numbers them: KV head, chunk of keys, row tile, key."""
+
+    def __init__(self, heads, kt, rt, run):
+        self.heads, self.kt, self.rt = heads, kt, rt
+        self.chunks = max(1, (2 * kt + run) // (2 * run)) if rt > 1 else 1
+        self.count = heads * kt * rt
+
+    def bound(self, chunk):
+        return self.kt * chunk // self.chunks
+
+    def segment(self, off, left):
+        """(head, row tile, k0, k1) of the segment at a tile, at most `left` tiles long."""
+        h, at = divmod(off, self.kt * self.rt)
+        chunk = at // self.rt * self.chunks // self.kt
+        while chunk + 1 < self.chunks and self.bound(chunk + 1) * self.rt <= at:
+            chunk += 1
+        while chunk > 0 and self.bound(chunk) * self.rt > at:
+            chunk -= 1
+        lo, hi = self.bound(chunk), self.bound(chunk + 1)
+        row, k = divmod(at - lo * self.rt, hi - lo)
+        assert 0 <= row < self.rt
+        return h, row, lo + k, min(hi, lo + k + left)
+
+
+def cut(sizes, ctas):
+    """Every CTA's segments [(sequence, head, row tile, k0, k1)], and the sequences."""
+    total = sum(h * kt * rt for h, kt, rt in sizes)
+    run = max(1, -(-total // ctas))
+    seqs, out = [Seq(*s, run) for s in sizes], []
+    b, base = 0, 0
+    for cta in range(ctas):
+        at, end, mine = begin(total, cta, ctas), begin(total, cta + 1, ctas), []
+        while at < end:
+            while at >= base + seqs[b].count:
+                base += seqs[b].count
+                b += 1
+            h, row, k0, k1 = seqs[b].segment(at - base, end - at)
+            mine.append((b, h, row, k0, k1))
             at += k1 - k0
-        base += n
-    return out
+        out.append(mine)
+    return out, seqs
 
 
-@pytest.mark.parametrize("seed", range(30))
-def test_parts_are_where_the_merge_looks(seed):
+PARTS = 3
+
+
+@pytest.mark.parametrize("seed", range(80))
+def test_every_tile_once_and_few_parts(seed):
+    """Every item's keys are covered once, in order; no CTA has more parts than it has places for."""
     rng = random.Random(seed)
     ctas = rng.choice([1, 2, 7, 152, 160])
-    items = [rng.choice([1, 2, 3, 17, 500]) for _ in range(rng.choice([1, 2, 5, 40, 400]))]
-    total, states, wholes = sum(items), {}, set()
-    for cta in range(ctas):
-        for seg, (i, k0, k1) in enumerate(segments_of(items, cta, ctas)):
-            if (k0, k1) == (0, items[i]):
-                wholes.add(i)
-                continue
-            slot = (cta, int(seg > 0))
-            assert slot not in states
-            states[slot] = (i, k0, k1)
-    t0 = 0
-    for i, n in enumerate(items):
-        def cta_of(t):
-            c = t if total <= ctas else t * ctas // total
-            while c + 1 < ctas and begin(total, c + 1, ctas) <= t:
-                c += 1
-            while c > 0 and begin(total, c, ctas) > t:
-                c -= 1
-            return c
-        first, last = cta_of(t0), cta_of(t0 + n - 1)
-        if first == last:
-            assert i in wholes
-        else:
-            got = [states[c, 0 if begin(total, c, ctas) >= t0 else 1] for c in range(first, last + 1)]
-            assert all(g[0] == i for g in got) and got[0][1] == 0 and got[-1][2] == n
-            assert all(a[2] == b[1] for a, b in zip(got, got[1:]))
-        t0 += n
+    most = rng.choice([1, 3, 20, 300])
+    sizes = [(rng.choice([1, 2, 8]), rng.randint(0, 1) and rng.randint(1, most), rng.choice([1, 1, 2, 3, 4, 8]))
+             for _ in range(rng.choice([1, 2, 5, 40]))]
+    runs, seqs = cut(sizes, ctas)
+    got = {}
+    for mine in runs:
+        assert sum((k0, k1) != (0, seqs[b].kt) for b, _, _, k0, k1 in mine) <= PARTS
+        for b, h, row, k0, k1 in mine:
+            got.setdefault((b, h, row), []).append((k0, k1))
+    for b, (heads, kt, rt) in enumerate(sizes):
+        for h in range(heads if kt else 0):
+            for row in range(rt):
+                parts = got.pop((b, h, row))
+                assert parts[0][0] == 0 and parts[-1][1] == kt and all(x[1] == y[0] for x, y in zip(parts, parts[1:]))
+    assert not got
+
+
+def test_row_tiles_of_a_chunk_go_over_the_same_keys_together():
+    """4 row tiles over 586 key tiles on 152 CTAs: CTAs that hold row tiles of one chunk are a few
+    keys apart at any time."""
+    runs, _ = cut([(2, 586, 4)] * 4, 152)
+    for tick in range(0, 120, 7):
+        at = {}
+        for mine in runs:
+            left = tick
+            for b, h, row, k0, k1 in mine:
+                if left < k1 - k0:
+                    at.setdefault((b, h), []).append(k0 + left)
+                    break
+                left -= k1 - k0
+        for keys in at.values():
+            keys.sort()
+            near = sum(any(j != i and abs(k - keys[j]) <= 20 for j in range(len(keys))) for i, k in enumerate(keys))
+            assert near >= 0.8 * len(keys)
