@@ -93,7 +93,8 @@ size_t tree_carve(moe::TreeParams& p, void* ws, int ctas) {
 
 bool tree_shape_supported(int N, int Hq, const moe_paged_t& c) {
   return N >= 0 && N < 1 << 24 && (c.d == 64 || c.d == 128 || c.d == 256) && Hq >= c.n_kv_heads &&
-         Hq % c.n_kv_heads == 0 && Hq / c.n_kv_heads <= 16 && (int64_t)N * Hq < (int64_t)1 << 31;
+         Hq % c.n_kv_heads == 0 && Hq / c.n_kv_heads <= 16 && (int64_t)N * Hq < (int64_t)1 << 31 &&
+         (int64_t)c.width * c.page * c.n_kv_heads < (int64_t)1 << 34;  // (a sequence's tiles in 32 bits)
 }
 
 }  // namespace

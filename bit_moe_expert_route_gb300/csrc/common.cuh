@@ -313,6 +313,18 @@ MOE_DEVINL void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// 16 lanes x 32 columns: the thread's registers 4 n + {0, 1} are lane (base + i / 4), columns col
+// + 8 n + 2 (i % 4) + {0, 1}, and 4 n + {2, 3} the same of eight lanes on.
+MOE_DEVINL void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // Shared-memory matrix descriptor (tcgen05), K-major operand in the 128-byte
 // swizzled layout: rows of 128 bytes (64 bf16 of K), 8-row atoms of 1024
 // bytes stacked along M/N (stride byte offset 1024), atoms 1024-byte aligned.

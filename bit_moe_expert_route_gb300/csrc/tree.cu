@@ -27,7 +27,12 @@
 // issues the scores' products, another the outputs', three tiles behind at most. K and V
 // tiles come by TMA, a box a page (or a tile, where pages are longer), through one ring of
 // slots in the order K0 K1 V0 K2 V1 ... that runs on through the segments, so that the next
-// segment's tiles land while this one ends.
+// segment's tiles land while this one ends. Which segments there are one thread works out
+// ahead of the others, who read it from shared memory.
+//
+// The code is kept short (waits that wait and what happens once a segment out of line, loops
+// rolled): with 130 KB of it, a call of few tiles spent most of its time fetching instructions, and
+// so did the softmax warps (64 sequences over 4096 positions 154 us).
 //
 // What rows do not attend to: scores are set to -infinity by the row's mask, whatever they
 // were. In V, a weight of 0 would still make NaN of an infinity or a NaN. Rows past the
@@ -46,7 +51,7 @@ namespace moe {
 namespace {
 
 constexpr int kTrThreads = 256;  // warp 0 TMA, warps 1 and 2 MMA, warps 4-7 softmax
-constexpr float kLazyLog2 = 8.f;
+constexpr float kMostSum = 1024.f;  // of 32 weights, from which on their reference moves
 constexpr int kBadRing = 16;     // tiles whose pages are known to be bad or not: more than the ring holds
 
 template <int D>
@@ -56,10 +61,11 @@ struct TrCfg {
   static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
   static constexpr int kQ = kTreeRows * D * 2;
   static constexpr int kBufs = 3;                   // tiles between their scores and their outputs
+  static constexpr int kSegs = 4;                   // segments that are worked out ahead
   static constexpr int kOffSlots = kQ;
   static constexpr int kOffBar = kOffSlots + kSlots * kSlot;
-  static constexpr int kBars = 2 * kSlots + 2 + 3 * kBufs + 1;
-  static constexpr int kSmem = kOffBar + 8 * kBars + 512 + 1024;
+  static constexpr int kBars = 2 * kSlots + 2 + 3 * kBufs + 1 + 2 * kSegs;
+  static constexpr int kSmem = kOffBar + (8 * kBars + 15) / 16 * 16 + 512 + 1024;
   static constexpr int kColS = D;                   // tensor memory: O, then the score buffers
   static_assert(kColS + kBufs * KT <= 512, "tensor memory exceeded");
   static_assert(kSmem <= 232448, "shared memory exceeded");
@@ -103,58 +109,124 @@ MOE_DEVINL int64_t run_begin(int64_t tiles, int cta, int ctas) {
   return tiles <= ctas ? min((int64_t)cta, tiles) : tiles * cta / ctas;
 }
 
+// What a CTA has of an item: keys k0 .. k1 - 1 (in tiles) of `rows` query rows from row0 on.
+struct alignas(16) Segment {
+  int64_t item;  // as no other's
+  int b, tok0, n, L, h, row0, rows, k0, k1, whole;
+};
+
 // A CTA's run of tiles, segment by segment. A sequence's tiles in order: KV head, chunk of
-// keys, row tile, key.
+// keys, row tile, key. (A sequence has fewer than 2^31.)
 template <int KT>
 struct Walk {
-  int64_t cur, end, base, count;  // of all tiles: the next, the run's end, this sequence's first; how many it has
-  int b, run;                     // (run: tiles of the longest one)
+  int64_t cur, end, base;  // of all tiles: the next, the run's end, this sequence's first
+  uint32_t count, run;     // this sequence's tiles; the longest run's
+  int b;
   Sequence s;
-  int kt, rt, chunks;
-  // the segment: keys k0 .. k1 - 1 (in tiles) of row tile row0 / 128
-  int h, row0, rows, k0, k1;
-  MOE_DEVINL void start(const TreeParams& p, const int64_t* found) {
-    cur = found[0], end = found[1], b = (int)found[2], base = found[3], run = (int)found[4];
-    if (cur < end) load(p);
+  uint32_t kt, rt, chunks, size, longer;  // chunks of `size` tiles, the first `longer` of them of one more
+  MOE_DEVINL void start(const TreeParams& p, const int64_t* found, const Sequence& first) {
+    cur = found[0], end = found[1], b = (int)found[2], base = found[3], run = (uint32_t)found[4];
+    s = first;
+    load(p);
   }
   MOE_DEVINL void load(const TreeParams& p) {
-    s = sequence_of(p, b);
-    kt = key_tiles<KT>(s), rt = row_tiles(p, s), count = tiles_of<KT>(p, s);
+    kt = key_tiles<KT>(s), rt = row_tiles(p, s), count = (uint32_t)tiles_of<KT>(p, s);
     // chunks of 3/4 to 3/2 of a run
-    chunks = rt > 1 ? max(1, (int)((2 * (int64_t)kt + run) / (2 * (int64_t)run))) : 1;
+    chunks = rt > 1 ? max(1u, (2 * kt + run) / (2 * run)) : 1u;
+    size = kt / chunks;
+    longer = kt - size * chunks;
   }
-  MOE_DEVINL int bound(int chunk) const { return chunks == 1 ? (chunk ? kt : 0) : (int)((int64_t)kt * chunk / chunks); }
-  MOE_DEVINL bool next(const TreeParams& p) {
+  MOE_DEVINL bool next(const TreeParams& p, Segment& g) {
     if (cur >= end) return false;
     while (cur >= base + count) {
-      if (b + 1 >= p.B) return cur = end, false;  // (only if the lengths changed under the kernel)
+      if (b + 1 >= p.B) return false;  // (only if the lengths changed under the kernel)
       base += count;
-      ++b;
+      s = sequence_of(p, ++b);
       load(p);
     }
-    const int64_t head = (int64_t)kt * rt, off = cur - base;
-    h = (int)(off / head);
-    const int64_t in = off - h * head;
-    int chunk = 0;
-    if (chunks > 1) {
-      chunk = (int)(in / rt * chunks / kt);
-      while (chunk + 1 < chunks && (int64_t)bound(chunk + 1) * rt <= in) ++chunk;
-      while (chunk > 0 && (int64_t)bound(chunk) * rt > in) --chunk;
-    }
-    const int from = bound(chunk), to = bound(chunk + 1);
-    const int64_t at = in - (int64_t)from * rt;
-    const int row = (int)(at / (to - from));
-    k0 = from + (int)(at - (int64_t)row * (to - from));
-    k1 = (int)min((int64_t)to, k0 + (end - cur));
-    cur += k1 - k0;
-    row0 = row * kTreeRows;
-    rows = min(kTreeRows, s.n * (p.Hq / p.Hkv) - row0);
+    const uint32_t head = kt * rt, off = (uint32_t)(cur - base), h = off / head, in = off - h * head, x = in / rt;
+    const uint32_t chunk = x < longer * (size + 1) ? x / (size + 1) : longer + (x - longer * (size + 1)) / size;
+    const uint32_t from = chunk * size + min(chunk, longer), length = size + (chunk < longer);
+    const uint32_t at = in - from * rt, row = at / length, k0 = from + at - row * length;
+    const uint32_t n = (uint32_t)min((int64_t)(from + length - k0), end - cur);
+    cur += n;
+    g.item = base + (int64_t)(h * rt + row) * kt;
+    g.b = b, g.tok0 = s.tok0, g.n = s.n, g.L = s.L;
+    g.h = (int)h;
+    g.row0 = (int)row * kTreeRows;
+    g.rows = min(kTreeRows, s.n * (p.Hq / p.Hkv) - g.row0);
+    g.k0 = (int)k0, g.k1 = (int)(k0 + n);
+    g.whole = n == kt;
     return true;
   }
-  MOE_DEVINL bool whole() const { return k0 == 0 && k1 == kt; }
-  // The segment's item, as no other's.
-  MOE_DEVINL int64_t item() const { return base + ((int64_t)h * rt + row0 / kTreeRows) * kt; }
 };
+
+// The note of a part, other than its item.
+MOE_DEVINL int what_of(const Segment& g) { return g.h << 16 | g.row0 / kTreeRows << 12 | (g.rows - 1) << 4 | (g.k0 == 0); }
+
+// mbar_wait, out of line where it has to wait.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
+  return mbar_wait(bar, parity, abort, status, where);
+}
+MOE_DEVINL bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status, where);
+}
+MOE_DEVINL bool warp_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status, int where) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort, status, where));
+}
+
+// After a wait that ran out: NaN for what the run has from its seg-th segment on, by the 128
+// softmax threads (`parts` of its parts have states already).
+template <int KT>
+__device__ __noinline__ void give_up(const TreeParams& p, const int64_t* found, const Sequence* first, int seg, int parts, int tid) {
+  Walk<KT> walk;
+  walk.start(p, found, *first);
+  Segment g;
+  const int G = p.Hq / p.Hkv;
+  TreePart* notes = p.parts + (int64_t)blockIdx.x * kTreeParts;
+  for (int i = 0; walk.next(p, g); ++i) {
+    if (i < seg) continue;
+    if (g.whole) {
+      for (int r = tid; r < g.rows; r += 128) {
+        const int x = g.row0 + r;
+        uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)(g.tok0 + x / G) * p.Hq + g.h * G + x % G) * p.d);
+        for (int c = 0; c < p.d / 8; ++c) out[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      }
+    } else if (parts < kTreeParts) {
+      if (tid < g.rows) p.part_ml[((int64_t)blockIdx.x * kTreeParts + parts) * p.rows + tid] = make_float2(0.f, __int_as_float(0x7fc00000));
+      if (tid == 0) notes[parts] = TreePart{g.item, g.tok0, what_of(g)};
+      ++parts;
+    }
+  }
+  if (tid == 0)
+    for (; parts < kTreeParts; ++parts) notes[parts].item = -1;
+}
+
+// Elements of new tokens' V that are not finite, for the rows that attend to them (a row a lane).
+template <int D, int KT>
+__device__ __noinline__ void add_not_finite(const TreeParams& p, const Segment& g, uint32_t tmem, uint64_t bits, bool mine) {
+  const int64_t from = max((int64_t)g.k0 * KT, (int64_t)g.L), to = min((int64_t)g.k1 * KT, (int64_t)g.L + g.n);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tmem_ld_32x32b_x16(tmem + c, o);
+    tc_wait_ld();
+#pragma unroll 1
+    for (int64_t at = from; at < to; ++at) {
+      if (!mine || !(bits >> (at - g.L) & 1)) continue;
+      const int64_t id = p.table[g.b * p.ld_table + (at >> p.page_log2)];
+      const uint16_t* v = p.v_pages + id * p.page_stride + (at & ((1 << p.page_log2) - 1)) * p.position_stride + g.h * p.head_stride + c;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = bf16_bits_to_f32(v[j]);
+        if (!(fabsf(x) <= 3.4e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
+      }
+    }
+    __syncwarp();
+    tmem_st_32x32b_x16(tmem + c, o);
+  }
+  tc_wait_st();
+}
 
 // Which of the 32 positions from the rel-th new token on (rel < 0: cached ones before) a
 // row with the mask `bits` attends to.
@@ -166,10 +238,78 @@ MOE_DEVINL uint32_t attended(int64_t rel, uint64_t bits) {
 
 MOE_DEVINL bool not_finite2(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 
+// The scores of a tile that rows do not attend to: -infinity.
+template <int KT>
+__device__ __noinline__ void mask_scores(uint32_t cols, int64_t rel, uint64_t bits) {
+#pragma unroll 1
+  for (int c = 0; c < KT; c += 32) {
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(cols + c, s);
+    tc_wait_ld();
+    const uint32_t in = attended(rel + c, bits);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!(in >> j & 1)) s[j] = 0xFF800000u;
+    tmem_st_32x32b_x32(cols + c, s);
+  }
+  tc_wait_st();
+}
+
+// A row's softmax so far: its reference m and sum l, and how weights are taken: 2^(scale s - at), at = m (0
+// without any score yet). Scores are scaled apart where m is large (scale 1): what the fused
+// product leaves of its rounding would pass 2^-8.
+struct Running {
+  float m, l, at, scale;
+};
+
+// The reference m of each row moves up to the largest of the piece of scores at column c (by whole steps of
+// log2, so that what there is scales without rounding): the sum, the tile's weights so far and, where there
+// are any, the outputs, whose products are complete.
+template <int D>
+__device__ __noinline__ Running move_reference(uint32_t cols, int c, uint32_t outputs, bool any_output, float scale_log2, float m, float l) {
+  float top = -INFINITY;
+  {
+    uint32_t s[32];
+    tc_wait_st();
+    tmem_ld_32x32b_x32(cols + c, s);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+  }
+  const float nm = fmaxf(m, ceilf(__fmul_rn(top, scale_log2)));
+  // 2^(m - nm), exactly
+  const float f = nm == -INFINITY ? 1.f : m - nm < -126.f ? 0.f : __int_as_float((127 + (int)(m - nm)) << 23);
+  l *= f;
+#pragma unroll 1
+  for (int e = 0; e < c; e += 16) {
+    uint32_t w[16];
+    tmem_ld_32x32b_x16(cols + e, w);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
+    tmem_st_32x32b_x16(cols + e, w);
+  }
+  if (any_output) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int e = 0; e < D; e += 16) {
+      uint32_t o[16];
+      tmem_ld_32x32b_x16(outputs + e, o);
+      tc_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st_32x32b_x16(outputs + e, o);
+    }
+  }
+  tc_wait_st();
+  const float at = nm == -INFINITY ? 0.f : nm;
+  return {nm, l, at, __any_sync(0xffffffffu, fabsf(at) >= 65536.f) ? 1.f : scale_log2};
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_constant__ TrArgs args) {
   using C = TrCfg<D>;
-  constexpr int KT = C::KT, NS = C::kSlots, NB = C::kBufs;
+  constexpr int KT = C::KT, NS = C::kSlots, NB = C::kBufs, NG = C::kSegs;
   const TreeParams& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -181,20 +321,22 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   uint64_t* p_full = s_full + NB;                                   // [NB] weights are written, over the scores
   uint64_t* pv_done = p_full + NB;                                  // [NB] their product is complete: the columns are free
   uint64_t* drain = pv_done + NB;                                   // [1]
-  int64_t* found = reinterpret_cast<int64_t*>(drain + 1);           // the run: first tile, end, sequence, its first tile, the longest's tiles
+  uint64_t* g_full = drain + 1;                                     // [NG] a segment is worked out
+  uint64_t* g_empty = g_full + NG;                                  // [NG] all have read it
+  Segment* segments = reinterpret_cast<Segment*>(smem + C::kOffBar + (8 * C::kBars + 15) / 16 * 16);  // [NG]
+  int64_t* found = reinterpret_cast<int64_t*>(segments + NG);       // the run: first tile, end, sequence, its first tile, the longest's tiles
   int64_t* sums = found + 5;                                        // [8] a warp's tiles
-  int* bad_tile = reinterpret_cast<int*>(sums + 8);                 // [kBadRing] 1 + tile of the run with a bad page
+  Sequence* first_seq = reinterpret_cast<Sequence*>(sums + 8);      // the run's first
+  int* bad_tile = reinterpret_cast<int*>(first_seq + 1);            // [kBadRing] 1 + tile of the run with a bad page
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad_tile + kBadRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* v_bad = abort_flag + 1;  // 1 + segment whose new V holds infinities or NaN
+  static_assert(NG * sizeof(Segment) + 13 * 8 + sizeof(Sequence) + kBadRing * 4 + 12 <= 512, "shared memory exceeded");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < 2 * NS; ++i) mbar_init(&full[i], 1);
     mbar_init(q_full, 4);
     mbar_init(v_ready, 4);
     for (int i = 0; i < NB; ++i) {
@@ -203,7 +345,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(drain, 2);
-    for (int i = 0; i < kBadRing; ++i) bad_tile[i] = 0;
+    for (int i = 0; i < NG; ++i) {
+      mbar_init(&g_full[i], 1);
+      mbar_init(&g_empty[i], 7);  // TMA, two issuers, four softmax warps
+    }
     found[0] = found[1] = 0;
     *abort_flag = 0;
     *v_bad = 0;
@@ -211,6 +356,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     tma_prefetch_desc(&args.tm_k);
     tma_prefetch_desc(&args.tm_v);
   }
+  if (threadIdx.x < kBadRing) bad_tile[threadIdx.x] = 0;
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -225,67 +371,90 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 
   // The run: the sum of all sequences' tiles, then where its share of it begins.
   {
-    int64_t total = 0, first = 0, mine = 0;  // of all; before this thread's last sequence; that one's
+    int64_t total = 0, all = 0, from = 0, to = 0;
     int bad = 0;
-    auto add = [&](int b0) {  // of the sequences b0 .. b0 + 255
-      const int b = b0 + threadIdx.x;
-      mine = 0;
-      if (b < p.B) {
-        const Sequence s = sequence_of(p, b);
-        mine = tiles_of<KT>(p, s);
-        bad |= s.bad;
-      }
-      int64_t upto = mine;  // of the warp's lanes up to this one
-#pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += v;
-      }
-      if (lane == 31) sums[warp] = upto;
-      __syncthreads();
-      first = total + upto - mine;
-#pragma unroll
-      for (int w = 0; w < kTrThreads / 32; ++w) {
-        if (w < warp) first += sums[w];
-        total += sums[w];
-      }
-      if (p.B > kTrThreads) __syncthreads();
-    };
-    for (int b0 = 0; b0 < p.B; b0 += kTrThreads) add(b0);
-    const int64_t all = total, from = run_begin(all, blockIdx.x, p.ctas), to = run_begin(all, blockIdx.x + 1, p.ctas);
-    auto note = [&](int b) {
-      if (first <= from && from < first + mine) {
-        found[0] = from, found[1] = to, found[2] = b, found[3] = first;
-        found[4] = (all + p.ctas - 1) / p.ctas;
-      }
-    };
-    if (p.B <= kTrThreads) {
-      if (from < to) note(threadIdx.x);
-    } else if (from < to) {
+    // (256 sequences at a time; more than those are gone through twice)
+    const int rounds = p.B > kTrThreads ? 2 : 1;
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
       total = 0;
+#pragma unroll 1
       for (int b0 = 0; b0 < p.B; b0 += kTrThreads) {
-        add(b0);
-        note(b0 + threadIdx.x);
+        const int b = b0 + threadIdx.x;
+        Sequence s;
+        int64_t mine = 0;
+        if (b < p.B) {
+          s = sequence_of(p, b);
+          mine = tiles_of<KT>(p, s);
+          bad |= s.bad;
+        }
+        int64_t upto = mine;  // of the warp's lanes up to this one
+#pragma unroll
+        for (int off = 1; off < 32; off *= 2) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += v;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        int64_t first = total + upto - mine;
+#pragma unroll
+        for (int w = 0; w < kTrThreads / 32; ++w) {
+          if (w < warp) first += sums[w];
+          total += sums[w];
+        }
+        if (rounds == 1 || (round == 0 && b0 + kTrThreads >= p.B)) {
+          all = total;
+          from = run_begin(all, blockIdx.x, p.ctas), to = run_begin(all, blockIdx.x + 1, p.ctas);
+        }
+        if (round + 1 == rounds && from < to && first <= from && from < first + mine) {
+          found[0] = from, found[1] = to, found[2] = b, found[3] = first;
+          found[4] = min((all + p.ctas - 1) / p.ctas, (int64_t)1 << 28);
+          *first_seq = s;
+        }
+        if (rounds > 1) __syncthreads();
       }
     }
     if (__syncthreads_or(bad)) {  // sequences that cannot be right: NaN, by all CTAs
+#pragma unroll 1
       for (int b = 0; b < p.B; ++b) {
         const Sequence s = sequence_of(p, b);
         if (!s.bad) continue;
         const int64_t words = (int64_t)s.n * p.Hq * (D / 8);
         uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)s.tok0 * p.Hq * D);
+#pragma unroll 1
         for (int64_t i = (int64_t)blockIdx.x * kTrThreads + threadIdx.x; i < words; i += (int64_t)p.ctas * kTrThreads)
           out[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
       }
     }
   }
-  Walk<KT> walk;
-  walk.start(p, found);
   const int total = (int)(found[1] - found[0]);  // tiles of the run
   TreePart* const parts = p.parts + (int64_t)blockIdx.x * kTreeParts;
 
+  // Segment number i, once it is worked out; false after the last (rows 0) and after a wait that ran out.
+  // (Each reader, once it has copied it, says so on g_empty.)
+  auto segment = [&](int i, Segment& g) {
+    if (!wait_for(&g_full[i % NG], (i / NG) & 1, abort_flag, p.status, 115)) return g.rows = 0, false;
+    g = segments[i % NG];
+    return g.rows > 0;
+  };
+
   if (total == 0) {  // fewer tiles than CTAs
     if (threadIdx.x < kTreeParts) parts[threadIdx.x].item = -1;
+  } else if (warp == 3) {
+    if (lane == 0) {
+      Walk<KT> walk;
+      walk.start(p, found, *first_seq);
+      Segment g;
+#pragma unroll 1
+      for (int i = 0;; ++i) {
+        const bool more = walk.next(p, g);
+        if (!more) g.rows = 0;
+        if (i >= NG && !wait_for(&g_empty[i % NG], (i / NG - 1) & 1, abort_flag, p.status, 116)) break;
+        segments[i % NG] = g;
+        mbar_arrive(&g_full[i % NG]);
+        if (!more) break;
+      }
+    }
   } else if (warp == 0) {
     fence_proxy_async_global();  // the pages are written by ordinary stores of earlier launches
     // keys that one CTA alone reads leave L2 first
@@ -295,83 +464,92 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     const int piece = lane & (pieces - 1), col = lane >> pieces_log2;
     const bool mine = col < D / 64;
     const uint32_t dst = col * (KT * 128) + ((piece << args.box_log2) * 128);
-    int slot = 0, phase = 1, loads = 0, h = 0, place = 0, page = 0;
-    int kh = 0, kplace = 0, kpage = 0;
-    auto load = [&](const CUtensorMap* tm, int head, int at, int id) {
-      if (!warp_wait(&empty[slot], phase, abort_flag, p.status, 101)) return false;
+    int slot = 0, phase = 1, loads = 0, seg = -1, key = 0;
+    Segment g;
+    g.k1 = 0;
+    struct Tile {
+      int h, place, page;
+      bool bad;
+    };
+    // A tile's page, looked up a tile ahead; past the sequence's end, or bad: past the pool, which reads as zeros.
+    auto look_up = [&](Tile& t) {
+      if (++key >= g.k1) {
+        if (!__all_sync(0xffffffffu, segment(++seg, g))) return false;
+        if (lane == 0) mbar_arrive(&g_empty[seg % NG]);
+        key = g.k0;
+      }
+      const int64_t at = (int64_t)key * KT + (piece << args.box_log2);
+      t.h = g.h;
+      t.place = (int)(at & ((1 << p.page_log2) - 1));
+      t.page = p.n_pages;
+      t.bad = false;
+      if (at < (int64_t)g.L + g.n) {
+        const int id = p.table[g.b * p.ld_table + (at >> p.page_log2)];
+        t.bad = id < 0 || id >= p.n_pages;
+        if (!t.bad) t.page = id;
+      }
+      return true;
+    };
+    Tile before, now, next;
+    bool alive = look_up(next);
+    // K0, then K and V of the tile before in turn, then the last V
+#pragma unroll 1
+    for (int i = 0; i < 2 * total && alive; ++i) {
+      const int it = (i + 1) / 2;
+      const bool is_k = i == 0 || (i & 1 && it < total);
+      Tile t = before;
+      if (is_k) {
+        t = next;
+        if (__any_sync(0xffffffffu, t.bad) && lane == 0) bad_tile[it % kBadRing] = it + 1;
+        before = it > 0 ? now : t;  // (its V is next; the first tile's comes after the second's K)
+        now = t;
+        if (it + 1 < total && !look_up(next)) break;
+      } else if (i + 1 == 2 * total) {
+        t = now;
+      }
+      if (!(alive = warp_wait_for(&empty[slot], phase, abort_flag, p.status, 101))) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlot);
       __syncwarp();
       if (mine)
-        tma_load_4d(smem + C::kOffSlots + slot * C::kSlot + dst, tm, col * 64, args.heads_out ? at : head,
-                    args.heads_out ? head : at, id, &full[slot], policy);
+        tma_load_4d(smem + C::kOffSlots + slot * C::kSlot + dst, is_k ? &args.tm_k : &args.tm_v, col * 64, args.heads_out ? t.place : t.h,
+                    args.heads_out ? t.h : t.place, t.page, &full[slot], policy);
       __syncwarp();
       ++loads;
       if (++slot == NS) slot = 0, phase ^= 1;
-      return true;
-    };
-    // a tile's page, looked up a tile ahead; past the sequence's end, or bad: past the pool, which reads as zeros
-    int key = 0, end = 0;
-    bool bad = false;
-    auto look_up = [&]() {
-      const int64_t at = (int64_t)key * KT + (piece << args.box_log2);
-      h = walk.h;
-      place = (int)(at & ((1 << p.page_log2) - 1));
-      page = p.n_pages;
-      bad = false;
-      if (at < (int64_t)walk.s.L + walk.s.n) {
-        const int id = p.table[walk.b * p.ld_table + (at >> p.page_log2)];
-        bad = id < 0 || id >= p.n_pages;
-        if (!bad) page = id;
-      }
-    };
-    auto advance = [&]() {
-      if (++key >= end) {
-        if (!walk.next(p)) return false;
-        key = walk.k0, end = walk.k1;
-      }
-      return true;
-    };
-    bool alive = advance();
-    if (alive) look_up();
-    for (int it = 0; it < total && alive; ++it) {
-      const int ph = kh, pplace = kplace, ppage = kpage;
-      kh = h, kplace = place, kpage = page;
-      if (__any_sync(0xffffffffu, bad) && lane == 0) bad_tile[it % kBadRing] = it + 1;
-      if (it + 1 < total) {
-        if (advance()) look_up(); else alive = false;
-      }
-      alive = alive && load(&args.tm_k, kh, kplace, kpage);
-      if (it > 0) alive = alive && load(&args.tm_v, ph, pplace, ppage);
     }
-    if (alive) load(&args.tm_v, kh, kplace, kpage);
     // every load lands before the CTA ends, also when another role gave up
     volatile int drained = 0;
+#pragma unroll 1
     for (int j = loads > NS ? loads - NS : 0; j < loads; ++j)
-      warp_wait(&full[j % NS], (j / NS) & 1, &drained, p.status, 102);
+      warp_wait_for(&full[j % NS], (j / NS) & 1, &drained, p.status, 102);
   } else if (warp == 1 || warp == 2) {
     if (lane == 0) {
       const uint32_t slots = smem_u32(smem + C::kOffSlots);
-      int slot = 0, phase = 0, buf = 0, turn = 0, it = 0, seg = 0;
+      int slot = 0, phase = 0, buf = 0, turn = 0, it = 0;
       bool alive = true;
       auto advance = [&](int by) {
         if ((slot += by) >= NS) slot -= NS, phase ^= 1;
         if (++buf == NB) buf = 0, turn ^= 1;
       };
+      Segment g;
       if (warp == 1) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(kTreeRows, KT);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(smem));
-        for (; alive && walk.next(p); ++seg) {
-          alive = mbar_wait(q_full, seg & 1, abort_flag, p.status, 104);
-          for (int key = walk.k0; key < walk.k1 && alive; ++key, ++it) {
+#pragma unroll 1
+        for (int seg = 0; alive && segment(seg, g); ++seg) {
+          mbar_arrive(&g_empty[seg % NG]);
+          alive = wait_for(q_full, seg & 1, abort_flag, p.status, 104);
+#pragma unroll 1
+          for (int key = g.k0; key < g.k1 && alive; ++key, ++it) {
             // the columns hold the weights of NB tiles before until their product is complete
-            if ((it >= NB && !mbar_wait(&pv_done[buf], turn ^ 1, abort_flag, p.status, 111)) ||
-                !mbar_wait(&full[slot], phase, abort_flag, p.status, 103)) {
+            if ((it >= NB && !wait_for(&pv_done[buf], turn ^ 1, abort_flag, p.status, 111)) ||
+                !wait_for(&full[slot], phase, abort_flag, p.status, 103)) {
               alive = false;
               break;
             }
             tc_fence_after();
             const uint64_t k_desc = smem_desc_sw128(slots + slot * C::kSlot);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -385,22 +563,25 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       } else {
         constexpr uint32_t idesc_o = idesc_bf16_f32(kTreeRows, D) | (1u << 16);  // B (V) is MN-major
         slot = total > 1 ? 2 : 1;
-        for (; alive && walk.next(p); ++seg) {
+#pragma unroll 1
+        for (int seg = 0; alive && segment(seg, g); ++seg) {
+          mbar_arrive(&g_empty[seg % NG]);
           // (the segment before: its outputs are read by the warps that write this one's weights)
-          for (int key = walk.k0; key < walk.k1 && alive; ++key, ++it) {
-            if (!mbar_wait(&full[slot], phase, abort_flag, p.status, 106) ||
-                !mbar_wait(&p_full[buf], turn, abort_flag, p.status, 105)) {
+#pragma unroll 1
+          for (int key = g.k0; key < g.k1 && alive; ++key, ++it) {
+            if (!wait_for(&full[slot], phase, abort_flag, p.status, 106) ||
+                !wait_for(&p_full[buf], turn, abort_flag, p.status, 105)) {
               alive = false;
               break;
             }
             tc_fence_after();
             const uint64_t v_desc = smem_desc_mn(slots + slot * C::kSlot, KT * 128);
+#pragma unroll 1
+            for (int k2 = 0; k2 < KT / 32; ++k2)
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-                tc_mma_ts(tmem, tmem + C::kColS + buf * KT + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, v_desc + ((kk * 2048) >> 4), idesc_o,
-                          ((key - walk.k0) | kk | part) != 0);
+              for (int in = 0; in < 4; ++in)  // 16 keys' first parts and second ones
+                tc_mma_ts(tmem, tmem + C::kColS + buf * KT + k2 * 32 + (in & 1) * 16 + (in >> 1) * 8,
+                          v_desc + (((2 * k2 + (in >> 1)) * 2048) >> 4), idesc_o, ((key - g.k0) | k2 | in) != 0);
             tc_commit(&empty[slot]);
             tc_commit(&pv_done[buf]);
             advance(it + 2 < total ? 2 : 1);  // the last V follows the one before it
@@ -409,240 +590,226 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       }
       volatile int drained = 0;
       tc_commit(drain);  // all MMAs complete before tensor memory is freed
-      mbar_wait(drain, 0, &drained, p.status, 107);
+      wait_for(drain, 0, &drained, p.status, 107);
     }
-  } else if (warp >= 4) {
+  } else {
     const int quarter = warp & 3, r = quarter * 32 + lane, tid = threadIdx.x - 128;  // r: this thread's row of the tile
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     bool alive = true;
     int buf = 0, turn = 0, last = 0, last_turn = 0, it = 0, seg = 0, tails = 0, n_parts = 0;  // of this tile and of the one before
     const uint32_t per_group = (65535 + G) / G;  // x / G = x per_group >> 16 for x < 4096
-    // The queries of the segment at hand into the swizzled K-major operand, as zeros past the end up to
-    // whole warps (which choose together when to rescale: what another call left there may not decide
-    // that; warps without rows hold what was there).
-    auto fetch_queries = [&]() {
+    // A segment's queries into the swizzled K-major operand, as zeros past the end up to whole warps
+    // (which choose together when to rescale: what another call left there may not decide that;
+    // warps without rows hold what was there). `ready`: they have landed.
+    auto fetch_queries = [&](const Segment& g) {
       constexpr int kChunks = D / 8;
-      const uint16_t* q = p.q + walk.s.tok0 * p.ldq + (int64_t)walk.h * G * D;
-#pragma unroll 4
-      for (int j = tid; j < (walk.rows + 31) / 32 * 32 * kChunks; j += 128) {
+      const uint16_t* q = p.q + g.tok0 * p.ldq + (int64_t)g.h * G * D;
+#pragma unroll 2
+      for (int j = tid; j < (g.rows + 31) / 32 * 32 * kChunks; j += 128) {
         const int row = j / kChunks, c = j % kChunks;
-        const bool in = row < walk.rows;
-        const int x = walk.row0 + (in ? row : 0), i = (int)(x * per_group >> 16);
+        const bool in = row < g.rows;
+        const int x = g.row0 + (in ? row : 0), i = (int)(x * per_group >> 16);
         cp_async_16(smem_u32(smem + (c / 8) * (kTreeRows * 128) + sw128_offset(row, c % 8)),
                     q + i * p.ldq + (x - i * G) * D + c * 8, in ? 16u : 0u);
       }
       cp_async_commit();
     };
-    auto queries_ready = [&]() {
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      warp_arrive(q_full);
+    Segment next, g;
+    // the segment after this one, if there is one (alive is false after a wait that ran out)
+    auto look_ahead = [&](int i) {
+      const bool more = __all_sync(0xffffffffu, segment(i, next));
+      __syncwarp();
+      if (more && lane == 0) mbar_arrive(&g_empty[i % NG]);
+      if (!more && *abort_flag) alive = false;
+      return more;
     };
-    bool more = walk.next(p);
-    if (more) {
-      fetch_queries();
-      queries_ready();
-    }
-    for (; more; ++seg) {
-      const Walk<KT> now = walk;
-      const int rows = now.rows, L = now.s.L, n = now.s.n;
-      const bool mine = r < rows, warp_rows = quarter * 32 < rows;
-      const int x = now.row0 + (mine ? r : 0), i_new = (int)(x * per_group >> 16);
-      const int token = now.s.tok0 + i_new, head = now.h * G + x - i_new * G;
-      uint64_t bits = p.tree ? (uint64_t)p.tree[token] : (2ull << i_new) - 1;
-      if (n < 64) bits &= (1ull << n) - 1;
-      float m = -INFINITY, l = 0.f;
+    bool more = look_ahead(0), ready = false;
+    if (more) fetch_queries(next);
+#pragma unroll 1
+    for (; more && alive; ++seg) {
+      g = next;
+      const bool mine = r < g.rows, warp_rows = quarter * 32 < g.rows;
+      const int x = g.row0 + (mine ? r : 0), i_new = (int)(x * per_group >> 16);
+      uint64_t bits = p.tree ? (uint64_t)p.tree[g.tok0 + i_new] : (2ull << i_new) - 1;
+      if (g.n < 64) bits &= (1ull << g.n) - 1;
+      if (!ready) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        warp_arrive(q_full);
+      }
+      Running now = {-INFINITY, 0.f, 0.f, p.scale_log2};
       bool poison = false;
-      for (int key = now.k0; key < now.k1 && alive; ++key, ++it) {
-        if (!(alive = warp_wait(&s_full[buf], turn, abort_flag, p.status, 108))) break;
+#pragma unroll 1
+      for (int key = g.k0; key < g.k1; ++key, ++it) {
+        if (!(alive = warp_wait_for(&s_full[buf], turn, abort_flag, p.status, 108))) break;
         tc_fence_after();
         if (bad_tile[it % kBadRing] == it + 1) poison = true;
-        const int64_t rel = (int64_t)key * KT - L;  // of the tile's first position to the first new token
+        const int64_t rel = (int64_t)key * KT - g.L;  // of the tile's first position to the first new token
         const bool tail = rel + KT > 0;
         if (warp_rows) {
-          // Twice over the scores in tensor memory, in pieces: the largest, then the weights, over
-          // the scores of their piece. (All of a tile's scores in registers are one long piece of code,
-          // which a call of few tiles spends its time fetching.)
+          // Once over the scores in tensor memory, in pieces of 32 keys, with the reference at hand, each
+          // piece's weights over its scores. The sum of the weights shows where the reference has to move.
           const uint32_t cols = tmem + lanes + C::kColS + buf * KT;
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (tail) mask_scores<KT>(cols, rel, bits);
+          bool moved = false;
 #pragma unroll 1
-          for (int c = 0; c < KT; c += 32) {
-            uint32_t s[32];
-            tmem_ld_32x32b_x32(cols + c, s);
-            tc_wait_ld();
-            if (tail) {
-              const uint32_t in = attended(rel + c, bits);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(in >> j & 1)) s[j] = 0xFF800000u;
-              tmem_st_32x32b_x32(cols + c, s);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-          }
-          if (tail) tc_wait_st();
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
-            const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.f : ex2(m - nm);  // (m -infinity: 0)
-            l *= f;
-            m = nm;
-            if (key > now.k0) {
-              // O is whole once the product before is complete
-              if (!(alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 109))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(tmem + lanes + c, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st_32x32b_x16(tmem + lanes + c, o);
-              }
-            }
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
-          // What the fused product leaves of a large reference's rounding would pass 2^-8: then scale apart,
-          // rounded as the reference was.
-          const bool apart = __any_sync(0xffffffffu, fabsf(ref) >= 65536.f);
-          const float sc1 = apart ? 1.f : p.scale_log2;
-          const float2 sc = make_float2(sc1, sc1), nr = make_float2(-ref, -ref);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < KT; c += 32) {
+          for (int c = 0; c < KT;) {
             uint32_t s[32], hi[16], lo[16];
             tmem_ld_32x32b_x32(cols + c, s);
+            const float2 sc = make_float2(now.scale, now.scale), nr = make_float2(-now.at, -now.at);
             tc_wait_ld();
-            if (apart) {
+            if (now.scale == 1.f) {  // (the same for the whole warp)
 #pragma unroll
               for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__fmul_rn(__uint_as_float(s[j]), p.scale_log2));
             }
+            float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sc, nr);
               const float2 e = make_float2(ex2(y.x), ex2(y.y));
-              sum = __fadd2_rn(sum, e);
+              sums = __fadd2_rn(sums, e);
               split_bf16(e.x, e.y, hi[j], lo[j]);
             }
+            const float sum = sums.x + sums.y;
+            if (__any_sync(0xffffffffu, !(sum <= kMostSum) || now.m == -INFINITY) && !moved) {
+              if (key > g.k0 && !(alive = warp_wait_for(&pv_done[last], last_turn, abort_flag, p.status, 109))) break;
+              now = move_reference<D>(cols, c, tmem + lanes, key > g.k0, p.scale_log2, now.m, now.l);
+              moved = true;
+              continue;
+            }
+            moved = false;
+            now.l += sum;
             tmem_st_32x32b_x16(cols + c, hi);
             tmem_st_32x32b_x16(cols + c + 16, lo);
+            c += 32;
           }
-          l += sum.x + sum.y;
+          if (!alive) break;
           tc_wait_st();
         }
         if (tail) {
           // V of this tile: what no row attends to as zeros, and elements of the new tokens that are not
           // finite (their rows' outputs have them added below)
           const int at = it + 1 < total ? 2 * it + 2 : 2 * it + 1;  // of the ring's loads
-          if (!(alive = warp_wait(&full[at % NS], (at / NS) & 1, abort_flag, p.status, 113))) break;
+          if (!(alive = warp_wait_for(&full[at % NS], (at / NS) & 1, abort_flag, p.status, 113))) break;
           uint8_t* v = smem + C::kOffSlots + (at % NS) * C::kSlot;
-          const int first = (int)max((int64_t)0, -rel), none = (int)min((int64_t)KT, n - rel);
+          const int first = (int)max((int64_t)0, -rel), none = (int)min((int64_t)KT, g.n - rel);
           bool odd = false;
+#pragma unroll 1
           for (int j = first * (D / 8) + tid; j < KT * (D / 8); j += 128) {
             const int row = j / (D / 8), c = j % (D / 8);
             uint4* w = reinterpret_cast<uint4*>(v + (c / 8) * (KT * 128) + sw128_offset(row, c % 8));
-            uint4 x = make_uint4(0, 0, 0, 0);
+            uint4 e = make_uint4(0, 0, 0, 0);
             if (row < none) {
-              x = *w;
-              if (!(not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w))) continue;
+              e = *w;
+              if (!(not_finite2(e.x) || not_finite2(e.y) || not_finite2(e.z) || not_finite2(e.w))) continue;
               odd = true;
-              uint32_t* e = &x.x;
+              uint32_t* pair = &e.x;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
+                if ((pair[k] & 0x7F80u) == 0x7F80u) pair[k] &= 0xFFFF0000u;
+                if ((pair[k] & 0x7F800000u) == 0x7F800000u) pair[k] &= 0xFFFFu;
               }
             }
-            *w = x;
+            *w = e;
           }
           if (odd) *v_bad = seg + 1;
           fence_proxy_async_smem();
           warp_arrive(v_ready);
-          if (!(alive = warp_wait(v_ready, tails++ & 1, abort_flag, p.status, 114))) break;  // (also: v_bad is known)
+          if (!(alive = warp_wait_for(v_ready, tails++ & 1, abort_flag, p.status, 114))) break;  // (also: v_bad is known)
         }
         tc_fence_before();
         warp_arrive(&p_full[buf]);
         last = buf, last_turn = turn;
         if (++buf == NB) buf = 0, turn ^= 1;
       }
+      if (!alive) break;
       // The next segment's queries: the products that read these are complete (their scores were), and
       // the next scores' run while this segment's outputs are read.
-      more = walk.next(p);
-      if (alive && more) fetch_queries();
+      more = look_ahead(seg + 1);
+      if (more) fetch_queries(next);
       // the segment's outputs: every product is complete with the last one
-      if (alive) alive = warp_wait(&pv_done[last], last_turn, abort_flag, p.status, 110);
-      if (alive && more) queries_ready();
-      const bool whole = now.whole();
-      int part = 0;
-      if (!whole) {
-        part = min(n_parts++, kTreeParts - 1);  // (never more: a chunk has 3/4 of a run at least)
-        if (tid == 0) parts[part] = TreePart{now.item(), now.s.tok0, now.h << 16 | now.row0 / kTreeRows << 12 | (rows - 1) << 4 | (now.k0 == 0)};
+      if (!(alive = alive && warp_wait_for(&pv_done[last], last_turn, abort_flag, p.status, 110))) break;
+      tc_fence_after();
+      if (more) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        warp_arrive(q_full);
+        ready = true;
       }
-      const int64_t state = ((int64_t)blockIdx.x * kTreeParts + part) * p.rows + r;
+      float m = now.m, l = now.l;
       if (l != l && m == -INFINITY) m = 0.f;  // nothing but NaN: not a state without positions
-      if (!alive || poison) {  // after a wait that ran out, or a bad page: NaN
-        m = 0.f;
-        l = __int_as_float(0x7fc00000);
+      if (poison) m = 0.f, l = __int_as_float(0x7fc00000);  // a bad page: NaN
+      int part = 0;
+      if (!g.whole) {
+        part = min(n_parts++, kTreeParts - 1);  // (never more: a chunk has 3/4 of a run at least)
+        if (tid == 0) parts[part] = TreePart{g.item, g.tok0, what_of(g)};
       }
-      if (alive) tc_fence_after();
-      if (mine && !whole) p.part_ml[state] = make_float2(m, l);
-      if (warp_rows && (alive || whole)) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing attended to: zeros
-        const bool odd = alive && *v_bad == seg + 1;
+      const int64_t state = ((int64_t)blockIdx.x * kTreeParts + part) * p.rows;  // of the tile's first row
+      if (mine && !g.whole) p.part_ml[state + r] = make_float2(m, l);
+      if (warp_rows && !poison && *v_bad == seg + 1) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
+      // A quad of lanes holds 8 columns of a row at a time; lanes exchange until each has 16 bytes that lie
+      // together, so that a store is 64 bytes of each of 8 rows. (A row a lane: 16 bytes of each of 32 rows,
+      // 5 us for 128 rows of 256.)
+      const float inv = l == 0.f ? 0.f : g.whole ? 1.f / l : 1.f;  // nothing attended to: zeros
+      const int q = lane & 3;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (alive) {
-            tmem_ld_32x32b_x32(tmem + lanes + c, o);
-            tc_wait_ld();
-          } else {
+      for (int half = 0; half < 32 && quarter * 32 + half < g.rows; half += 16) {
+        float f[2];
+        uint8_t* dst[2];  // of the two rows that this lane stores parts of; null past the end
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0x7fc00000u;
-          }
-          if (l == 0.f) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
-          }
-          if (odd && mine && !poison) {
-            const int64_t from = max((int64_t)now.k0 * KT, (int64_t)L), to = min((int64_t)now.k1 * KT, (int64_t)L + n);
+        for (int k = 0; k < 2; ++k) {
+          const int in = half + 8 * k + (lane >> 2), row = quarter * 32 + in;
+          f[k] = __shfl_sync(0xffffffffu, inv, in);
+          const int y = g.row0 + row, i = (int)(y * per_group >> 16);
+          dst[k] = row >= g.rows ? nullptr
+                   : g.whole ? reinterpret_cast<uint8_t*>(p.out + ((int64_t)(g.tok0 + i) * p.Hq + g.h * G + y - i * G) * D) + q * 16
+                             : reinterpret_cast<uint8_t*>(p.part_o + (state + row) * D) + (8 * (q & 1) + 2 * (q & 2)) * 4;
+        }
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32 + half) << 16);
 #pragma unroll 1
-            for (int64_t at = from; at < to; ++at) {
-              if (!(bits >> (at - L) & 1)) continue;
-              const int64_t id = p.table[now.b * p.ld_table + (at >> p.page_log2)];
-              const uint16_t* v = p.v_pages + id * p.page_stride + (at & ((1 << p.page_log2) - 1)) * p.position_stride +
-                                  now.h * p.head_stride + c;
+        for (int c = 0; c < D; c += 64) {
+          uint32_t o[2][16];  // two loads in flight
+          tmem_ld_16x256b_x4(from + c, o[0]);
+          tmem_ld_16x256b_x4(from + c + 32, o[1]);
+          tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float x = bf16_bits_to_f32(v[j]);
-                if (!(fabsf(x) <= 3.4e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
+          for (int z = 0; z < 4; ++z) {
+            const int k = z & 1, c32 = c + 32 * (z >> 1);
+            float2 v[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              v[b] = make_float2(__uint_as_float(o[z >> 1][4 * b + 2 * k]) * f[k], __uint_as_float(o[z >> 1][4 * b + 2 * k + 1]) * f[k]);
+              if (f[k] == 0.f) v[b] = make_float2(0.f, 0.f);
+            }
+            if (g.whole) {
+              uint32_t w[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) w[b] = pack_bf16(v[b].x, v[b].y);
+              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, q & 1 ? w[0] : w[1], 1);
+              const uint32_t r1 = __shfl_xor_sync(0xffffffffu, q & 1 ? w[2] : w[3], 1);
+              const uint32_t a0 = q & 1 ? r0 : w[0], a1 = q & 1 ? w[1] : r0, b0 = q & 1 ? r1 : w[2], b1 = q & 1 ? w[3] : r1;
+              const uint32_t s0 = __shfl_xor_sync(0xffffffffu, q & 2 ? a0 : b0, 2);
+              const uint32_t s1 = __shfl_xor_sync(0xffffffffu, q & 2 ? a1 : b1, 2);
+              if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + c32 * 2) = q & 2 ? make_uint4(s0, s1, b0, b1) : make_uint4(a0, a1, s0, s1);
+            } else {
+#pragma unroll
+              for (int b = 0; b < 4; b += 2) {
+                const float2 send = q & 1 ? v[b] : v[b + 1], keep = q & 1 ? v[b + 1] : v[b];
+                const float e0 = __shfl_xor_sync(0xffffffffu, send.x, 1), e1 = __shfl_xor_sync(0xffffffffu, send.y, 1);
+                if (dst[k])
+                  *reinterpret_cast<float4*>(dst[k] + (c32 + 8 * b) * 4) = q & 1 ? make_float4(e0, e1, keep.x, keep.y) : make_float4(keep.x, keep.y, e0, e1);
               }
             }
           }
-          if (!mine) {
-          } else if (whole) {
-            uint16_t* out = p.out + ((int64_t)token * p.Hq + head) * D + c;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16(__uint_as_float(o[8 * j + 2 * k]) * inv, __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            float* out = p.part_o + state * D + c;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(out + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
-          __syncwarp();  // (tcgen05.ld wants the warp undivided)
         }
       }
       tc_fence_before();
     }
     cp_async_wait<0>();  // (after a wait that ran out: queries on their way)
-    if (tid == 0)
-      for (int i = n_parts; i < kTreeParts; ++i) parts[i].item = -1;
+    if (!alive)
+      give_up<KT>(p, found, first_seq, seg, n_parts, tid);
+    else if (tid < kTreeParts && tid >= n_parts)
+      parts[tid].item = -1;
   }
   __syncwarp();  // the single-lane roles join their warps
   tc_fence_before();
@@ -651,8 +818,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Merges items' parts. Every block reads all notes; eight rows of an item at a time, a warp a
-// row. (Grids over all rows would mostly find nothing to do: 60 sequences of 59 tokens, 48000
+// Merges items' parts. Every block reads all notes and counts the rows that need it; it takes a row
+// at a time, a warp every eighth part, where they are few, else eight rows, a warp each.
+// (Grids over all rows would mostly find nothing to do: 60 sequences of 59 tokens, 48000
 // rows in 480 items that no run cuts, 206 us instead of 33.)
 constexpr int kMergeWarps = 8;
 template <int D>
@@ -661,94 +829,93 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   constexpr int kAll = kTreeMaxSms * kTreeParts, kThreads = 32 * kMergeWarps, kPer = (kAll + kThreads - 1) / kThreads;
   __shared__ int list[kAll];
   __shared__ float weight[kMergeWarps][kAll];
+  __shared__ float4 sums[kMergeWarps][D / 4];
   __shared__ int counts[kMergeWarps];
   __shared__ TreePart chosen;
-  __shared__ int chosen_unit;  // of the item
+  __shared__ int chosen_row;  // of the item
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, all = p.ctas * kTreeParts;
-  // this thread's notes, and the units of all
+  // this thread's notes, and the rows of all first parts
   TreePart mine[kPer];
-  int units = 0;
+  int rows_of[kPer], rows = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     mine[k].item = -1;
     if (tid * kPer + k < all) mine[k] = p.parts[tid * kPer + k];
   }
 #pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    if (mine[k].item >= 0 && (mine[k].what & 1)) units += ((mine[k].what >> 4 & 255) + kMergeWarps) / kMergeWarps;
-  int upto = units;
+  for (int k = 0; k < kPer; ++k) rows += rows_of[k] = mine[k].item >= 0 && (mine[k].what & 1) ? (mine[k].what >> 4 & 255) + 1 : 0;
+  auto ordered = [&](int x, int& before) {  // the sum over the block, and that of the threads before
+    int upto = x;
 #pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += v;
-  }
-  if (lane == 31) counts[warp] = upto;
-  __syncthreads();
-  int n_units = 0, before = upto - units;
+    for (int off = 1; off < 32; off *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    if (lane == 31) counts[warp] = upto;
+    __syncthreads();
+    int total = 0;
+    before = upto - x;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    if (w < warp) before += counts[w];
-    n_units += counts[w];
+    for (int w = 0; w < kMergeWarps; ++w) {
+      if (w < warp) before += counts[w];
+      total += counts[w];
+    }
+    return total;
+  };
+  int before;
+  const int n_rows = ordered(rows, before);
+  const bool alone = n_rows <= (int)gridDim.x;  // a row a block
+  const int per = alone ? 1 : kMergeWarps;
+  int units_before = before, units = rows, n_units = n_rows;
+  if (!alone) {
+    __syncthreads();
+    units = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) units += (rows_of[k] + per - 1) / per;
+    n_units = ordered(units, units_before);
   }
   const int G = p.Hq / p.Hkv;
   for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
     __syncthreads();  // (the unit before is done with what is shared)
-    if (before <= unit && unit < before + units) {
-      int u = before;
+    if (units_before <= unit && unit < units_before + units) {
+      int u = units_before;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        if (mine[k].item < 0 || !(mine[k].what & 1)) continue;
-        const int n = ((mine[k].what >> 4 & 255) + kMergeWarps) / kMergeWarps;
-        if (u <= unit && unit < u + n) {
-          chosen = mine[k];
-          chosen_unit = unit - u;
-        }
+        const int n = (rows_of[k] + per - 1) / per;
+        if (u <= unit && unit < u + n) chosen = mine[k], chosen_row = (unit - u) * per;
         u += n;
       }
     }
     __syncthreads();
     const TreePart first = chosen;
-    const int rows = (first.what >> 4 & 255) + 1, r = chosen_unit * kMergeWarps + warp;
+    const int r = chosen_row + (alone ? 0 : warp);
     // the item's parts, in the order of their places
-    int is = 0;
+    int is = 0, at;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) is += mine[k].item == first.item;
-    int at = is;
-#pragma unroll
-    for (int off = 1; off < 32; off *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, at, off);
-      if (lane >= off) at += v;
-    }
-    if (lane == 31) counts[warp] = at;
-    __syncthreads();
-    int n = 0;
-    at -= is;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      if (w < warp) at += counts[w];
-      n += counts[w];
-    }
+    const int n = ordered(is, at);
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (mine[k].item == first.item) list[at++] = tid * kPer + k;
     __syncthreads();
-    if (r >= rows) continue;
-    float M = -INFINITY, sum = 0.f;
+    if (r > (first.what >> 4 & 255)) continue;
+    // every warp: the weights of all parts (as many as 32 at once)
+    float M = -INFINITY, mass = 0.f;
+    float2 ml = make_float2(-INFINITY, 0.f);
     for (int i = lane; i < n; i += 32) {
-      const float2 ml = p.part_ml[(int64_t)list[i] * p.rows + r];
-      M = fmaxf(M, ml.x);
-      weight[warp][i] = ml.x;
-      sum = i == lane ? ml.y : sum;  // (the lane's first; others are read again)
+      const float2 x = p.part_ml[(int64_t)list[i] * p.rows + r];
+      M = fmaxf(M, x.x);
+      if (i < 32) ml = x;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float mass = 0.f;
     for (int i = lane; i < n; i += 32) {
-      const float x = weight[warp][i], f = x == -INFINITY ? 0.f : ex2(x - M);
+      const float2 x = i < 32 ? ml : p.part_ml[(int64_t)list[i] * p.rows + r];
+      const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
       weight[warp][i] = f;
-      mass = fmaf(f, i == lane ? sum : p.part_ml[(int64_t)list[i] * p.rows + r].y, mass);
+      mass = fmaf(f, x.y, mass);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, off);
@@ -756,36 +923,59 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
     float4 acc[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane * 4 < D) {
-      const float* o = p.part_o + (int64_t)r * D + lane * 4;
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        float4 v[8][kC];
+    const bool in = lane * 4 < D;
+    const float* o = p.part_o + (int64_t)r * D + (in ? lane * 4 : 0);
+    const int step = alone ? kMergeWarps : 1;
+    for (int i0 = alone ? warp : 0; i0 < n; i0 += 4 * step) {
+      float4 v[4][kC];
+      float f[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // (a part in which the row attends to nothing has zeros)
+      for (int i = 0; i < 4; ++i) {  // (a part in which the row attends to nothing has zeros)
+        const int k = i0 + i * step;
+        f[i] = 0.f;
+        if (k >= n) continue;
+        f[i] = weight[warp][k];
+        const float* from = o + (int64_t)list[k] * p.rows * D;
 #pragma unroll
-          for (int c = 0; c < kC; ++c)
-            v[i][c] = *reinterpret_cast<const float4*>(o + (int64_t)list[min(i0 + i, n - 1)] * p.rows * D + c * 128);
+        for (int c = 0; c < kC; ++c) v[i][c] = *reinterpret_cast<const float4*>(from + c * 128);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i0 + i >= n) break;
-          const float f = weight[warp][i0 + i];
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i * step >= n) continue;
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            acc[c].x = fmaf(f, v[i][c].x, acc[c].x);
-            acc[c].y = fmaf(f, v[i][c].y, acc[c].y);
-            acc[c].z = fmaf(f, v[i][c].z, acc[c].z);
-            acc[c].w = fmaf(f, v[i][c].w, acc[c].w);
-          }
+        for (int c = 0; c < kC; ++c) {
+          acc[c].x = fmaf(f[i], v[i][c].x, acc[c].x);
+          acc[c].y = fmaf(f[i], v[i][c].y, acc[c].y);
+          acc[c].z = fmaf(f[i], v[i][c].z, acc[c].z);
+          acc[c].w = fmaf(f[i], v[i][c].w, acc[c].w);
         }
       }
-      const float inv = mass == 0.f ? 0.f : 1.f / mass;  // nothing attended to: zeros
-      const int x = (first.what >> 12 & 15) * kTreeRows + r;
-      uint16_t* out = p.out + ((int64_t)(first.tok0 + x / G) * p.Hq + (first.what >> 16) * G + x % G) * D + lane * 4;
+    }
+    if (alone) {
 #pragma unroll
       for (int c = 0; c < kC; ++c)
-        *reinterpret_cast<uint2*>(out + c * 128) =
-            make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
+        if (in) sums[warp][lane + 32 * c] = acc[c];
+      __syncthreads();
+      if (warp > 0) continue;
+#pragma unroll
+      for (int w = 1; w < kMergeWarps; ++w)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const float4 v = sums[w][in ? lane + 32 * c : 0];
+          acc[c].x += v.x;
+          acc[c].y += v.y;
+          acc[c].z += v.z;
+          acc[c].w += v.w;
+        }
     }
+    if (!in) continue;
+    const float inv = mass == 0.f ? 0.f : 1.f / mass;  // nothing attended to: zeros
+    const int x = (first.what >> 12 & 15) * kTreeRows + r;
+    uint16_t* out = p.out + ((int64_t)(first.tok0 + x / G) * p.Hq + (first.what >> 16) * G + x % G) * D + lane * 4;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      *reinterpret_cast<uint2*>(out + c * 128) =
+          make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
   }
 }
 

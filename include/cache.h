@@ -133,8 +133,8 @@ int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t 
  *   ws     256-byte aligned, >= moe_tree_attention_workspace_bytes (no initialisation
  *          needed), holds the status word; where the status says MOE_DEV_TIMEOUT, the rows
  *          not computed are NaN
- * 0 <= N < 2^24 (0 launches nothing), 1 <= n_sequences <= 65535, width * page <= 2^28, d in
- * {64, 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a KV head.
+ * 0 <= N < 2^24 (0 launches nothing), 1 <= n_sequences <= 65535, width * page <= 2^28
+ * and below 2^34 / n_kv_heads, d in {64, 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a KV head.
  * Scores and softmax in fp32; the softmax weights multiply the values as two bf16 parts
  * (2^-16 of each weight), with fp32 sums. Two launches: partial states over slices of the
  * sequences, cut evenly over the SMs whatever their lengths, then their merge in a fixed

@@ -185,21 +185,17 @@ class Seq:
         self.chunks = max(1, (2 * kt + run) // (2 * run)) if rt > 1 else 1
         self.count = heads * kt * rt
 
-    def bound(self, chunk):
-        return self.kt * chunk // self.chunks
+        self.size, self.longer = divmod(kt, self.chunks) if kt else (0, 0)
 
     def segment(self, off, left):
         """(head, row tile, k0, k1) of the segment at a tile, at most `left` tiles long."""
         h, at = divmod(off, self.kt * self.rt)
-        chunk = at // self.rt * self.chunks // self.kt
-        while chunk + 1 < self.chunks and self.bound(chunk + 1) * self.rt <= at:
-            chunk += 1
-        while chunk > 0 and self.bound(chunk) * self.rt > at:
-            chunk -= 1
-        lo, hi = self.bound(chunk), self.bound(chunk + 1)
-        row, k = divmod(at - lo * self.rt, hi - lo)
-        assert 0 <= row < self.rt
-        return h, row, lo + k, min(hi, lo + k + left)
+        x, long = at // self.rt, self.longer * (self.size + 1)
+        chunk = x // (self.size + 1) if x < long else self.longer + (x - long) // self.size
+        lo, n = chunk * self.size + min(chunk, self.longer), self.size + (chunk < self.longer)
+        row, k = divmod(at - lo * self.rt, n)
+        assert 0 <= row < self.rt and 0 <= chunk < self.chunks
+        return h, row, lo + k, min(lo + n, lo + k + left)
 
 
 def cut(sizes, ctas):
