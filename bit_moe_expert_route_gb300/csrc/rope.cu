@@ -73,17 +73,44 @@ MOE_DEVINL void pack(const float2 (&a)[2], const float2 (&b)[2], uint2& x, uint2
   }
 }
 
-// The place of token t: its sequence is the last b with starts[b] <= t.
-MOE_DEVINL bool find_place(const RopeParams& p, int t, int64_t& place, int& position) {
-  int lo = 0, hi = p.B + 1;  // starts[lo - 1] <= t (or lo 0), starts[hi] > t (or hi B + 1)
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (p.starts[mid] <= t) lo = mid + 1; else hi = mid;
+// The last b with starts[b] <= t (-1: none; B: t is past the last), by a warp: 32 places a step.
+MOE_DEVINL int find_sequence(const int32_t* starts, int B, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B + 1;  // starts[lo - 1] <= t, starts[lo + n] > t
+#pragma unroll 1
+  while (n > 0) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool le = at < lo + n && starts[at] <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));  // (rising: the first c lanes)
+    if (c == 0) break;
+    const int end = lo + n;
+    lo += (c - 1) * step + 1;
+    n = min(step - 1, end - lo);
   }
-  const int b = lo - 1;
-  if (b < 0 || b >= p.B) return false;  // no sequence's
-  const int from = p.starts[b];
-  if (t < from || t >= p.starts[b + 1]) return false;  // (only where starts do not rise)
+  return lo - 1;
+}
+
+// The place of token t, whose sequence is b or one after it.
+MOE_DEVINL bool find_place(const RopeParams& p, int b, int t, int64_t& place, int& position) {
+  b = max(b, 0);
+  int from = b < p.B ? p.starts[b] : 0, to = b < p.B ? p.starts[b + 1] : 0;
+#pragma unroll 1
+  for (int i = 0; i < 3 && b < p.B && t >= to; ++i) {
+    ++b;
+    from = to;
+    if (b < p.B) to = p.starts[b + 1];
+  }
+  if (b < p.B && t >= to) {  // many short sequences
+    int hi = p.B + 1;
+#pragma unroll 1
+    while (b < hi) {
+      const int mid = (b + hi) / 2;
+      if (p.starts[mid] <= t) b = mid + 1; else hi = mid;
+    }
+    --b;
+    if (b >= 0 && b < p.B) from = p.starts[b], to = p.starts[b + 1];
+  }
+  if (b < 0 || b >= p.B || t < from || t >= to) return false;  // no sequence's
   const int64_t at = (int64_t)max(p.lens[b], 0) + ((int64_t)t - from);
   const int64_t index = at >> p.page_log2;
   if (index >= p.width) return false;
@@ -95,7 +122,7 @@ MOE_DEVINL bool find_place(const RopeParams& p, int t, int64_t& place, int& posi
 }
 
 // cos and sin of the angle by which a pair of token t turns.
-MOE_DEVINL float2 turn_of(const RopeParams& p, int t, int pair, int position) {
+MOE_DEVINL float2 turn_of(const RopeParams& p, int t, int pair, float freq, uint64_t turns, int position) {
   int axis = 0;
   if (p.n_axes > 1) {
     if (p.cyclic) {
@@ -108,8 +135,7 @@ MOE_DEVINL float2 turn_of(const RopeParams& p, int t, int pair, int position) {
     }
   }
   const int pos = p.positions ? p.positions[axis * p.ld_positions + t] : position;
-  const float freq = p.freqs[pair];
-  const uint64_t turn = turns_per_position(freq) * (uint64_t)(int64_t)pos;
+  const uint64_t turn = turns * (uint64_t)(int64_t)pos;
   const int32_t left = (int32_t)(uint32_t)((turn + 0x80000000ull) >> 32);  // of a turn, in 2^-32
   float2 cs;
   sincospif((float)left * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31
@@ -120,10 +146,23 @@ MOE_DEVINL float2 turn_of(const RopeParams& p, int t, int pair, int position) {
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeMaxTokens = 32;  // a block's
 
+// The sum of squares of 2^-70 of a head's elements.
+template <int LPR>
+__device__ __noinline__ float small_squares(float2 a0, float2 a1, float2 b0, float2 b1) {
+  const float f = 8.470329472543003e-22f;
+  const float x[8] = {a0.x * f, a0.y * f, a1.x * f, a1.y * f, b0.x * f, b0.y * f, b1.x * f, b1.y * f};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+
 template <int LPR, bool PAGED, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p) {
   constexpr int RPW = 32 / LPR;  // heads a warp's load holds: a group
-  constexpr int U = 4;           // groups at a time
+  constexpr int U = 2;           // groups at a time
   extern __shared__ float2 rope_smem[];  // [tokens][pairs]
   __shared__ int64_t places[kRopeMaxTokens];
   __shared__ int ats[kRopeMaxTokens];
@@ -137,34 +176,42 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams 
   const int j_step = max(1, kRopeWarps / p.split);
   const int share = p.token_blocks > 1 ? (int)(blockIdx.x % p.token_blocks) * kRopeWarps + warp : warp & (p.split - 1);
   int j = p.token_blocks > 1 ? 0 : warp / p.split;  // token of the block
-  const int groups0 = (p.part[0].heads + RPW - 1) / RPW, groups = groups0 + (p.part[1].heads + RPW - 1) / RPW;
-  int g = share;                                    // first group of a batch
-  bool more = j < n_tokens && share < groups;
 
-  // this lane's elements of a head: four from the one place, four from the other
+  // this lane's elements of a head: four from the one place, four from the other (all lanes' first
+  // four lie together, and their second four)
   const int turning = p.pairs / 4;  // lanes that turn
   const bool turns = c < turning, active = c * 8 < p.d;
-  const int at_a = ADJ || !turns ? c * 8 : c * 4;
-  const int at_b = ADJ || !turns ? at_a + 4 : at_a + p.pairs;
+  const int at_a = ADJ ? c * 8 : turns ? c * 4 : 2 * p.pairs + (c - turning) * 4;
+  const int at_b = ADJ ? at_a + 4 : turns ? at_a + p.pairs : at_a + p.d / 2 - p.pairs;
 
+  // A batch: U groups of one part's heads of one token, from group g on. The groups of both
+  // parts are counted on, part 1's from `groups0`.
+  const int groups0 = (p.part[0].heads + RPW - 1) / RPW, groups = groups0 + (p.part[1].heads + RPW - 1) / RPW;
+  int g = share;
+  bool more = j < n_tokens && g < groups;
   uint2 va[U], vb[U];
+  auto heads_left = [&](int k) {  // of the part, from this lane's head on (0: none)
+    return active ? p.part[k].heads - ((g - (k ? groups0 : 0)) * RPW + sub) : 0;
+  };
   auto fetch = [&]() {
+    const int k = g >= groups0;
     int64_t row = t0 + j;
     if (PAGED && p.rows) {
       row = p.rows[row];
       if (row < 0 || row >= p.n_rows) return;  // (left out below)
     }
-    const uint16_t* s0 = p.part[0].src + row * p.part[0].ld;
-    const uint16_t* s1 = p.part[1].src + row * p.part[1].ld;
+    const uint16_t* s = p.part[k].src + row * p.part[k].ld + ((g - (k ? groups0 : 0)) * RPW + sub) * p.d;
+    const int left = heads_left(k), step = p.split * RPW;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int gu = g + u * p.split;
-      const bool k = gu >= groups0;
-      const int head = (k ? gu - groups0 : gu) * RPW + sub;
-      if (active && head < (k ? p.part[1].heads : p.part[0].heads)) {
-        const uint16_t* s = (k ? s1 : s0) + head * p.d;
-        va[u] = *reinterpret_cast<const uint2*>(s + at_a);
-        vb[u] = *reinterpret_cast<const uint2*>(s + at_b);
+      if (u * step < left) {
+        if constexpr (ADJ) {
+          const uint4 x = *reinterpret_cast<const uint4*>(s + u * step * p.d + at_a);
+          va[u] = make_uint2(x.x, x.y), vb[u] = make_uint2(x.z, x.w);
+        } else {
+          va[u] = *reinterpret_cast<const uint2*>(s + u * step * p.d + at_a);
+          vb[u] = *reinterpret_cast<const uint2*>(s + u * step * p.d + at_b);
+        }
       }
     }
   };
@@ -172,120 +219,146 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams 
   for (int u = 0; u < U; ++u) va[u] = vb[u] = make_uint2(0, 0);
   if (more) fetch();
 
+  // this thread's first pair
+  int pair = p.pairs > 0 ? threadIdx.x % p.pairs : 0;
+  float freq = p.pairs > 0 ? p.freqs[pair] : 0.f;
+  uint64_t turns_by = turns_per_position(freq);
   if constexpr (PAGED) {
-    if (threadIdx.x < n_tokens) {
-      const int t = (int)t0 + threadIdx.x;
+    if (warp == 0) {
+      const int t = (int)t0 + lane, first = find_sequence(p.starts, p.B, (int)t0);
       int64_t place = 0;
       int position = 0;
-      bool in = find_place(p, t, place, position);
+      bool in = lane < n_tokens && find_place(p, first, t, place, position);
       if (in && p.rows) {
         const int row = p.rows[t];
         in = row >= 0 && row < p.n_rows;
       }
-      places[threadIdx.x] = in ? place : -1;
-      ats[threadIdx.x] = position;
+      places[lane] = in ? place : -1;
+      ats[lane] = position;
     }
     __syncthreads();
   }
+#pragma unroll 1
   for (int i = threadIdx.x; i < n_tokens * p.pairs; i += kRopeThreads) {
-    const int jt = i / p.pairs, pair = i - jt * p.pairs;
-    rope_smem[i] = turn_of(p, (int)t0 + jt, pair, PAGED ? ats[jt] : 0);
+    const int jt = i / p.pairs, this_pair = i - jt * p.pairs;
+    if (this_pair != pair) {  // (where the pairs do not divide the threads)
+      pair = this_pair;
+      freq = p.freqs[pair];
+      turns_by = turns_per_position(freq);
+    }
+    rope_smem[i] = turn_of(p, (int)t0 + jt, pair, freq, turns_by, PAGED ? ats[jt] : 0);
   }
   __syncthreads();
 
   // cos and sin of this lane's pairs, times the weights: a' = a ca - b sb, b' = b cb + a sa
   float2 ca[2], cb[2], sa[2], sb[2];
-  auto coefficients = [&](int k) {
-    float2 wa[2], wb[2];
-    if (const uint16_t* w = k ? p.part[1].weight : p.part[0].weight; w && active) {
-      unpack<ADJ>(*reinterpret_cast<const uint2*>(w + at_a), *reinterpret_cast<const uint2*>(w + at_b), wa, wb);
-    } else {
+  int made = -1;  // token and part that they are for
+#pragma unroll 1
+  while (more) {
+    const int k = g >= groups0;
+    const bool norm = p.part[k].weight != nullptr, turn = p.part[k].turn;
+    if ((norm || turn) && made != 2 * j + k) {
+      made = 2 * j + k;
+      float2 wa[2], wb[2];
       wa[0] = wa[1] = wb[0] = wb[1] = make_float2(1.f, 1.f);
-    }
-    if (turns && (k ? p.part[1].turn : p.part[0].turn)) {
-      const float2* from = rope_smem + j * p.pairs + c * 4;
+      if (norm && active) {
+        const uint16_t* w = p.part[k].weight;
+        unpack<ADJ>(*reinterpret_cast<const uint2*>(w + at_a), *reinterpret_cast<const uint2*>(w + at_b), wa, wb);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 x = from[2 * i], y = from[2 * i + 1];
-        const float2 cos = make_float2(x.x, y.x), sin = make_float2(x.y, y.y);
-        ca[i] = __fmul2_rn(wa[i], cos);
-        cb[i] = __fmul2_rn(wb[i], cos);
-        sa[i] = __fmul2_rn(wa[i], sin);
-        sb[i] = __fmul2_rn(wb[i], make_float2(-sin.x, -sin.y));
+        ca[i] = wa[i], cb[i] = wb[i];
+        if (turns && turn) {
+          const float2 x = rope_smem[j * p.pairs + c * 4 + 2 * i], y = rope_smem[j * p.pairs + c * 4 + 2 * i + 1];
+          const float2 cos = make_float2(x.x, y.x), sin = make_float2(x.y, y.y);
+          ca[i] = __fmul2_rn(wa[i], cos);
+          cb[i] = __fmul2_rn(wb[i], cos);
+          sa[i] = __fmul2_rn(wa[i], sin);
+          sb[i] = __fmul2_rn(wb[i], make_float2(-sin.x, -sin.y));
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) ca[i] = wa[i], cb[i] = wb[i];
     }
-  };
-  // one group: the sum of a head's squares, then the head
-  auto squares = [&](const float2 (&a)[2], const float2 (&b)[2]) {
-    float2 s = __fmul2_rn(a[0], a[0]);
-    s = __ffma2_rn(a[1], a[1], s);
-    s = __ffma2_rn(b[0], b[0], s);
-    s = __ffma2_rn(b[1], b[1], s);
-    float ss = s.x + s.y;
+    if (norm || turn) {
+      float2 a[U][2], b[U][2];
 #pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    return ss;
-  };
-  int made = -1;  // token and part of the coefficients
-  while (more) {
-    const int64_t place = PAGED ? places[j] : 0;
-    if (!PAGED || place >= 0) {
-      uint16_t* d0 = p.part[0].dst + (PAGED ? place : (t0 + j) * p.part[0].ld_dst);
-      uint16_t* d1 = p.part[1].dst + (PAGED ? place : (t0 + j) * p.part[1].ld_dst);
+      for (int u = 0; u < U; ++u) unpack<ADJ>(va[u], vb[u], a[u], b[u]);
+      if (norm) {
+        float ss[U];
+        bool over = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float2 s = __fmul2_rn(a[u][0], a[u][0]);
+          s = __ffma2_rn(a[u][1], a[u][1], s);
+          s = __ffma2_rn(b[u][0], b[u][0], s);
+          s = __ffma2_rn(b[u][1], b[u][1], s);
+          ss[u] = s.x + s.y;
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], off);
+#pragma unroll
+        for (int u = 0; u < U; ++u) over |= !(ss[u] <= 3.4e38f);
+        float eps[U], f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) eps[u] = p.eps, f[u] = 1.f;
+        if (__any_sync(0xffffffffu, over)) {  // squares past fp32: those of 2^-70 of the head
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float s = small_squares<LPR>(a[u][0], a[u][1], b[u][0], b[u][1]);
+            if (!(ss[u] <= 3.4e38f)) ss[u] = s, eps[u] = 0.f, f[u] = 8.470329472543003e-22f;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float inv = rsqrtf(fmaf(ss[u], p.inv_d, eps[u]));
+          if (over) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              a[u][i] = make_float2(a[u][i].x * f[u], a[u][i].y * f[u]);
+              b[u][i] = make_float2(b[u][i].x * f[u], b[u][i].y * f[u]);
+            }
+          }
+          const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) a[u][i] = __fmul2_rn(a[u][i], inv2), b[u][i] = __fmul2_rn(b[u][i], inv2);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int gu = g + u * p.split;
-        const bool k = gu >= groups0;
-        if (gu >= groups) break;  // (the warp's)
-        const int head = (k ? gu - groups0 : gu) * RPW + sub;
-        const bool norm = (k ? p.part[1].weight : p.part[0].weight) != nullptr, turn = k ? p.part[1].turn : p.part[0].turn;
-        uint2 oa = va[u], ob = vb[u];
-        if (norm || turn) {
-          if (made != 2 * j + k) {
-            made = 2 * j + k;
-            coefficients(k);
-          }
-          float2 a[2], b[2];
-          unpack<ADJ>(oa, ob, a, b);
-          if (norm) {
-            float ss = squares(a, b), eps = p.eps;
-            const bool over = !(ss <= 3.4e38f);
-            if (__any_sync(0xffffffffu, over)) {  // squares past fp32: of a row 2^-70 of this one
-              const float f = over ? 8.470329472543003e-22f : 1.f;
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                a[i] = make_float2(a[i].x * f, a[i].y * f);
-                b[i] = make_float2(b[i].x * f, b[i].y * f);
-              }
-              const float s2 = squares(a, b);
-              if (over) ss = s2, eps = 0.f;
-            }
-            const float inv = rsqrtf(fmaf(ss, p.inv_d, eps));
-            const float2 inv2 = make_float2(inv, inv);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) a[i] = __fmul2_rn(a[i], inv2), b[i] = __fmul2_rn(b[i], inv2);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float2 x = __fmul2_rn(a[i], ca[i]), y = __fmul2_rn(b[i], cb[i]);
-            if (turns && turn) x = __ffma2_rn(b[i], sb[i], x), y = __ffma2_rn(a[i], sa[i], y);
-            a[i] = x, b[i] = y;
-          }
-          pack<ADJ>(a, b, oa, ob);
+        for (int i = 0; i < 2; ++i) {
+          float2 x = __fmul2_rn(a[u][i], ca[i]), y = __fmul2_rn(b[u][i], cb[i]);
+          if (turns && turn) x = __ffma2_rn(b[u][i], sb[i], x), y = __ffma2_rn(a[u][i], sa[i], y);
+          a[u][i] = x, b[u][i] = y;
         }
-        if (active && head < (k ? p.part[1].heads : p.part[0].heads)) {
-          uint16_t* to = (k ? d1 : d0) + head * (PAGED ? p.head_stride : (int64_t)p.d);
-          *reinterpret_cast<uint2*>(to + at_a) = oa;
-          *reinterpret_cast<uint2*>(to + at_b) = ob;
+        pack<ADJ>(a[u], b[u], va[u], vb[u]);
+      }
+    }
+    const int64_t place = PAGED ? places[j] : (t0 + j) * p.part[k].ld_dst;
+    if (!PAGED || place >= 0) {
+      const int left = heads_left(k), step = p.split * RPW;
+      const int64_t hs = PAGED ? p.head_stride : (int64_t)p.d;
+      uint16_t* to = p.part[k].dst + place + ((g - (k ? groups0 : 0)) * RPW + sub) * hs;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * step < left) {
+          if constexpr (ADJ) {
+            *reinterpret_cast<uint4*>(to + u * step * hs + at_a) = make_uint4(va[u].x, va[u].y, vb[u].x, vb[u].y);
+          } else {
+            *reinterpret_cast<uint2*>(to + u * step * hs + at_a) = va[u];
+            *reinterpret_cast<uint2*>(to + u * step * hs + at_b) = vb[u];
+          }
         }
       }
     }
+    // the next batch: of this part, the other, the next token
     g += U * p.split;
+    if (!k && g >= groups0) {  // this warp's first group of part 1
+      g = groups0 + (share + p.split - groups0 % p.split) % p.split;
+    }
     if (g >= groups) g = share, j += j_step;
-    more = j < n_tokens;
+    more = j < n_tokens && g < groups;
     if (more) fetch();
   }
 }

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import numpy as np
@@ -606,17 +607,10 @@ class PagedCache(NamedTuple):
     table: torch.Tensor
 
 
-class _RopeArgs(ctypes.Structure):
-    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64),
-                ("pairs", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
-                ("cyclic", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
-
-
-class _PagedArgs(ctypes.Structure):
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)] + [
-        (n, ctypes.c_int64) for n in ("page_stride", "position_stride", "head_stride")] + [
-        ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64)] + [
-        (n, ctypes.c_int32) for n in ("n_pages", "page", "width", "n_sequences", "n_kv_heads", "d")]
+# moe_rope and moe_paged as the C structures lie (packing bytes costs a small call a tenth of
+# filling a ctypes.Structure)
+_ROPE_ARGS = struct.Struct("@PPq8i")
+_PAGED_ARGS = struct.Struct("@PP3qPq6i")
 
 
 def rope_freqs(rotary: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -641,66 +635,94 @@ def tree_masks(parents) -> tuple[torch.Tensor, torch.Tensor]:
     return torch.tensor(signed, dtype=torch.int64), torch.tensor(depths, dtype=torch.int32)
 
 
-def _here(fn, *named):
-    """Refuses tensors that are not on the current device, whose stream the call goes to."""
-    dev = torch._C._cuda_getDevice()
-    for name, t in named:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, cuda:{dev} is the current device")
+def _refuse(fn, name, t, dtype, shape, dev):
+    """Why a tensor is not what a call on device `dev` reads."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, {dtype} {tuple(shape)} on the GPU is wanted")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    raise ValueError(f"{fn}: {name} is not contiguous")
 
 
-def _want_heads(fn, name, t, shape):
-    """The address of bf16 [tokens, heads, d] whose heads are contiguous, and its tokens' stride."""
-    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, "
-                         f"torch.bfloat16 {tuple(shape)} on the GPU is wanted")
-    (T, H, d), st = shape, t.stride()
-    if t.numel() and (st[2] != 1 or (H > 1 and st[1] != d)):
+def _heads(fn, name, t, T, H, d, dev):
+    """The address of bf16 [T, H, d] whose heads are contiguous, and its tokens' stride."""
+    shape = (T, H, d)
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(fn, name, t, torch.bfloat16, shape, dev)
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or s1 != d and H > 1) and T:
         raise ValueError(f"{fn}: {name} has scattered heads")
-    return t.data_ptr(), st[0] if T > 1 else H * d  # the stride of an axis of one entry says nothing
+    return t.data_ptr(), s0 if T > 1 else H * d  # the stride of an axis of one entry says nothing
 
 
-def _rope_args(fn, rope, positions, T):
+def _vector(fn, name, t, dtype, n, dev):
+    """The address of a contiguous vector; None of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(fn, name, t, dtype, (n,), dev)
+    return t.data_ptr()
+
+
+def _rows(fn, name, t, shape, dev):
+    """The address of int32 rows, and their stride."""
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or t.stride(1) != 1 and shape[1] > 1:
+        _refuse(fn, name, t, torch.int32, shape, dev)
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _current(fn, dev):
+    """The stream for tensors on `dev`, which has to be the current device."""
+    here = torch._C._cuda_getDevice()
+    if dev != here:
+        raise ValueError(f"{fn}: the tensors are on cuda:{dev}, cuda:{here} is the current device")
+    return torch._C._cuda_getCurrentRawStream(here)
+
+
+def _rope_args(fn, rope, positions, T, dev):
     """moe_rope of a rotation for T tokens (None: none)."""
     if rope is None:
         if positions is not None:
             raise ValueError(f"{fn}: positions without rope")
         return None
-    pairs = rope.freqs.numel()
-    sections = (pairs,) if rope.sections is None else tuple(rope.sections)
-    A = len(sections)
+    freqs, sections, cyclic, adjacent = rope
+    pairs = freqs.numel()
+    s = (pairs,) if sections is None else tuple(sections)
+    A = len(s)
     if not 1 <= A <= 4:
         raise ValueError(f"{fn}: {A} sections, 1 to 4 are wanted")
-    pf, pp, ld = _want(fn, "rope.freqs", rope.freqs, torch.float32, (pairs,)), None, 0
+    if any(not 0 <= n <= pairs for n in s):
+        raise ValueError(f"{fn}: sections {s}, each of 0 to {pairs} pairs, are wanted")
+    pf, pp, ld = _vector(fn, "rope.freqs", freqs, torch.float32, pairs, dev), 0, 0
     if positions is not None:
-        if positions.dim() == 1 and A == 1:
-            positions = positions[None]
-        pp = _want(fn, "positions", positions, torch.int32, (A, T), rows=True) if T else None
-        ld = positions.stride(0) if A > 1 else 0
-        _here(fn, ("positions", positions))
-    _here(fn, ("rope.freqs", rope.freqs))
-    return ctypes.byref(_RopeArgs(pf, pp, ld, pairs, A, (ctypes.c_int32 * 4)(*sections), rope.cyclic, rope.adjacent))
+        if A == 1 and positions.dim() == 1:
+            pp = _vector(fn, "positions", positions, torch.int32, T, dev)
+        else:
+            pp, ld = _rows(fn, "positions", positions, (A, T), dev)
+    return _ROPE_ARGS.pack(pf, pp, ld, pairs, A, *s, *(0, 0, 0)[:4 - A], bool(cyclic), bool(adjacent))
 
 
-def _paged_args(fn, cache, Hkv, d):
-    """moe_paged of a cache with heads of the sizes that the call's other tensors have."""
+def _paged_args(fn, cache, Hkv, d, dev):
+    """moe_paged of a cache with heads of the sizes that the call's other tensors have, and its
+    sequences."""
     k, v, table = cache
     if k.dim() != 4 or table.dim() != 2:
         raise ValueError(f"{fn}: k_pages {tuple(k.shape)} and table {tuple(table.shape)}: "
                          "[n_pages, page, Hkv, d] and [B, width] are wanted")
     n, page = k.shape[:2]
     shape, bf = (n, page, Hkv, d), torch.bfloat16
-    for name, t in (("k_pages", k), ("v_pages", v)):
-        if t.dtype != bf or t.shape != shape or not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, "
-                             f"{bf} {tuple(shape)} on the GPU is wanted")
+    if k.dtype is not bf or k.shape != shape or k.get_device() != dev:
+        _refuse(fn, "k_pages", k, bf, shape, dev)
+    if v.dtype is not bf or v.shape != shape or v.get_device() != dev:
+        _refuse(fn, "v_pages", v, bf, shape, dev)
     st, sv = k.stride(), v.stride()
-    if any(a != b and e > 1 for e, a, b in zip(shape, st, sv)) or st[3] != 1:
+    if st[3] != 1 or st != sv and any(a != b and e > 1 for e, a, b in zip(shape, st, sv)):
         raise ValueError(f"{fn}: k_pages and v_pages have different strides or scattered elements")
     B, width = table.shape
-    pt = _want(fn, "table", table, torch.int32, (B, width), rows=True)
-    _here(fn, ("k_pages", k), ("v_pages", v), ("table", table))
-    return _PagedArgs(k.data_ptr(), v.data_ptr(), *st[:3], pt, _ld(table), n, page, width, B, Hkv, d), B
+    pt, ld = _rows(fn, "table", table, (B, width), dev)
+    if max(n, page, width, B) > 0x7fffffff:
+        raise ValueError(f"{fn}: a cache of {n} pages and {B} x {width} entries is too large")
+    return _PAGED_ARGS.pack(k.data_ptr(), v.data_ptr(), *st[:3], pt, ld, n, page, width, B, Hkv, d), B
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: Rope | None = None,
@@ -715,30 +737,30 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: Rope | No
         return _on(stream, qk_norm_rope, q, k, rope, positions, q_weight, k_weight, eps, q_out, k_out)
     fn, bf = "qk_norm_rope", torch.bfloat16
     T, Hq, d = q.shape
+    dev = q.get_device()
     if rope is not None and positions is None:
         raise ValueError(f"{fn}: rope without positions")
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError(f"{fn}: k_weight or k_out without k")
-    pq, ldq = _want_heads(fn, "q", q, (T, Hq, d))
-    pk = pko = pwq = pwk = None
+    pq, ldq = _heads(fn, "q", q, T, Hq, d, dev)
+    pk = pko = None
     Hkv = ldk = ldko = 0
     if k is not None:
         Hkv = k.shape[1]
-        pk, ldk = _want_heads(fn, "k", k, (T, Hkv, d))
+        pk, ldk = _heads(fn, "k", k, T, Hkv, d, dev)
         if k_out is None:
             k_out = torch.empty((T, Hkv, d), dtype=bf, device=q.device)
-        pko, ldko = _want_heads(fn, "k_out", k_out, (T, Hkv, d))
+            pko, ldko = k_out.data_ptr(), Hkv * d
+        else:
+            pko, ldko = _heads(fn, "k_out", k_out, T, Hkv, d, dev)
     if q_out is None:
         q_out = torch.empty((T, Hq, d), dtype=bf, device=q.device)
-    pqo, ldqo = _want_heads(fn, "q_out", q_out, (T, Hq, d))
-    if q_weight is not None:
-        pwq = _want(fn, "q_weight", q_weight, bf, (d,))
-    if k_weight is not None:
-        pwk = _want(fn, "k_weight", k_weight, bf, (d,))
-    turn = _rope_args(fn, rope, positions, T)
-    _here(fn, ("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out), ("k_out", k_out))
-    rc = lib().moe_qk_norm_rope(pq, ldq, pk, ldk, T, Hq, Hkv, d, pwq, pwk, eps, turn, pqo, ldqo, pko, ldko,
-                                _stream())
+        pqo, ldqo = q_out.data_ptr(), Hq * d
+    else:
+        pqo, ldqo = _heads(fn, "q_out", q_out, T, Hq, d, dev)
+    rc = lib().moe_qk_norm_rope(pq, ldq, pk, ldk, T, Hq, Hkv, d, _vector(fn, "q_weight", q_weight, bf, d, dev),
+                                _vector(fn, "k_weight", k_weight, bf, d, dev), eps,
+                                _rope_args(fn, rope, positions, T, dev), pqo, ldqo, pko, ldko, _current(fn, dev))
     _check("moe_qk_norm_rope", rc)
     return q_out, k_out
 
@@ -757,17 +779,14 @@ def append_paged(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, starts: to
     fn, i32 = "append_paged", torch.int32
     M, Hkv, d = k.shape
     N = M if rows is None else rows.shape[0]
-    pk, ldk = _want_heads(fn, "k", k, (M, Hkv, d))
-    pv, ldv = _want_heads(fn, "v", v, (M, Hkv, d))
-    paged, B = _paged_args(fn, cache, Hkv, d)
-    ps = _want(fn, "starts", starts, i32, (B + 1,))
-    pl = _want(fn, "lens", lens, i32, (B,))
-    pw = None if k_weight is None else _want(fn, "k_weight", k_weight, torch.bfloat16, (d,))
-    pr = None if rows is None else _want(fn, "rows", rows, i32, (N,))
-    turn = _rope_args(fn, rope, positions, N)
-    _here(fn, ("k", k), ("v", v), ("starts", starts), ("lens", lens), ("k_weight", k_weight), ("rows", rows))
-    rc = lib().moe_append_paged(pk, ldk, pv, ldv, pr, M, N, ps, pl, ctypes.byref(paged), pw, eps, turn,
-                                _stream())
+    dev = k.get_device()
+    pk, ldk = _heads(fn, "k", k, M, Hkv, d, dev)
+    pv, ldv = _heads(fn, "v", v, M, Hkv, d, dev)
+    paged, B = _paged_args(fn, cache, Hkv, d, dev)
+    rc = lib().moe_append_paged(pk, ldk, pv, ldv, _vector(fn, "rows", rows, i32, N, dev), M, N,
+                                _vector(fn, "starts", starts, i32, B + 1, dev), _vector(fn, "lens", lens, i32, B, dev), paged,
+                                _vector(fn, "k_weight", k_weight, torch.bfloat16, d, dev), eps,
+                                _rope_args(fn, rope, positions, N, dev), _current(fn, dev))
     _check("moe_append_paged", rc)
 
 
@@ -784,26 +803,27 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, starts: torch.Tensor, len
         return _on(stream, tree_attention, q, cache, starts, lens, tree, scale, out, ws)
     fn, bf, i32 = "tree_attention", torch.bfloat16, torch.int32
     N, Hq, d = q.shape
-    Hkv = cache.k_pages.shape[2] if cache.k_pages.dim() == 4 else 0
-    pq, ldq = _want_heads(fn, "q", q, (N, Hq, d))
-    paged, B = _paged_args(fn, cache, Hkv, d)
-    ps = _want(fn, "starts", starts, i32, (B + 1,))
-    pl = _want(fn, "lens", lens, i32, (B,))
-    pt = None if tree is None else _want(fn, "tree", tree, torch.int64, (N,))
+    dev, pages = q.get_device(), cache.k_pages
+    pq, ldq = _heads(fn, "q", q, N, Hq, d, dev)
+    paged, B = _paged_args(fn, cache, pages.shape[2] if pages.dim() == 4 else 0, d, dev)
+    ps, pl = _vector(fn, "starts", starts, i32, B + 1, dev), _vector(fn, "lens", lens, i32, B, dev)
+    pt = _vector(fn, "tree", tree, torch.int64, N, dev)
     if out is None:
         out = torch.empty((N, Hq, d), dtype=bf, device=q.device)
         po = out.data_ptr()
     else:
         po = _want(fn, "out", out, bf, (N, Hq, d))
-    ref = ctypes.byref(paged)
     if ws is None:
-        nbytes = lib().moe_tree_attention_workspace_bytes(N, Hq, ref)
+        nbytes = lib().moe_tree_attention_workspace_bytes(N, Hq, paged)
         if nbytes == 0:
             raise MoeError("moe_tree_attention_workspace_bytes", -3)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    pws, nbytes = _want_ws(fn, ws)
-    _here(fn, ("q", q), ("starts", starts), ("lens", lens), ("tree", tree), ("out", out), ("ws", ws))
-    rc = lib().moe_tree_attention(pq, ldq, N, Hq, ps, pl, pt, ref, scale, po, pws, nbytes, _stream())
+        pws = ws.data_ptr()
+    else:
+        pws, nbytes = _want_ws(fn, ws)
+    if out.get_device() != dev or ws.get_device() != dev:
+        raise ValueError(f"{fn}: out or ws is on another device than q")
+    rc = lib().moe_tree_attention(pq, ldq, N, Hq, ps, pl, pt, paged, scale, po, pws, nbytes, _current(fn, dev))
     _check("moe_tree_attention", rc)
     return out
 

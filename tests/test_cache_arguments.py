@@ -26,12 +26,12 @@ def L():
 def rope(freqs=A, positions=A, ld=1 << 20, pairs=32, axes=1, sections=None, cyclic=0, adjacent=0):
     from bit_moe_expert_route_gb300 import ops
     s = list(sections or (pairs,))
-    return ctypes.byref(ops._RopeArgs(freqs, positions, ld, pairs, axes, (ctypes.c_int32 * 4)(*(s + [0] * 4)[:4]), cyclic, adjacent))
+    return ops._ROPE_ARGS.pack(freqs or 0, positions or 0, ld, pairs, axes, *(s + [0] * 4)[:4], cyclic, adjacent)
 
 
 def cache(k=A, v=A, ps=16 * 2 * 128, os=2 * 128, hs=128, table=A, ld=10, n=50, page=16, width=10, B=3, H=2, d=128):
     from bit_moe_expert_route_gb300 import ops
-    return ctypes.byref(ops._PagedArgs(k, v, ps, os, hs, table, ld, n, page, width, B, H, d))
+    return ops._PAGED_ARGS.pack(k or 0, v or 0, ps, os, hs, table or 0, ld, n, page, width, B, H, d)
 
 
 def norm(L, q=A, ldq=2048, k=A, ldk=256, T=10, Hq=16, Hkv=2, d=128, wq=A, wk=A, eps=1e-6, r="one", qo=A, ldqo=2048, ko=A, ldko=256):
@@ -222,7 +222,7 @@ def test_the_binding_refuses():
     refused("starts", a, k, k, c, starts[:1], lens)
     refused("lens", a, k, k, c, starts, starts)
     refused("rows", a, k, k, c, starts, lens, rows=at.long())
-    refused("q is", t, q[:, :, :32].contiguous().view(3, 4, 32).half(), c, starts, lens)
+    refused("q is", t, q.half(), c, starts, lens)
     refused("k_pages is", t, torch.zeros(3, 4, 128, **bf), c, starts, lens)
     refused("tree", t, q, c, starts, lens, at)
     refused("out", t, q, c, starts, lens, out=q.float())
@@ -235,15 +235,49 @@ def test_the_binding_refuses():
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
-    """What is on another device than the current one, whose stream the call would go to."""
+    """What is on another device than the call's other tensors, or than the current one, whose stream the
+    call would go to."""
     from bit_moe_expert_route_gb300 import ops
 
     class Elsewhere:
-        device = "cuda:1"
+        device, dtype, shape, is_cuda = "cuda:1", torch.int32, (3,), True
 
         def get_device(self):
             return 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 64
+    assert ops._vector("f", "x", Elsewhere(), torch.int32, 3, 1) == 64
+    with pytest.raises(ValueError, match="f: x is on cuda:1, the call's other tensors on cuda:0"):
+        ops._vector("f", "x", Elsewhere(), torch.int32, 3, 0)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    ops._here("f", ("none", None))
-    with pytest.raises(ValueError, match="f: x is on cuda:1, cuda:0 is the current device"):
-        ops._here("f", ("x", Elsewhere()))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 7, raising=False)
+    assert ops._current("f", 0) == 7
+    with pytest.raises(ValueError, match="f: the tensors are on cuda:1, cuda:0 is the current device"):
+        ops._current("f", 1)
+
+
+def test_the_structures_are_the_headers():
+    """What the binding packs lies as a C compiler lays the header's structures out."""
+    import os
+    import subprocess
+    import tempfile
+    from bit_moe_expert_route_gb300 import ops
+    from bit_moe_expert_route_gb300 import build as B
+    src = r"""#include <stdio.h>
+#include <stddef.h>
+#include "cache.h"
+int main() {
+  printf("%zu %zu %zu %zu %zu\n", sizeof(moe_rope_t), offsetof(moe_rope_t, ld_positions), offsetof(moe_rope_t, pairs), offsetof(moe_rope_t, sections), offsetof(moe_rope_t, adjacent));
+  printf("%zu %zu %zu %zu\n", sizeof(moe_paged_t), offsetof(moe_paged_t, page_stride), offsetof(moe_paged_t, table), offsetof(moe_paged_t, n_pages));
+}
+"""
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "s.c"), os.path.join(d, "s")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-I", B.INCLUDE, c, "-o", exe], check=True)
+        out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(x) for x in out] == [ops._ROPE_ARGS.size, 16, 24, 32, 52, ops._PAGED_ARGS.size, 16, 40, 56]

@@ -62,9 +62,8 @@ def paged(lens, news, Hq, Hkv, d, page, seed=0, tree=True, order="places", **mor
 def call(P, q, tree, **more):
     """The output, from a workspace of 0xFF, with its status checked."""
     from bit_moe_expert_route_gb300 import ops
-    import ctypes
-    args = ops._paged_args("test", P.cache, P.Hkv, P.d)[0]
-    ws = torch.full((ops.lib().moe_tree_attention_workspace_bytes(q.shape[0], q.shape[1], ctypes.byref(args)),), 255,
+    args = ops._paged_args("test", P.cache, P.Hkv, P.d, 0)[0]
+    ws = torch.full((ops.lib().moe_tree_attention_workspace_bytes(q.shape[0], q.shape[1], args),), 255,
                     dtype=torch.uint8, device="cuda")
     out = ops.tree_attention(q, P.cache, P.starts, P.lens, tree, ws=ws, **more)
     assert ops.device_status(ws) == 0
