@@ -69,6 +69,9 @@ struct TrCfg {
   static constexpr int kColS = D;                   // tensor memory: O, then the score buffers
   static_assert(kColS + kBufs * KT <= 512, "tensor memory exceeded");
   static_assert(kSmem <= 232448, "shared memory exceeded");
+  // V of tile i takes the slot that load 2 i + 2 - kSlots had: that has to be one whose landing the outputs' issuer
+  // knows of (K of tile i - 1 or an earlier load), or its wait for V would take the phase before for this one.
+  static_assert(kSlots >= 4, "a wait may be two phases ahead of its barrier");
   static_assert(kSlots < kBadRing, "a tile's note is overwritten before it is read");
 };
 
@@ -457,8 +460,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     }
   } else if (warp == 0) {
     fence_proxy_async_global();  // the pages are written by ordinary stores of earlier launches
-    // keys that one CTA alone reads leave L2 first
-    const uint64_t policy = p.rows < kTreeRows ? l2_policy_evict_first() : l2_policy_evict_normal();
+    // Keys leave L2 first: they are read once, or by the next CTAs at about the same time (8 sequences of 16
+    // tokens over 32768 positions 77 us, without a policy 84; 4 of 64 over 50001, four row tiles, 153 and 155).
+    const uint64_t policy = l2_policy_evict_first();
     const int pieces_log2 = (KT == 64 ? 6 : 7) - args.box_log2, pieces = 1 << pieces_log2;
     // a lane's box of each tile: 64 columns, one page's (or the tile's) positions
     const int piece = lane & (pieces - 1), col = lane >> pieces_log2;
@@ -694,7 +698,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           uint8_t* v = smem + C::kOffSlots + (at % NS) * C::kSlot;
           const int first = (int)max((int64_t)0, -rel), none = (int)min((int64_t)KT, g.n - rel);
           bool odd = false;
-#pragma unroll 1
+#pragma unroll 4
           for (int j = first * (D / 8) + tid; j < KT * (D / 8); j += 128) {
             const int row = j / (D / 8), c = j % (D / 8);
             uint4* w = reinterpret_cast<uint4*>(v + (c / 8) * (KT * 128) + sw128_offset(row, c % 8));
@@ -747,58 +751,47 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       const int64_t state = ((int64_t)blockIdx.x * kTreeParts + part) * p.rows;  // of the tile's first row
       if (mine && !g.whole) p.part_ml[state + r] = make_float2(m, l);
       if (warp_rows && !poison && *v_bad == seg + 1) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
-      // A quad of lanes holds 8 columns of a row at a time; lanes exchange until each has 16 bytes that lie
-      // together, so that a store is 64 bytes of each of 8 rows. (A row a lane: 16 bytes of each of 32 rows,
-      // 5 us for 128 rows of 256.)
+      // A quad of lanes holds 8 columns of a row at a time: stores are whole sectors of 8 rows. (A row a
+      // lane: 16 bytes of each of 32 rows, 5 us for 128 rows of 256.)
       const float inv = l == 0.f ? 0.f : g.whole ? 1.f / l : 1.f;  // nothing attended to: zeros
       const int q = lane & 3;
 #pragma unroll 1
       for (int half = 0; half < 32 && quarter * 32 + half < g.rows; half += 16) {
         float f[2];
-        uint8_t* dst[2];  // of the two rows that this lane stores parts of; null past the end
+        uint8_t* dst[2];  // of the two rows that this lane has parts of; null past the end
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int in = half + 8 * k + (lane >> 2), row = quarter * 32 + in;
           f[k] = __shfl_sync(0xffffffffu, inv, in);
           const int y = g.row0 + row, i = (int)(y * per_group >> 16);
           dst[k] = row >= g.rows ? nullptr
-                   : g.whole ? reinterpret_cast<uint8_t*>(p.out + ((int64_t)(g.tok0 + i) * p.Hq + g.h * G + y - i * G) * D) + q * 16
-                             : reinterpret_cast<uint8_t*>(p.part_o + (state + row) * D) + (8 * (q & 1) + 2 * (q & 2)) * 4;
+                   : g.whole ? reinterpret_cast<uint8_t*>(p.out + ((int64_t)(g.tok0 + i) * p.Hq + g.h * G + y - i * G) * D) + (8 * (q & 1) + 2 * (q & 2)) * 2
+                             : reinterpret_cast<uint8_t*>(p.part_o + (state + row) * D) + 2 * q * 4;
         }
         const uint32_t from = tmem + ((uint32_t)(quarter * 32 + half) << 16);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t o[2][16];  // two loads in flight
-          tmem_ld_16x256b_x4(from + c, o[0]);
-          tmem_ld_16x256b_x4(from + c + 32, o[1]);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[16];
+          tmem_ld_16x256b_x4(from + c, o);
           tc_wait_ld();
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int k = z & 1, c32 = c + 32 * (z >> 1);
+          for (int k = 0; k < 2; ++k) {
             float2 v[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              v[b] = make_float2(__uint_as_float(o[z >> 1][4 * b + 2 * k]) * f[k], __uint_as_float(o[z >> 1][4 * b + 2 * k + 1]) * f[k]);
-              if (f[k] == 0.f) v[b] = make_float2(0.f, 0.f);
+              v[b] = make_float2(__uint_as_float(o[4 * b + 2 * k]), __uint_as_float(o[4 * b + 2 * k + 1]));
+              v[b] = f[k] == 0.f ? make_float2(0.f, 0.f) : __fmul2_rn(v[b], make_float2(f[k], f[k]));
             }
-            if (g.whole) {
-              uint32_t w[4];
-#pragma unroll
-              for (int b = 0; b < 4; ++b) w[b] = pack_bf16(v[b].x, v[b].y);
-              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, q & 1 ? w[0] : w[1], 1);
-              const uint32_t r1 = __shfl_xor_sync(0xffffffffu, q & 1 ? w[2] : w[3], 1);
-              const uint32_t a0 = q & 1 ? r0 : w[0], a1 = q & 1 ? w[1] : r0, b0 = q & 1 ? r1 : w[2], b1 = q & 1 ? w[3] : r1;
-              const uint32_t s0 = __shfl_xor_sync(0xffffffffu, q & 2 ? a0 : b0, 2);
-              const uint32_t s1 = __shfl_xor_sync(0xffffffffu, q & 2 ? a1 : b1, 2);
-              if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + c32 * 2) = q & 2 ? make_uint4(s0, s1, b0, b1) : make_uint4(a0, a1, s0, s1);
-            } else {
+            if (g.whole) {  // lanes exchange with their neighbours: 8 bytes of one of two blocks
 #pragma unroll
               for (int b = 0; b < 4; b += 2) {
-                const float2 send = q & 1 ? v[b] : v[b + 1], keep = q & 1 ? v[b + 1] : v[b];
-                const float e0 = __shfl_xor_sync(0xffffffffu, send.x, 1), e1 = __shfl_xor_sync(0xffffffffu, send.y, 1);
-                if (dst[k])
-                  *reinterpret_cast<float4*>(dst[k] + (c32 + 8 * b) * 4) = q & 1 ? make_float4(e0, e1, keep.x, keep.y) : make_float4(keep.x, keep.y, e0, e1);
+                const uint32_t w0 = pack_bf16(v[b].x, v[b].y), w1 = pack_bf16(v[b + 1].x, v[b + 1].y);
+                const uint32_t x = __shfl_xor_sync(0xffffffffu, q & 1 ? w0 : w1, 1);
+                if (dst[k]) *reinterpret_cast<uint2*>(dst[k] + (c + 8 * b) * 2) = q & 1 ? make_uint2(x, w1) : make_uint2(w0, x);
               }
+            } else if (dst[k]) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) *reinterpret_cast<float2*>(dst[k] + (c + 8 * b) * 4) = v[b];
             }
           }
         }

@@ -687,42 +687,43 @@ def _rope_args(fn, rope, positions, T, dev):
         return None
     freqs, sections, cyclic, adjacent = rope
     pairs = freqs.numel()
-    s = (pairs,) if sections is None else tuple(sections)
-    A = len(s)
+    A = 1 if sections is None else len(sections)
     if not 1 <= A <= 4:
         raise ValueError(f"{fn}: {A} sections, 1 to 4 are wanted")
-    if any(not 0 <= n <= pairs for n in s):
-        raise ValueError(f"{fn}: sections {s}, each of 0 to {pairs} pairs, are wanted")
-    pf, pp, ld = _vector(fn, "rope.freqs", freqs, torch.float32, pairs, dev), 0, 0
+    s = (pairs, 0, 0, 0) if sections is None else (*sections, 0, 0, 0)[:4]
+    if min(s) < 0 or max(s) > pairs:
+        raise ValueError(f"{fn}: sections {sections}, each of 0 to {pairs} pairs, are wanted")
+    pp = ld = 0
     if positions is not None:
         if A == 1 and positions.dim() == 1:
             pp = _vector(fn, "positions", positions, torch.int32, T, dev)
         else:
             pp, ld = _rows(fn, "positions", positions, (A, T), dev)
-    return _ROPE_ARGS.pack(pf, pp, ld, pairs, A, *s, *(0, 0, 0)[:4 - A], bool(cyclic), bool(adjacent))
+    return _ROPE_ARGS.pack(_vector(fn, "rope.freqs", freqs, torch.float32, pairs, dev), pp, ld, pairs, A, *s,
+                           bool(cyclic), bool(adjacent))
 
 
 def _paged_args(fn, cache, Hkv, d, dev):
     """moe_paged of a cache with heads of the sizes that the call's other tensors have, and its
     sequences."""
     k, v, table = cache
-    if k.dim() != 4 or table.dim() != 2:
-        raise ValueError(f"{fn}: k_pages {tuple(k.shape)} and table {tuple(table.shape)}: "
+    shape, size = k.shape, table.shape
+    if len(shape) != 4 or len(size) != 2:
+        raise ValueError(f"{fn}: k_pages {tuple(shape)} and table {tuple(size)}: "
                          "[n_pages, page, Hkv, d] and [B, width] are wanted")
-    n, page = k.shape[:2]
-    shape, bf = (n, page, Hkv, d), torch.bfloat16
-    if k.dtype is not bf or k.shape != shape or k.get_device() != dev:
-        _refuse(fn, "k_pages", k, bf, shape, dev)
-    if v.dtype is not bf or v.shape != shape or v.get_device() != dev:
+    (n, page, heads, width), bf = shape, torch.bfloat16
+    if heads != Hkv or width != d or k.dtype is not bf or k.get_device() != dev:
+        _refuse(fn, "k_pages", k, bf, (n, page, Hkv, d), dev)
+    if v.shape != shape or v.dtype is not bf or v.get_device() != dev:
         _refuse(fn, "v_pages", v, bf, shape, dev)
     st, sv = k.stride(), v.stride()
     if st[3] != 1 or st != sv and any(a != b and e > 1 for e, a, b in zip(shape, st, sv)):
         raise ValueError(f"{fn}: k_pages and v_pages have different strides or scattered elements")
-    B, width = table.shape
-    pt, ld = _rows(fn, "table", table, (B, width), dev)
+    pt, ld = _rows(fn, "table", table, size, dev)
+    B, width = size
     if max(n, page, width, B) > 0x7fffffff:
         raise ValueError(f"{fn}: a cache of {n} pages and {B} x {width} entries is too large")
-    return _PAGED_ARGS.pack(k.data_ptr(), v.data_ptr(), *st[:3], pt, ld, n, page, width, B, Hkv, d), B
+    return _PAGED_ARGS.pack(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], pt, ld, n, page, width, B, Hkv, d), B
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: Rope | None = None,
