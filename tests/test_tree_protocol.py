@@ -41,15 +41,23 @@ def run(NS, segments, seed, skip=None):
     slot, cols = [None] * NS, [None] * NB  # what a slot holds; a buffer's scores or weights
     queries, output = [None] * W, None       # the segment whose queries each warp has written, whose outputs there are
     state = dict(load=0, qk=0, pv=0)
-    done_pv, mended = -1, set()
+    done_pv, mended, coming = -1, set(), []
 
     def load():
         at = state["load"]
         if at >= 2 * T or (at >= NS and not empty[at % NS].test(at // NS - 1)):
             return False
+        slot[at % NS] = None
+        coming.append(at)
+        state["load"] += 1
+        return True
+
+    def land():  # copies end in any order
+        if not coming:
+            return False
+        at = coming.pop(rng.randrange(len(coming)))
         slot[at % NS] = order[at]
         full[at % NS].arrive(at // NS)
-        state["load"] += 1
         return True
 
     def qk():
@@ -147,7 +155,7 @@ def run(NS, segments, seed, skip=None):
             w["step"] = "queries"
         return True
 
-    roles, idle = [load, qk, pv] + [lambda n=n: soft(n) for n in range(W)], 0
+    roles, idle = [load, land, qk, pv] + [lambda n=n: soft(n) for n in range(W)], 0
     while any(w["i"] < T for w in warps):
         idle = 0 if rng.choice(roles)() else idle + 1
         assert idle < 20000, f"no role can move: {state} {warps}"
