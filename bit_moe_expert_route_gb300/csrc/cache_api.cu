@@ -34,7 +34,7 @@ int enter_rope(moe::RopeParams& p, const moe_rope_t* rope, int tokens, bool plac
   }
   if (sum != r.pairs) return MOE_ERR_SHAPE;
   if (!r.positions && placed && r.n_axes != 1) return MOE_ERR_SHAPE;
-  if (r.positions && r.n_axes > 1 && r.ld_positions < tokens) return MOE_ERR_SHAPE;
+  if (r.positions && r.n_axes > 1 && r.ld_positions < 0) return MOE_ERR_SHAPE;
   if (tokens > 0) {
     if (!r.freqs || (!r.positions && !placed)) return MOE_ERR_NULL;
     if (!aligned(r.freqs, 4) || !aligned(r.positions, 4)) return MOE_ERR_ALIGN;

@@ -5,11 +5,16 @@
 //
 // A block takes a few tokens. Their places in the cache (a lane a token) and their sines and
 // cosines (a thread a pair) are made once and kept in shared memory; then one warp or several take a
-// token's heads, four loads of heads at a time. A lane holds 8 elements of a head, four pairs
+// token's heads, two loads of heads at a time. A lane holds 8 elements of a head, four pairs
 // (a, b) where it turns: (a0 a1 a2 a3 | b0 b1 b2 b3) from two places, or (a0 b0 a1 b1 | ...), so
 // that no pair is spread over lanes; a head takes d / 8 lanes (rounded up to 8, 16 or 32), a warp's
 // load 1, 2 or 4 whole heads. The weights go into the sines and cosines once a token. Loads of heads do not
-// wait for angles or places. Bound by HBM for many tokens, by one chain of load - sum - store for few.
+// wait for angles or places.
+//
+// Few tokens: one chain of load - sum - store, 2.5 us. 32768 tokens of 16 + 2 heads of 256: 112 us,
+// 79% of the measured copy; the same without arithmetic 96 us. About 160 instructions a head fill two
+// thirds of the issue slots. (Two loads a warp and 32 warps an SM; four and 24 warps 115 us, six 125. Warps
+// that go from token to token by themselves 119 to 128.)
 //
 // Angles: a frequency is held as the part of a whole turn that one position makes, in
 // 64 bits with the point in front (freq / 2 pi mod 1); times the position, mod 2^64,
@@ -187,6 +192,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
   // A batch: U groups of one part's heads of one token, from group g on. The groups of both
   // parts are counted on, part 1's from `groups0`.
   const int groups0 = (p.part[0].heads + RPW - 1) / RPW, groups = groups0 + (p.part[1].heads + RPW - 1) / RPW;
+  const int g1 = groups0 + (share + p.split - groups0 % p.split) % p.split;  // this warp's first group of part 1
   int g = share;
   bool more = j < n_tokens && g < groups;
   uint2 va[U], vb[U];
@@ -219,10 +225,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
   for (int u = 0; u < U; ++u) va[u] = vb[u] = make_uint2(0, 0);
   if (more) fetch();
 
-  // this thread's first pair
-  int pair = p.pairs > 0 ? threadIdx.x % p.pairs : 0;
-  float freq = p.pairs > 0 ? p.freqs[pair] : 0.f;
-  uint64_t turns_by = turns_per_position(freq);
+  // this thread's first pair (beside the search for places; without one it only takes registers: 32768 tokens 119
+  // us instead of 115)
+  const bool early = PAGED && p.pairs > 0;
+  int pair = early ? threadIdx.x % p.pairs : -1;
+  float freq = early ? p.freqs[pair] : 0.f;
+  uint64_t turns_by = early ? turns_per_position(freq) : 0;
   if constexpr (PAGED) {
     if (warp == 0) {
       const int t = (int)t0 + lane, first = find_sequence(p.starts, p.B, (int)t0);
@@ -354,9 +362,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     }
     // the next batch: of this part, the other, the next token
     g += U * p.split;
-    if (!k && g >= groups0) {  // this warp's first group of part 1
-      g = groups0 + (share + p.split - groups0 % p.split) % p.split;
-    }
+    if (!k && g >= groups0) g = g1;
     if (g >= groups) g = share, j += j_step;
     more = j < n_tokens && g < groups;
     if (more) fetch();

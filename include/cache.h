@@ -30,7 +30,8 @@ extern "C" {
  * elements from 2 pairs on stay. Angles are reduced in whole numbers, so that
  * cos and sin are exact to fp32 (2^-22) at every int32 position.
  *   freqs         fp32 [pairs] device, finite and below 2^16 in magnitude
- *   positions     int32 [n_axes][tokens] device, axes ld_positions elements apart
+ *   positions     int32 [n_axes][tokens] device, axes ld_positions elements apart (0: all
+ *                 axes have the same)
  *   pairs         0 (no rotation) .. d / 2; a multiple of 8, of 4 if adjacent
  *   n_axes        1 .. 4
  *   sections      pairs of each axis, pairs in all: axis 0's come first, then axis
@@ -61,9 +62,9 @@ typedef struct moe_rope {
  * All pointers but freqs and positions (4 bytes) 16-byte aligned, strides multiples
  * of 8 elements and at least n_heads * d; d a multiple of 8, 8 <= d <= 256; T >= 0 (0
  * launches nothing), T * heads < 2^31; eps > 0 and finite. fp32 arithmetic; a row
- * whose squares pass the fp32 range has its norm all the same. An element that is
- * infinite or NaN makes its pair NaN, and with a norm its row what 1 / sqrt(inf) = 0
- * gives (finite elements 0). One launch.
+ * whose squares pass the fp32 range has its norm all the same. With a norm, a row with
+ * an infinity has zeros for its finite elements and NaN for the infinite ones, before
+ * it is turned; a row with a NaN is NaN. One launch.
  */
 int moe_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, int T,
                      int n_q_heads, int n_kv_heads, int d, const uint16_t* q_weight,

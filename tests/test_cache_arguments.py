@@ -53,11 +53,11 @@ def test_norm_and_rotation(L):
         assert norm(L, **bad) == ALIGN, bad
     for bad in (dict(pairs=-8), dict(pairs=68), dict(pairs=72), dict(pairs=20), dict(pairs=10, adjacent=1), dict(axes=0), dict(axes=5),
                 dict(axes=3, sections=(10, 10, 10)), dict(axes=2, sections=(-8, 40)), dict(axes=2, sections=(40, -8)),
-                dict(axes=3, sections=(8, 12, 12), cyclic=1), dict(axes=3, sections=(16, 8, 8), ld=9),
+                dict(axes=3, sections=(8, 12, 12), cyclic=1), dict(axes=3, sections=(16, 8, 8), ld=-1),
                 dict(axes=2, sections=((1 << 31) - 1, 33))):
         assert norm(L, r=rope(**bad)) == SHAPE, bad
     for good in (dict(pairs=0), dict(pairs=64), dict(pairs=12, adjacent=1), dict(axes=3, sections=(12, 10, 10), cyclic=1),
-                 dict(axes=4, sections=(0, 0, 32, 0)), dict(axes=3, sections=(16, 8, 8), ld=10)):
+                 dict(axes=4, sections=(0, 0, 32, 0)), dict(axes=3, sections=(16, 8, 8), ld=0)):
         assert norm(L, r=rope(**good)) == 0, good
     assert norm(L, r=rope(freqs=None)) == NULL and norm(L, r=rope(positions=None)) == NULL
     assert norm(L, r=rope(freqs=A + 2)) == ALIGN and norm(L, r=rope(positions=A + 1)) == ALIGN

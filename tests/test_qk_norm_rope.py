@@ -94,6 +94,20 @@ def test_parts_alone(d):
 
 
 @gpu
+def test_one_position_for_all_axes():
+    """Positions of three axes that are one row of memory (text among patches), or a slice of a wider tensor."""
+    from bit_moe_expert_route_gb300 import ops
+    (q, k), (wq, wk), g = inputs(50, 8, 2, 128, 4)
+    rope, at = ops.Rope(ops.rope_freqs(128), (16, 24, 24)), torch.arange(50, dtype=torch.int32, device="cuda")
+    a = ops.qk_norm_rope(q, k, rope, at.expand(3, 50), wq, wk)
+    wide = torch.zeros(3, 70, dtype=torch.int32, device="cuda")
+    wide[:, 5:55] = at
+    b = ops.qk_norm_rope(q, k, rope, wide[:, 5:55], wq, wk)
+    c = ops.qk_norm_rope(q, k, ops.Rope(rope.freqs), at, wq, wk)
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+
+
+@gpu
 def test_in_place_and_into_views():
     from bit_moe_expert_route_gb300 import ops
     (q, k), (wq, wk), g = inputs(300, 16, 2, 128, 1)
