@@ -192,7 +192,8 @@ int moe_tree_attention(const uint16_t* q, int64_t ldq, int N, int n_q_heads,
   moe_paged_t c;
   if (const int rc = check_cache(cache, c, kMaxPositions); rc != MOE_OK) return rc;
   if (!tree_shape_supported(N, n_q_heads, c) || !stride_ok(ldq, (int64_t)n_q_heads * c.d)) return MOE_ERR_SHAPE;
-  if (std::isnan(scale) || std::isinf(scale)) return MOE_ERR_SHAPE;
+  const float scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf((float)c.d)) * 1.4426950408889634f;
+  if (!std::isfinite(scale) || !std::isfinite(scale_log2)) return MOE_ERR_SHAPE;
   if (N == 0) return MOE_OK;
   if (const int rc = check_cache_pointers(c); rc != MOE_OK) return rc;
   if (!q || !out || !starts || !lens) return MOE_ERR_NULL;
@@ -222,7 +223,7 @@ int moe_tree_attention(const uint16_t* q, int64_t ldq, int N, int n_q_heads,
   p.width = c.width;
   p.n_pages = c.n_pages;
   p.page_log2 = log2_of(c.page);
-  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf((float)c.d)) * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.out = out;
   p.ctas = std::min(sms, moe::kTreeMaxSms);
   tree_carve(p, ws, moe::kTreeMaxSms);

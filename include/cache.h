@@ -80,6 +80,8 @@ int moe_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t 
  *   table             int32 [n_sequences][width] device, rows ld_table apart; entries
  *                     that no position needs are not read
  *   page              a power of two, 8 .. 4096
+ * n_pages >= 1, 1 <= n_sequences <= 65535, 1 <= n_kv_heads <= 1024, width >= 1, width * page
+ * <= 2^28; no two places share an element, of K and of V neither
  */
 typedef struct moe_paged {
   uint16_t *k_pages, *v_pages;
@@ -124,7 +126,7 @@ int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t 
  *   o_{t,h} = sum_j softmax_j(scale * q_{t,h} . k_{g,j}) v_{g,j},  g = h / (n_q_heads / n_kv_heads)
  *   q      bf16 [N][n_q_heads][d], tokens ldq elements apart (ldq a multiple of 8)
  *   tree   int64 [N] device, 8-byte aligned, or NULL
- *   scale  multiplies every score; <= 0 means 1 / sqrt(d)
+ *   scale  multiplies every score, finite and below 2^127; <= 0 means 1 / sqrt(d)
  *   out    bf16 [N][n_q_heads][d]. Tokens of no sequence are left as they were. Zeros for a
  *          row that attends to nothing or whose every score is -infinity. NaN for a row
  *          with a score that is NaN or +infinity, and for all rows of a sequence with more
@@ -134,8 +136,8 @@ int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t 
  *   ws     256-byte aligned, >= moe_tree_attention_workspace_bytes (no initialisation
  *          needed), holds the status word; where the status says MOE_DEV_TIMEOUT, the rows
  *          not computed are NaN
- * 0 <= N < 2^24 (0 launches nothing), 1 <= n_sequences <= 65535, width * page <= 2^28
- * and below 2^34 / n_kv_heads, d in {64, 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a KV head.
+ * out and ws overlap nothing else. Sequences may share pages. 0 <= N < 2^24 (0 launches nothing), width * page
+ * below 2^34 / n_kv_heads, d in {64, 128, 256}, n_q_heads a multiple of n_kv_heads with at most 16 query heads a KV head.
  * Scores and softmax in fp32; the softmax weights multiply the values as two bf16 parts
  * (2^-16 of each weight), with fp32 sums. Two launches: partial states over slices of the
  * sequences, cut evenly over the SMs whatever their lengths, then their merge in a fixed

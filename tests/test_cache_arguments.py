@@ -118,7 +118,7 @@ def test_attention(L):
             assert tree(L, c=cache(**dict(c, **order)), ldq=16 * d) == 0
     assert tree(L, N=0, q=None, out=None, starts=None, lens=None, ws=None) == 0 and tree(L, bits=None) == 0
     for bad in (dict(N=-1), dict(N=1 << 24), dict(Hq=15), dict(Hq=1), dict(Hq=34, ldq=1 << 14), dict(ldq=2040), dict(ldq=2052),
-                dict(scale=float("nan")), dict(scale=float("inf"))):
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38)):
         assert tree(L, **bad, n=1 << 30) == SHAPE, bad
     for bad in BAD_CACHES + [dict(d=96, hs=96, os=192, ps=16 * 192)]:
         assert tree(L, c=cache(**bad), n=1 << 30) == SHAPE and L.moe_tree_attention_workspace_bytes(10, 16, cache(**bad)) == 0, bad

@@ -98,10 +98,10 @@ def test_matches_64_bits(lens, news, Hq, Hkv, d, page, tree):
 @pytest.mark.parametrize("page", [8, 64, 256])
 def test_layouts_and_scale(d, order, page):
     """Positions inside heads; K and V side by side; queries out of a wider buffer."""
-    P, q, tree = paged([300, 40, 1000], [7, 1, 30], 12, 3, d, page, d, True, order)
+    P, q, tree = paged([300, 40, 1000], [7, 1, 30], 15, 3, d, page, d, True, order)
     wide = torch.zeros(P.N, 17, d, dtype=torch.bfloat16, device="cuda")
-    wide[:, 2:14] = q
-    check(call(P, wide[:, 2:14], tree, scale=0.2), *expected(P, q, tree, 0.2))
+    wide[:, 1:16] = q
+    check(call(P, wide[:, 1:16], tree, scale=0.2), *expected(P, q, tree, 0.2))
 
 
 @gpu
