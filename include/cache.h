@@ -81,7 +81,7 @@ int moe_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t 
  *                     that no position needs are not read
  *   page              a power of two, 8 .. 4096
  * n_pages >= 1, 1 <= n_sequences <= 65535, 1 <= n_kv_heads <= 1024, width >= 1, width * page
- * <= 2^28; no two places share an element, of K and of V neither
+ * <= 2^28
  */
 typedef struct moe_paged {
   uint16_t *k_pages, *v_pages;
@@ -108,8 +108,8 @@ typedef struct moe_paged {
  *            n_axes 1); else they are [n_axes][N], of token t
  * A token whose row is outside 0 .. n_rows - 1, whose position is past the table's width or
  * whose page is outside 0 .. n_pages - 1 is left out. Two tokens may not come to the same
- * place (sequences share no page that is written). Sizes, alignment and arithmetic as
- * above; strides of the cache multiples of 8 elements below 2^39, pages at a 16-byte
+ * place (sequences share no page that is written), and no two places, of K or V, share
+ * elements. Sizes, alignment and arithmetic as above; strides of the cache multiples of 8 elements below 2^39, pages at a 16-byte
  * aligned address; table, starts, lens and rows 4-byte aligned. One launch.
  */
 int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
