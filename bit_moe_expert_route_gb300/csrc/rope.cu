@@ -11,10 +11,11 @@
 // load 1, 2 or 4 whole heads. The weights go into the sines and cosines once a token. Loads of heads do not
 // wait for angles or places.
 //
-// Few tokens: one chain of load - sum - store, 2.5 us. 32768 tokens of 16 + 2 heads of 256: 112 us,
-// 79% of the measured copy; the same without arithmetic 96 us. About 160 instructions a head fill two
-// thirds of the issue slots. (Two loads a warp and 32 warps an SM; four and 24 warps 115 us, six 125. Warps
-// that go from token to token by themselves 119 to 128.)
+// Few tokens: one chain of load - sum - store, 2.2 us. 32768 tokens of 16 + 2 heads of 256: 109 us,
+// 82% of the measured copy; the same without arithmetic 96 us. About 160 instructions a head fill two
+// thirds of the issue slots. (Blocks of 128 threads; of 256, whose warps wait for each other's places and sines, 112
+// us. Warps that go from token to token by themselves 119 to 128.) Appending 32768 tokens of 2 heads of 256: 32 us,
+// 62% of the copy, blocks of 256 threads 36.
 //
 // Angles: a frequency is held as the part of a whole turn that one position makes, in
 // 64 bits with the point in front (freq / 2 pi mod 1); times the position, mod 2^64,
@@ -30,7 +31,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // freq / (2 pi) mod 1 in units of 2^-64. freq = M 2^(e - 150) with a 24-bit M;
 // M 2^40 * (2^64 / 2 pi) / 2^64 is freq / 2 pi in units of 2^(e - 126 - 64).
@@ -164,8 +165,11 @@ __device__ __noinline__ float small_squares(float2 a0, float2 a1, float2 b0, flo
   return s;
 }
 
+// Registers: 28 warps an SM without spills; of 32 and 24 the same 32768 tokens take 109.4 and 114 us, 4099 of 16 heads
+// of 128 8.8 and 7.7 instead of 8.5. With places 36, which spill a few registers once a token and hide more of the
+// chain (32768 appended tokens 32 us; 28 or 32 warps 34.8, 44 37. 301 accepted tokens 4.6 us, in blocks of 256 threads 4.0: the call takes 13.)
 template <int LPR, bool PAGED, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, PAGED ? 9 : 7) rope_kernel(const RopeParams p) {
   constexpr int RPW = 32 / LPR;  // heads a warp's load holds: a group
   constexpr int U = 2;           // groups at a time
   extern __shared__ float2 rope_smem[];  // [tokens][pairs]
@@ -374,9 +378,9 @@ cudaError_t rope_launch_t(RopeParams p, int sms, cudaStream_t s) {
   constexpr int RPW = 32 / LPR;
   const int groups = (p.part[0].heads + RPW - 1) / RPW + (p.part[1].heads + RPW - 1) / RPW;
   p.inv_d = 1.f / (float)p.d;
-  // Few tokens: a token's heads go to several warps, while those are at most the 24 an SM that
-  // run at once: 2, 4 or 8 of a block, or more blocks a token. Many: a warp takes several tokens
-  // where they have few heads, for at least two batches of loads.
+  // Few tokens: a token's heads go to several warps, while those are at most 24 an SM, fewer than
+  // run at once (32: 1003 tokens of 40 heads 7.3 us instead of 6.4): 2 or 4 of a block, or more blocks a
+  // token. Many: a warp takes several tokens where they have few heads, for at least two batches of loads.
   const int64_t room = std::min<int64_t>(groups, (int64_t)sms * 24 / p.T);
   p.split = 1;
   while (p.split < kRopeWarps && 2 * p.split <= room) p.split *= 2;
