@@ -300,3 +300,15 @@ def test_far_pages():
     assert torch.equal(got, want)
     del buf, kp, vp, far
     torch.cuda.empty_cache()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_shared_pages_and_one_pool(d):
+    """Sequences whose first pages are the same ones; a pool that is keys and values both."""
+    P, q, tree = paged([400, 170, 333], [5, 64, 1], 8, 2, d, 32, 9)
+    P.table[1:, :5] = P.table[0, :5]
+    P.cache.table.copy_(P.table)
+    check(call(P, q, tree), *expected(P, q, tree))
+    P.cache = P.cache._replace(v_pages=P.cache.k_pages)
+    check(call(P, q, tree), *expected(P, q, tree))
