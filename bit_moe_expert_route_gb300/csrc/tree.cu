@@ -744,6 +744,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       // the segment's outputs: every product is complete with the last one
       if (!(alive = alive && warp_wait_for(&pv_done[last], last_turn, abort_flag, p.status, 110))) break;
       tc_fence_after();
+      // (read before the arrival: once all warps have arrived, the next segment's scores run, and a warp that is ahead may
+      // set it for that one)
+      const bool odd_values = *v_bad == seg + 1;
       if (more) {
         cp_async_wait<0>();
         fence_proxy_async_smem();
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       }
       const int64_t state = ((int64_t)blockIdx.x * kTreeParts + part) * p.rows;  // of the tile's first row
       if (mine && !g.whole) p.part_ml[state + r] = make_float2(m, l);
-      if (warp_rows && !poison && *v_bad == seg + 1) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
+      if (warp_rows && !poison && odd_values) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
       // A quad of lanes holds 8 columns of a row at a time: stores are whole sectors of 8 rows. (A row a
       // lane: 16 bytes of each of 32 rows, 5 us for 128 rows of 256.)
       const float inv = l == 0.f ? 0.f : g.whole ? 1.f / l : 1.f;  // nothing attended to: zeros
