@@ -37,7 +37,8 @@
 // What rows do not attend to: scores are set to -infinity by the row's mask, whatever they
 // were. In V, a weight of 0 would still make NaN of an infinity or a NaN. Rows past the
 // sequence's end (a page's rest) are set to 0 in shared memory; so are infinite and NaN elements of the
-// new tokens' V, and rows that do attend to such a token have the element added at the end.
+// new tokens' V, and rows that do attend to such a token have the element added at the end. Cached positions, which
+// all rows attend to, are looked through for such elements where an output is not finite.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -205,6 +206,8 @@ __device__ __noinline__ void give_up(const TreeParams& p, const int64_t* found, 
     for (; parts < kTreeParts; ++parts) notes[parts].item = -1;
 }
 
+MOE_DEVINL bool not_finite2(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
+
 // Elements of new tokens' V that are not finite, for the rows that attend to them (a row a lane).
 template <int D, int KT>
 __device__ __noinline__ void add_not_finite(const TreeParams& p, const Segment& g, uint32_t tmem, uint64_t bits, bool mine) {
@@ -231,6 +234,63 @@ __device__ __noinline__ void add_not_finite(const TreeParams& p, const Segment& 
   tc_wait_st();
 }
 
+// Outputs where cached values are infinite or NaN. The weights' two parts make NaN of most of them (the second is as often
+// negative or 0 as not), so the columns are looked for in the segment's cached V, all of which every row attends
+// to, and set: an infinity where those of a column are of one sign, else NaN. Only where outputs are not finite: a warp reads
+// the segment's V once more (8 x 16 tokens over 32768 positions 630 us instead of 79).
+template <int D, int KT>
+__device__ __noinline__ void show_not_finite(const TreeParams& p, const Segment& g, uint32_t tmem) {
+  constexpr int kLanes = D / 8;  // of a position: 8 columns each
+  const int lane = threadIdx.x & 31;
+  const int64_t to = min((int64_t)g.k1 * KT, (int64_t)g.L);
+  const uint16_t* v = p.v_pages + g.h * p.head_stride + lane % kLanes * 8;
+  uint32_t signs = 0;  // of this lane's columns: + infinity, 8 bits on - infinity; NaN is both
+#pragma unroll 1
+  for (int64_t at0 = (int64_t)g.k0 * KT + lane / kLanes; at0 < to; at0 += 8 * (32 / kLanes)) {
+    int64_t at[8];
+    int id[8];
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at[i] = min(at0 + i * (32 / kLanes), to - 1);  // (the last one again past the end)
+      id[i] = p.table[g.b * p.ld_table + (at[i] >> p.page_log2)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = *reinterpret_cast<const uint4*>(v + id[i] * p.page_stride + (at[i] & ((1 << p.page_log2) - 1)) * p.position_stride);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!(not_finite2(x[i].x) || not_finite2(x[i].y) || not_finite2(x[i].z) || not_finite2(x[i].w))) continue;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t e = w[j / 2] >> (j & 1) * 16 & 0xFFFFu;
+        if ((e & 0x7FFFu) > 0x7F80u) signs |= 0x101u << j;
+        if (e == 0x7F80u) signs |= 1u << j;
+        if (e == 0xFF80u) signs |= 0x100u << j;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = kLanes; off < 32; off *= 2) signs |= __shfl_xor_sync(0xffffffffu, signs, off);
+  if (!__any_sync(0xffffffffu, signs != 0)) return;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    const uint32_t of[2] = {__shfl_sync(0xffffffffu, signs, c / 8), __shfl_sync(0xffffffffu, signs, c / 8 + 1)};
+    if ((of[0] | of[1]) == 0) continue;
+    uint32_t o[16];
+    tmem_ld_32x32b_x16(tmem + c, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t sign = of[j / 8] >> j % 8 & 0x101u;
+      if (sign) o[j] = sign == 1u ? 0x7F800000u : sign == 0x100u ? 0xFF800000u : 0x7FC00000u;
+    }
+    tmem_st_32x32b_x16(tmem + c, o);
+  }
+  tc_wait_st();
+}
+
 // Which of the 32 positions from the rel-th new token on (rel < 0: cached ones before) a
 // row with the mask `bits` attends to.
 MOE_DEVINL uint32_t attended(int64_t rel, uint64_t bits) {
@@ -238,8 +298,6 @@ MOE_DEVINL uint32_t attended(int64_t rel, uint64_t bits) {
   if (rel < 0) return (uint32_t)((bits << -rel) | ((1ull << -rel) - 1));
   return rel < 64 ? (uint32_t)(bits >> rel) : 0u;
 }
-
-MOE_DEVINL bool not_finite2(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 
 // The scores of a tile that rows do not attend to: -infinity.
 template <int KT>
@@ -768,14 +826,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       // lane: 16 bytes of each of 32 rows, 5 us for 128 rows of 256.)
       const float inv = l == 0.f ? 0.f : g.whole ? 1.f / l : 1.f;  // nothing attended to: zeros
       const int q = lane & 3;
+      bool looked = poison || g.L <= g.k0 * (int64_t)KT;  // for infinite cached values (there may be none)
 #pragma unroll 1
-      for (int half = 0; half < 32 && quarter * 32 + half < g.rows; half += 16) {
+      for (int half = 0; half < 32 && quarter * 32 + half < g.rows;) {
         float f[2];
+        float2 none[2];  // f, or NaN once outputs are not finite: 0 times those is NaN
         uint8_t* dst[2];  // of the two rows that this lane has parts of; null past the end
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int in = half + 8 * k + (lane >> 2), row = quarter * 32 + in;
           f[k] = __shfl_sync(0xffffffffu, inv, in);
+          none[k] = make_float2(f[k], f[k]);
           const int y = g.row0 + row, i = (int)(y * per_group >> 16);
           dst[k] = row >= g.rows ? nullptr
                    : g.whole ? reinterpret_cast<uint8_t*>(p.out + ((int64_t)(g.tok0 + i) * p.Hq + g.h * G + y - i * G) * D) + (8 * (q & 1) + 2 * (q & 2)) * 2
@@ -787,6 +848,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
           uint32_t o[16];
           tmem_ld_16x256b_x4(from + c, o);
           tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            none[j & 1] = __ffma2_rn(make_float2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), make_float2(0.f, 0.f), none[j & 1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float2 v[4];
@@ -808,6 +872,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
             }
           }
         }
+        bool odd = false;  // (rows of NaN need no looking for)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) odd |= f[k] == f[k] && !(none[k].x == f[k] && none[k].y == f[k]);
+        if (!looked && __any_sync(0xffffffffu, odd)) {
+          looked = true;
+          show_not_finite<D, KT>(p, g, tmem + lanes);
+          if (odd_values) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
+          continue;  // these rows once more
+        }
+        half += 16;
       }
       tc_fence_before();
     }

@@ -132,7 +132,10 @@ int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t 
  *          with a score that is NaN or +infinity, and for all rows of a sequence with more
  *          than 64 new tokens, with positions past the table's width, or with a page
  *          outside 0 .. n_pages - 1. What a position that a row does not attend to holds, infinities
- *          and NaN too, does not come into the row
+ *          and NaN too, does not come into the row. An infinite value of one that it does attend to
+ *          makes its element of the row that infinity, whatever the position's weight; infinities of both
+ *          signs, or a NaN, make it NaN. (Weights are below 2^10 until they are divided by their sum: sums
+ *          of them times finite values that pass the fp32 range are infinite or NaN too)
  *   ws     256-byte aligned, >= moe_tree_attention_workspace_bytes (no initialisation
  *          needed), holds the status word; where the status says MOE_DEV_TIMEOUT, the rows
  *          not computed are NaN
