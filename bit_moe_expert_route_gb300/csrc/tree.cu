@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       if (warp_rows && !poison && odd_values) add_not_finite<D, KT>(p, g, tmem + lanes, bits, mine);
       // A quad of lanes holds 8 columns of a row at a time: stores are whole sectors of 8 rows. (A row a
       // lane: 16 bytes of each of 32 rows, 5 us for 128 rows of 256.)
-      const float inv = l == 0.f ? 0.f : g.whole ? 1.f / l : 1.f;  // nothing attended to: zeros
+      // nothing attended to: zeros (a part's are, but for infinities, which the merge takes out)
+      const float inv = l != l ? l : !g.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const int q = lane & 3;
       bool looked = poison || g.L <= g.k0 * (int64_t)KT;  // for infinite cached values (there may be none)
 #pragma unroll 1
@@ -903,6 +904,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 // (Grids over all rows would mostly find nothing to do: 60 sequences of 59 tokens, 48000
 // rows in 480 items that no run cuts, 206 us instead of 33.)
 constexpr int kMergeWarps = 8;
+MOE_DEVINL float not_finite(float x) { return fabsf(x) < INFINITY ? 0.f : x; }
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeParams p) {
   constexpr int kC = D < 128 ? 1 : D / 128;  // float4 a lane (D = 64: half the lanes)
@@ -1010,7 +1012,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
       float4 v[4][kC];
       float f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // (a part in which the row attends to nothing has zeros)
+      for (int i = 0; i < 4; ++i) {  // (a part in which the row attends to nothing has zeros, or infinities)
         const int k = i0 + i * step;
         f[i] = 0.f;
         if (k >= n) continue;
@@ -1022,6 +1024,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i0 + i * step >= n) continue;
+        if (f[i] == 0.f) {  // what is infinite or NaN has no weight
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            v[i][c] = make_float4(not_finite(v[i][c].x), not_finite(v[i][c].y), not_finite(v[i][c].z), not_finite(v[i][c].w));
+          f[i] = 1.f;
+        }
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
           acc[c].x = fmaf(f[i], v[i][c].x, acc[c].x);
@@ -1049,12 +1057,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
         }
     }
     if (!in) continue;
-    const float inv = mass == 0.f ? 0.f : 1.f / mass;  // nothing attended to: zeros
+    const float inv = 1.f / mass;
     const int x = (first.what >> 12 & 15) * kTreeRows + r;
     uint16_t* out = p.out + ((int64_t)(first.tok0 + x / G) * p.Hq + (first.what >> 16) * G + x % G) * D + lane * 4;
 #pragma unroll
     for (int c = 0; c < kC; ++c)
       *reinterpret_cast<uint2*>(out + c * 128) =
+          mass == 0.f ? make_uint2(0, 0) :  // nothing attended to
           make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
   }
 }

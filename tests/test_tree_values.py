@@ -81,3 +81,30 @@ def test_infinite_values_of_cached_positions(lens, news, Hq, Hkv, page, tree, d)
     got = call(P, q, tree)
     check_odd(got, *odd_expected(P, q, tree))
     assert torch.equal(call(P, q, tree).view(torch.int16), got.view(torch.int16))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("below", ["far", "infinitely"])
+@pytest.mark.parametrize("L", [90, 30000])
+def test_infinite_values_of_positions_without_weight(L, below, d):
+    """Positions whose weights are 0 in fp32, or exactly (scores of -infinity), in a block of their own or in one with the
+    largest score: what is infinite there shows all the same. A row of nothing but -infinity is zeros."""
+    P, q, tree = paged([L, 40], [5, 9], 8, 2, d, 16, d)
+    q[..., 0] = 1.0
+    for b, last in ((0, L), (1, 40)):
+        to = P.places(b, range(last))
+        P.cache.k_pages[to[0], to[1], :, 0] = 0.0
+    if below == "far":
+        to = P.places(0, range(10))
+        P.cache.k_pages[to[0], to[1], :, 0] = 300.0 * d ** 0.5   # 300 above the rest: e^-300
+    else:
+        to = P.places(0, range(10, L + 5))
+        P.cache.k_pages[to[0], to[1], :, 0] = float("-inf")
+    for at, column in ((L - 7, 3), (L // 2 + 20, 4), (L, 5), (L + 4, 6)):
+        to = tuple(int(x) for x in P.places(0, [at]))
+        P.cache.v_pages[to][:, column] = float("inf")
+    got = call(P, q, tree)
+    check_odd(got, *odd_expected(P, q, tree))
+    to = P.places(0, range(L + 5))
+    P.cache.k_pages[to[0], to[1], :, 0] = float("-inf")
+    assert not call(P, q, tree)[:5].any()
