@@ -19,8 +19,8 @@
 //
 // Angles: a frequency is held as the part of a whole turn that one position makes, in
 // 64 bits with the point in front (freq / 2 pi mod 1); times the position, mod 2^64,
-// it is the part of a turn that is left, whole turns gone, to 2^-31 of a turn at any
-// 32-bit position (for frequencies up to 1). The top 32 bits go to sincospi. (In fp32 position * freq alone is
+// it is the part of a turn that is left, whole turns gone, to 2^-33 of a turn at any
+// 32-bit position. The top 32 bits go to sincospi. (In fp32 position * freq alone is
 // 0.06 radians off at a million; in FP64, a 64th of the fp32 rate here, the angles of a
 // token would take longer than its heads.)
 #include <algorithm>
@@ -33,8 +33,9 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 
-// freq / (2 pi) mod 1 in units of 2^-64. freq = M 2^(e - 150) with a 24-bit M;
-// M 2^40 * (2^64 / 2 pi) / 2^64 is freq / 2 pi in units of 2^(e - 126 - 64).
+// freq / (2 pi) mod 1 in units of 2^-64, cut off below them, for |freq| < 2^16. freq = M 2^(e - 150) with a 24-bit M, and
+// the product of M and 2^128 / (2 pi), times 2^(e - 214), is that. (128 bits: of 64, the places that a frequency of
+// 2^15 shifts in would be missing, 2^-14 radians at position 2^31.)
 MOE_DEVINL uint64_t turns_per_position(float freq) {
   const uint32_t u = __float_as_uint(freq);
   int e = (int)((u >> 23) & 255u);
@@ -43,10 +44,11 @@ MOE_DEVINL uint64_t turns_per_position(float freq) {
     e = 1;  // subnormal
   else
     m |= 0x800000u;
-  const uint64_t kInv2Pi = 2935890503282001226ull;  // round(2^64 / (2 pi))
-  const uint64_t f = __umul64hi((uint64_t)m << 40, kInv2Pi);
-  const int shift = e - 126;
-  const uint64_t r = shift >= 0 ? (shift < 64 ? f << shift : 0) : (shift > -64 ? f >> -shift : 0);
+  const uint64_t kHigh = 2935890503282001226ull, kLow = 9154082963658192752ull;  // round(2^128 / (2 pi))
+  const uint64_t carried = __umul64hi((uint64_t)m, kLow), low = m * kHigh + carried;
+  const uint64_t high = __umul64hi((uint64_t)m, kHigh) + (low < carried);
+  const int shift = max(1, 150 - e);  // of (high, low), the product's bits from the 64th on
+  const uint64_t r = shift < 64 ? low >> shift | high << (64 - shift) : shift < 128 ? high >> (shift - 64) : 0;
   return (u >> 31) ? 0 - r : r;
 }
 
@@ -145,7 +147,7 @@ MOE_DEVINL float2 turn_of(const RopeParams& p, int t, int pair, float freq, uint
   const int32_t left = (int32_t)(uint32_t)((turn + 0x80000000ull) >> 32);  // of a turn, in 2^-32
   float2 cs;
   sincospif((float)left * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31
-  const float bad = freq - freq;  // NaN for a frequency that is not finite
+  const float bad = fabsf(freq) < 65536.f ? 0.f : __int_as_float(0x7fc00000);  // a frequency too large or not finite
   return make_float2(cs.x + bad, cs.y + bad);
 }
 

@@ -29,7 +29,7 @@ extern "C" {
  * (a, b) being elements (i, i + pairs), or, where `adjacent` is set, (2i, 2i + 1);
  * elements from 2 pairs on stay. Angles are reduced in whole numbers, so that
  * cos and sin are exact to fp32 (2^-22) at every int32 position.
- *   freqs         fp32 [pairs] device, finite and below 2^16 in magnitude
+ *   freqs         fp32 [pairs] device, below 2^16 in magnitude (any other makes its pair NaN)
  *   positions     int32 [n_axes][tokens] device, axes ld_positions elements apart (0: all
  *                 axes have the same)
  *   pairs         0 (no rotation) .. d / 2; a multiple of 8, of 4 if adjacent
