@@ -23,7 +23,7 @@ bool stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s 
 int enter_rope(moe::RopeParams& p, const moe_rope_t* rope, int tokens, bool placed) {
   if (!rope || rope->pairs == 0) return MOE_OK;
   const moe_rope_t& r = *rope;
-  if (r.pairs < 0 || 2 * r.pairs > p.d || r.pairs % (r.adjacent ? 4 : 8) != 0) return MOE_ERR_SHAPE;
+  if (r.pairs < 0 || r.pairs > p.d / 2 || r.pairs % (r.adjacent ? 4 : 8) != 0) return MOE_ERR_SHAPE;
   if (r.n_axes < 1 || r.n_axes > MOE_ROPE_MAX_AXES) return MOE_ERR_SHAPE;
   int64_t sum = 0;
   for (int a = 0; a < r.n_axes; ++a) {
