@@ -613,6 +613,9 @@ _ROPE_ARGS = struct.Struct("@PPq8i")
 _PAGED_ARGS = struct.Struct("@PP3qPq6i")
 
 
+_MOST = 0x7fffffff  # what the C calls' sizes hold: ctypes would wrap larger ones
+
+
 def rope_freqs(rotary: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
     """Frequencies theta^(-2i / rotary), i < rotary / 2, as Rope takes them (rounded to fp32 once)."""
     i = torch.arange(0, rotary, 2, dtype=torch.float64)
@@ -649,6 +652,8 @@ def _heads(fn, name, t, T, H, d, dev):
     shape = (T, H, d)
     if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or dev < 0:
         _refuse(fn, name, t, torch.bfloat16, shape, dev)
+    if T > _MOST or H > _MOST or d > _MOST:
+        raise ValueError(f"{fn}: {name} {tuple(shape)} is too large")
     s0, s1, s2 = t.stride()
     if (s2 != 1 or s1 != d and H > 1) and T:
         raise ValueError(f"{fn}: {name} has scattered heads")
@@ -661,6 +666,8 @@ def _vector(fn, name, t, dtype, n, dev):
         return None
     if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
         _refuse(fn, name, t, dtype, (n,), dev)
+    if n > _MOST:
+        raise ValueError(f"{fn}: {name} of {n} elements is too large")
     return t.data_ptr()
 
 
@@ -721,7 +728,7 @@ def _paged_args(fn, cache, Hkv, d, dev):
         raise ValueError(f"{fn}: k_pages and v_pages have different strides or scattered elements")
     pt, ld = _rows(fn, "table", table, size, dev)
     B, width = size
-    if max(n, page, width, B) > 0x7fffffff:
+    if max(n, page, width, B) > _MOST:
         raise ValueError(f"{fn}: a cache of {n} pages and {B} x {width} entries is too large")
     return _PAGED_ARGS.pack(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], pt, ld, n, page, width, B, Hkv, d), B
 
