@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? 9 : 7) rope_kernel(const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  // Up to 8 warps a token: a block has 8 / split tokens at a time, `tokens` in all. More: a block
+  // Up to 4 warps (a block's) a token: a block has 4 / split tokens at a time, `tokens` in all. More: a block
   // has one token, of which it is the (blockIdx % token_blocks)-th.
   const int64_t t0 = (int64_t)(blockIdx.x / p.token_blocks) * p.tokens;
   const int n_tokens = (int)min((int64_t)p.tokens, p.T - t0);

@@ -66,7 +66,8 @@ int moe_decode_attention(const uint16_t* q, const uint16_t* K, const uint16_t* V
  *   out                 bf16 [B][n_q_heads][d]; zeros for a sequence without any
  *                       position (P == 0 and len[b] == 0), and for a row whose
  *                       every score is -infinity; NaN for a row with a score that
- *                       is NaN or +infinity
+ *                       is NaN or +infinity. An infinite value may make its
+ *                       element NaN (a weight's second part may be 0 or negative)
  *   ws                  256-byte aligned, >= moe_prefix_attention_workspace_bytes
  *                       (no initialisation needed), holds the status word.
  *                       May be NULL where little work takes one launch (then

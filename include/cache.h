@@ -107,7 +107,7 @@ typedef struct moe_paged {
  *   rope     its positions may be NULL: a token turns by its position in the cache (with
  *            n_axes 1); else they are [n_axes][N], of token t
  * A token whose row is outside 0 .. n_rows - 1, whose position is past the table's width or
- * whose page is outside 0 .. n_pages - 1 is left out. Two tokens may not come to the same
+ * whose page is outside 0 .. n_pages - 1 is left out. k and v share no memory with the pages. Two tokens may not come to the same
  * place (sequences share no page that is written), and no two places, of K or V, share
  * elements. Sizes, alignment and arithmetic as above; strides of the cache multiples of 8 elements below 2^39, pages at a 16-byte
  * aligned address; table, starts, lens and rows 4-byte aligned. One launch.
@@ -134,7 +134,7 @@ int moe_append_paged(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t 
  *          outside 0 .. n_pages - 1. What a position that a row does not attend to holds, infinities
  *          and NaN too, does not come into the row. An infinite value of one that it does attend to
  *          makes its element of the row that infinity, whatever the position's weight; infinities of both
- *          signs, or a NaN, make it NaN. (Weights are below 2^10 until they are divided by their sum: sums
+ *          signs, or a NaN, make it NaN. (Weights are up to 2^10 until they are divided by their sum: sums
  *          of them times finite values that pass the fp32 range are infinite or NaN too)
  *   ws     256-byte aligned, >= moe_tree_attention_workspace_bytes (no initialisation
  *          needed), holds the status word; where the status says MOE_DEV_TIMEOUT, the rows
